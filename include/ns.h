@@ -260,6 +260,205 @@ ns_status ns_muon_workspace_size(const ns_muon_matrix* mats, int count,
 ns_status ns_muon_step(const ns_muon_matrix* mats, int count, const ns_params* params,
                        float beta, float lr, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the matrix update of a training step: the parameters that
+ * are not matrices of the Newton-Schulz update (token embeddings, norm
+ * gains) forward, backward and their optimizer step, and a loss on logits.
+ *
+ * The conventions at the top of this file hold (ownership, streams, graphs,
+ * errors, device, determinism), with these differences: no call uploads a
+ * table or copies from the host, a workspace is needed only where an argument
+ * says so, and every pointer must be aligned to its element type only (rows
+ * of any leading dimension and width take the same vector path). Element
+ * types are fp32, bf16 and fp16 throughout unless a call says otherwise;
+ * arithmetic, statistics and sums are fp32 or wider and each output is
+ * rounded once, to nearest even. Offsets are 64-bit. An output that overlaps
+ * an input, another output or the workspace is refused (NS_ERR_INVALID_ARG)
+ * except where a call allows it.
+ * ---------------------------------------------------------------------- */
+
+/* One more element type, accepted only where a call names it: 8 bits, 4 of
+ * exponent and 3 of mantissa, no infinities, largest value 448 (OCP e4m3). */
+#define NS_DT_E4M3 3
+
+/* Token ids and labels: a dense host-unchecked device array of int32 or
+ * int64 (ids outside the range a call names are handled by the kernels). */
+typedef enum { NS_IDS_I32 = 0, NS_IDS_I64 = 1 } ns_id_type;
+
+/* Largest number of table rows or vocabulary entries, and of ids or rows of
+ * one call. */
+#define NS_MAX_ROWS (1 << 23)
+
+/* Embedding lookup with scaling: out[i] = scale * table[ids[i]], i < count.
+ * An id outside [0, rows) gives a row of zeros (a table that holds one
+ * shard of a vocabulary is looked up with ids less its first row, and the
+ * shards' outputs are summed).
+ *   table   (rows, dim), ld_table >= dim;   out   (count, dim), ld_out >= dim.
+ * 1 <= rows <= NS_MAX_ROWS, 1 <= dim <= NS_MAX_DIM, 0 <= count <=
+ * NS_MAX_ROWS (0 is a no-op); scale finite. */
+ns_status ns_embedding(const void* table, ns_dtype table_dtype, int64_t rows, int64_t dim,
+                       int64_t ld_table, const void* ids, ns_id_type id_type, int64_t count,
+                       float scale, void* out, ns_dtype out_dtype, int64_t ld_out,
+                       void* stream);
+
+/* Gradient of ns_embedding with respect to the table:
+ *   grad[v] = scale * sum of grad_out[i] over the i with ids[i] == v,
+ * every row of grad written (zeros where no id names it), or, with
+ * accumulate != 0, that sum added to grad (rows that no id names are not
+ * touched). ids outside [0, rows) and ids equal to padding_id (any negative
+ * value: none) contribute nothing.
+ *   grad_out  (count, dim), ld_grad_out >= dim;  grad  (rows, dim), ld_grad >= dim.
+ * The ids are sorted on the device and each row's terms are added in a fixed
+ * order that depends on the ids alone, so results are reproducible.
+ * Workspace: ns_embedding_grad_workspace_size bytes, 256-byte aligned.
+ * Limits as for ns_embedding; count == 0 writes zeros (or, accumulating,
+ * nothing). */
+ns_status ns_embedding_grad_workspace_size(int64_t rows, int64_t dim, int64_t count,
+                                           size_t* bytes);
+ns_status ns_embedding_grad(const void* grad_out, ns_dtype grad_out_dtype, int64_t ld_grad_out,
+                            const void* ids, ns_id_type id_type, int64_t count, int64_t rows,
+                            int64_t dim, float scale, int64_t padding_id, int accumulate,
+                            void* grad, ns_dtype grad_dtype, int64_t ld_grad, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Root-mean-square norm of each row, with the residual's addition:
+ *   h = x + residual               (rounded to h's type; h = x if no residual)
+ *   rstd = 1 / sqrt(mean(h^2) + eps)            (of the rounded h)
+ *   y = h * rstd * weight
+ * or, with y_dtype NS_DT_E4M3, the codes and one scale for each row:
+ *   scale = max |y| / 448 (1 where that maximum is 0),  code = e4m3(y / scale).
+ * A scale below 2^-126 is raised to that. A NaN in a row of h makes every y
+ * of it NaN; a code stands for NaN where y is NaN, and a NaN does not enter
+ * the maximum.
+ *   x         (rows, dim), ldx >= dim;
+ *   residual  (rows, dim) of type h_dtype, or NULL;
+ *   h         (rows, dim) of type h_dtype, written when residual is given
+ *             (may be the residual's own buffer, or x's where the types
+ *             agree, with the same leading dimension); NULL without one;
+ *   h_dtype   the type of residual and h: x's or fp32 (x's, if no residual);
+ *   weight    (dim), fp32 or x's type;
+ *   y         (rows, dim), ldy >= dim;
+ *   scales    (rows) fp32 for NS_DT_E4M3, else NULL;
+ *   rstd      (rows) fp32, or NULL.
+ * 0 <= rows <= NS_MAX_ROWS (0 is a no-op), 1 <= dim <= NS_MAX_DIM; eps
+ * finite and >= 0. */
+typedef struct {
+  const void* x;
+  const void* residual;
+  void* h;
+  const void* weight;
+  void* y;
+  float* scales;
+  float* rstd;
+  int64_t rows, dim, ldx, ld_residual, ldh, ldy;
+  ns_dtype x_dtype, h_dtype, weight_dtype;
+  int y_dtype;                   /* an ns_dtype or NS_DT_E4M3 */
+  float eps;
+} ns_rms_norm_args;
+ns_status ns_rms_norm(const ns_rms_norm_args* args, void* stream);
+
+/* Gradient of ns_rms_norm (8-bit output included, its rounding taken as the
+ * identity). With u = h * rstd and g = dy * weight:
+ *   dx = rstd * (g - u * mean(g * u)) + dh
+ *   dweight = sum over the rows of dy * u
+ * dx is the gradient of x and of the residual alike.
+ *   dy       (rows, dim), lddy >= dim, any type;
+ *   h        (rows, dim), ldh >= dim: the h that ns_rms_norm normalised (x,
+ *            if it had no residual), with its rstd (rows);
+ *   dh       (rows, dim) of type dx_dtype: the gradient that reaches h past
+ *            the norm, or NULL;
+ *   dx       (rows, dim), lddx >= dim: dy's type or fp32; may be dh's own
+ *            buffer with the same leading dimension;
+ *   dweight  (dim), any type, written (zeros if rows == 0), or NULL.
+ * dweight is summed in a fixed order. Workspace:
+ * ns_rms_norm_grad_workspace_size bytes, 256-byte aligned. h has dy's type
+ * or fp32; weight fp32 or dy's type. */
+typedef struct {
+  const void* dy;
+  const void* h;
+  const void* weight;
+  const float* rstd;
+  const void* dh;
+  void* dx;
+  void* dweight;
+  int64_t rows, dim, lddy, ldh, lddh, lddx;
+  ns_dtype dy_dtype, h_dtype, weight_dtype, dx_dtype, dweight_dtype;
+} ns_rms_norm_grad_args;
+ns_status ns_rms_norm_grad_workspace_size(int64_t rows, int64_t dim, size_t* bytes);
+ns_status ns_rms_norm_grad(const ns_rms_norm_grad_args* args, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* Preference loss on paired sequences. Sequence s < pairs is the preferred
+ * one of pair s, sequence pairs + s the other; z is the policy's logits:
+ *   logp_s = sum over the counted positions t of z[s][t][label] - lse[s][t]
+ *   lse[s][t] = log sum_v exp z[s][t][v]
+ *   margin_p = beta * ((logp_p - ref_p) - (logp_{pairs+p} - ref_{pairs+p}))
+ *   loss_p = -(1 - label_smoothing) log sigmoid(margin_p)
+ *            - label_smoothing log sigmoid(-margin_p)
+ * A position counts if its label lies in [0, vocab); logits of other
+ * positions are not read, and their lse is 0. Sums over a sequence are
+ * taken in 64 bits.
+ *   logits   (2 * pairs * length, vocab): row s * length + t, ld >= vocab;
+ *   labels   (2 * pairs, length) dense;   ref_logps  (2 * pairs) fp32;
+ *   losses, margins  (pairs) fp32;  logps  (2 * pairs) fp32;
+ *   lse      (2 * pairs * length) fp32.
+ * The gradient call takes margins and lse of the forward call and the
+ * gradient of each loss, dlosses (pairs) fp32, and writes every element of
+ *   dlogits[s][t][v] = k_s * ([v == label] - exp(z - lse))   (0 if not counted)
+ *   k_p = dloss_p * beta * (label_smoothing * sigmoid(margin_p)
+ *                           - (1 - label_smoothing) * sigmoid(-margin_p)),
+ *   k_{pairs+p} = -k_p
+ * of logits' type, ld_dlogits >= vocab; dlogits may be the logits' own
+ * buffer with the same leading dimension. length >= 0 (0: empty sequences,
+ * losses of the reference alone), pairs >= 0 (0 is a no-op), 2 * pairs *
+ * length <= NS_MAX_ROWS, 1 <= vocab <= NS_MAX_ROWS; beta finite,
+ * 0 <= label_smoothing <= 1. Workspace of the forward call:
+ * ns_preference_loss_workspace_size bytes, 256-byte aligned. */
+typedef struct {
+  const void* logits;
+  const void* labels;
+  int64_t pairs, length, vocab, ld;
+  ns_dtype dtype;
+  ns_id_type label_type;
+  float beta, label_smoothing;
+} ns_preference_args;
+ns_status ns_preference_loss_workspace_size(int64_t pairs, int64_t length, int64_t vocab,
+                                            size_t* bytes);
+ns_status ns_preference_loss(const ns_preference_args* args, const float* ref_logps,
+                             float* losses, float* margins, float* logps, float* lse, void* ws,
+                             size_t ws_bytes, void* stream);
+ns_status ns_preference_loss_grad(const ns_preference_args* args, const float* margins,
+                                  const float* lse, const float* dlosses, void* dlogits,
+                                  int64_t ld_dlogits, void* stream);
+
+/* AdamW step of `count` tensors, in place, one launch for up to 32 of them:
+ *   m <- beta1 m + (1 - beta1) g
+ *   v <- beta2 v + (1 - beta2) g^2
+ *   w <- w - lr (weight_decay w + (m / (1 - beta1^step))
+ *                                 / (sqrt(v / (1 - beta2^step)) + eps))
+ * The update uses m and v before they are rounded to their storage types. w
+ * is `master` (fp32) where that is given, and param then receives w rounded
+ * to its type (param is not read); otherwise w is param.
+ *   Each buffer is dense with `elems` elements (0 is allowed); param, grad,
+ *   exp_avg any type, exp_avg_sq fp32 or bf16 (fp16 cannot hold the square
+ *   of a small gradient and is refused), master fp32 or NULL. Buffers of
+ *   different tensors must not overlap either (the caller's to avoid).
+ * step >= 1; 0 <= beta1, beta2 < 1; lr, eps, weight_decay finite and >= 0.
+ * The bias corrections are computed on the host in 64 bits: a captured call
+ * replays the step it was captured with. */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* master;
+  int64_t elems;
+  ns_dtype param_dtype, grad_dtype, exp_avg_dtype, exp_avg_sq_dtype;
+  float weight_decay;
+} ns_adamw_tensor;
+ns_status ns_adamw_step(const ns_adamw_tensor* tensors, int count, int64_t step, double lr,
+                        double beta1, double beta2, double eps, void* stream);
+
 /* Building blocks of the iteration, exposed for kernel-level testing.
  * All operands are fp16 row-major device matrices; products accumulate in
  * fp32 and the scaled sum is rounded once to fp16.

@@ -8,7 +8,8 @@ not built, importing works but every call raises.
 Names follow the C ABI: ``ns_normalize``, ``ns_gram``, ``ns_direct``,
 ``ns_batched``, ``ns_workspace_size``, plus the building blocks ``ns_syrk``
 and ``ns_gemm_nt`` and the diagnostics ``ns_backend_info`` /
-``ns_status_string``.
+``ns_status_string``. The operators around the matrix update (embedding, RMS
+norm, preference loss, AdamW) are in ``operators`` and exported here.
 
 The coefficient tables are the two 5-step sets of the DMuon page
 "Newton-Schulz 变体", section "系数集" (coefficient sets), as printed there;
@@ -156,6 +157,7 @@ def library() -> ctypes.CDLL:
             "ns_plan_check": [ctypes.c_int, vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, P,
                               vp, sz, ctypes.c_int, ctypes.c_char_p, sz],
         }
+        sigs.update(operators.SIGNATURES)
         for name, args in sigs.items():
             f = getattr(lib, name)
             f.argtypes = args
@@ -652,3 +654,7 @@ class NewtonSchulz:
     def __repr__(self):
         return (f"NewtonSchulz(backend={self.backend!r}, kernel={self.kernel!r}, "
                 f"steps={len(self.coefficients)}, restarts={self.restart_iterations})")
+
+
+from . import operators  # noqa: E402  (needs the names above)
+from .operators import *  # noqa: E402,F401,F403

@@ -18,7 +18,9 @@ SRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libnsmi.so")
-SOURCES = ["ns_api.hip", "norm_kernels.hip", "gemm_kernels.hip"]
+SOURCES = ["ns_api.hip", "norm_kernels.hip", "gemm_kernels.hip",
+           "train_api.hip", "train_embedding.hip", "train_rms_norm.hip",
+           "train_preference.hip", "train_adamw.hip"]
 ARCH = "gfx950"
 
 COMPILE_FLAGS = [

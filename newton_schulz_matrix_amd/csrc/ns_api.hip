@@ -21,6 +21,7 @@
 
 #include "../../include/ns.h"
 #include "ns_internal.h"
+#include "train_internal.h"
 
 #define NS_API extern "C" __attribute__((visibility("default")))
 
@@ -1325,6 +1326,15 @@ ns_status run_batched(const ns_matrix* mats, int count, ns_backend be, const ns_
 std::string g_info;
 
 }  // namespace
+
+ns_status device_status() noexcept {
+  try {
+    return check_device();
+  } catch (...) {   // the device table could not grow
+    return NS_ERR_HIP;
+  }
+}
+
 }  // namespace nsmi
 
 using namespace nsmi;

@@ -1,0 +1,403 @@
+"""Operators around the matrix update of a training step (see include/ns.h).
+
+``ns_embedding`` and its gradient, ``ns_rms_norm`` / ``ns_rms_norm_fp8`` and
+their gradient, the preference loss on logits and its gradient, and the AdamW
+step of the parameters that the Newton-Schulz update does not take. Argument
+marshalling only, like the rest of the package, which exports every name of
+this module: tensors become pointers, outputs and workspaces come from torch,
+work goes to the current stream of the tensors' device. There is no autograd
+wrapper: a backward pass calls the gradient functions.
+
+Tensors of rows may have any number of leading dimensions, as long as those
+collapse into one without a copy (a slice of the columns, or every k-th row,
+of a larger tensor is fine; a transposed view is refused).
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import List, Optional, Sequence, Tuple
+
+from . import (NS_DT_BF16, NS_DT_F16, NS_DT_F32, _check, _device_tensor, _dtype_code,
+               _stream_ptr, _torch, _workspace, library)
+
+NS_DT_E4M3 = 3
+NS_IDS_I32, NS_IDS_I64 = 0, 1
+NS_MAX_ROWS = 1 << 23
+
+_i64, _vp, _f32, _f64, _int = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_double,
+                               ctypes.c_int)
+_size = ctypes.c_size_t
+
+
+class _RmsNormArgs(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("x", "residual", "h", "weight", "y", "scales", "rstd")]
+                + [(n, _i64) for n in ("rows", "dim", "ldx", "ld_residual", "ldh", "ldy")]
+                + [(n, _int) for n in ("x_dtype", "h_dtype", "weight_dtype", "y_dtype")]
+                + [("eps", _f32)])
+
+
+class _RmsNormGradArgs(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("dy", "h", "weight", "rstd", "dh", "dx", "dweight")]
+                + [(n, _i64) for n in ("rows", "dim", "lddy", "ldh", "lddh", "lddx")]
+                + [(n, _int) for n in ("dy_dtype", "h_dtype", "weight_dtype", "dx_dtype",
+                                       "dweight_dtype")])
+
+
+class _PreferenceArgs(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("labels", _vp), ("pairs", _i64), ("length", _i64),
+                ("vocab", _i64), ("ld", _i64), ("dtype", _int), ("label_type", _int),
+                ("beta", _f32), ("label_smoothing", _f32)]
+
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "master")]
+                + [("elems", _i64)]
+                + [(n, _int) for n in ("param_dtype", "grad_dtype", "exp_avg_dtype",
+                                       "exp_avg_sq_dtype")]
+                + [("weight_decay", _f32)])
+
+
+SIGNATURES = {
+    "ns_embedding": [_vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _f32, _vp, _int, _i64, _vp],
+    "ns_embedding_grad_workspace_size": [_i64, _i64, _i64, ctypes.POINTER(_size)],
+    "ns_embedding_grad": [_vp, _int, _i64, _vp, _int, _i64, _i64, _i64, _f32, _i64, _int, _vp,
+                          _int, _i64, _vp, _size, _vp],
+    "ns_rms_norm": [ctypes.POINTER(_RmsNormArgs), _vp],
+    "ns_rms_norm_grad_workspace_size": [_i64, _i64, ctypes.POINTER(_size)],
+    "ns_rms_norm_grad": [ctypes.POINTER(_RmsNormGradArgs), _vp, _size, _vp],
+    "ns_preference_loss_workspace_size": [_i64, _i64, _i64, ctypes.POINTER(_size)],
+    "ns_preference_loss": [ctypes.POINTER(_PreferenceArgs), _vp, _vp, _vp, _vp, _vp, _vp, _size,
+                           _vp],
+    "ns_preference_loss_grad": [ctypes.POINTER(_PreferenceArgs), _vp, _vp, _vp, _vp, _i64, _vp],
+    "ns_adamw_step": [ctypes.POINTER(_AdamwTensor), _int, _i64, _f64, _f64, _f64, _f64, _vp],
+}
+
+
+def _ids_type(t, name: str) -> int:
+    torch = _torch()
+    if t.dtype == torch.int64:
+        return NS_IDS_I64
+    if t.dtype == torch.int32:
+        return NS_IDS_I32
+    raise TypeError(f"{name} must be int32 or int64, not {t.dtype}")
+
+
+def _rows_of(t, name: str) -> Tuple[int, int, int]:
+    """(rows, columns, leading dimension) of a tensor of rows on the current device."""
+    _device_tensor(t, name)
+    shape = t.shape
+    if len(shape) == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    cols = shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // cols if cols else 0), cols, cols
+    stride = t.stride()
+    if cols > 1 and stride[-1] != 1:
+        raise ValueError(f"{name}: rows must be contiguous (stride(-1) == 1)")
+    rows, ld = 1, None
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 0:
+            return 0, cols, max(cols, 1)
+        if n == 1:
+            continue
+        if ld is None:
+            ld = s
+        elif s != ld * rows:
+            raise ValueError(f"{name}: the dimensions before the last do not collapse into rows of "
+                             f"one stride (shape {tuple(shape)}, strides {tuple(stride)})")
+        rows *= n
+    if ld is None:
+        ld = cols
+    if ld < cols:
+        raise ValueError(f"{name}: row stride {ld} is smaller than the row length {cols} "
+                         f"(overlapping rows, e.g. an expanded view)")
+    return rows, cols, ld
+
+
+def _like_rows(t, shape, name: str, dtype=None) -> int:
+    """Leading dimension of a tensor that must have this shape (and type)."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return _rows_of(t, name)[2]
+
+
+def _dense(t, shape, name: str, dtype=None) -> int:
+    """Pointer of a dense tensor that must have this shape (and type)."""
+    _device_tensor(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _sized(name: str, *args) -> int:
+    nbytes = _size(0)
+    _check(getattr(library(), name)(*args, ctypes.byref(nbytes)), name)
+    return nbytes.value
+
+
+def _given_or_new(workspace, nbytes: int, device):
+    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+        return _workspace(nbytes, device)
+    return _device_tensor(workspace, "workspace")
+
+
+# ------------------------------------------------------------------ embedding
+
+def ns_embedding(table, ids, scale: float = 1.0, out_dtype=None, out=None):
+    """scale * table[ids], for ids (int32 or int64) of any shape; an id outside
+    the table gives zeros. Returns a tensor of shape ids.shape + (dim,)."""
+    torch = _torch()
+    if table.dim() != 2:
+        raise ValueError("table must be 2-D")
+    rows, dim, ld = _rows_of(table, "table")
+    id_type = _ids_type(_device_tensor(ids, "ids"), "ids")
+    ids = ids if ids.is_contiguous() else ids.contiguous()
+    shape = (*ids.shape, dim)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or table.dtype, device=table.device)
+        ld_out = dim
+    else:
+        ld_out = _like_rows(out, shape, "out", out_dtype)
+    _check(library().ns_embedding(table.data_ptr(), _dtype_code(table.dtype), rows, dim, ld,
+                                  ids.data_ptr(), id_type, ids.numel(), scale, out.data_ptr(),
+                                  _dtype_code(out.dtype), ld_out, _stream_ptr(table)),
+           "ns_embedding")
+    return out
+
+
+def ns_embedding_grad_workspace_size(rows: int, dim: int, count: int) -> int:
+    return _sized("ns_embedding_grad_workspace_size", rows, dim, count)
+
+
+def ns_embedding_grad(grad_out, ids, rows: int, scale: float = 1.0,
+                      padding_idx: Optional[int] = None, out_dtype=None, out=None,
+                      accumulate: bool = False, workspace=None):
+    """Gradient of ns_embedding's table (rows, dim): scale times the sum of
+    grad_out over the places that name each row. With accumulate it is added
+    to out, which must then be given. ids outside the table and padding_idx
+    contribute nothing."""
+    torch = _torch()
+    count, dim, ld = _rows_of(grad_out, "grad_out")
+    id_type = _ids_type(_device_tensor(ids, "ids"), "ids")
+    if tuple(ids.shape) != tuple(grad_out.shape[:-1]):
+        raise ValueError(f"ids have shape {tuple(ids.shape)}, grad_out {tuple(grad_out.shape)}")
+    if padding_idx is not None and not 0 <= padding_idx < rows:
+        raise ValueError(f"padding_idx {padding_idx} is not a row of the table (0 to {rows - 1})")
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to out: give it")
+    ids = ids if ids.is_contiguous() else ids.contiguous()
+    if out is None:
+        out = torch.empty((rows, dim), dtype=out_dtype or grad_out.dtype, device=grad_out.device)
+        ld_out = dim
+    else:
+        ld_out = _like_rows(out, (rows, dim), "out", out_dtype)
+    workspace = _given_or_new(workspace, ns_embedding_grad_workspace_size(rows, dim, count),
+                              grad_out.device)
+    _check(library().ns_embedding_grad(
+        grad_out.data_ptr(), _dtype_code(grad_out.dtype), ld, ids.data_ptr(), id_type, count, rows,
+        dim, scale, -1 if padding_idx is None else padding_idx, 1 if accumulate else 0,
+        out.data_ptr(), _dtype_code(out.dtype), ld_out, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_ptr(grad_out)), "ns_embedding_grad")
+    return out
+
+
+# ------------------------------------------------------------------- RMS norm
+
+def _rms_norm(x, weight, residual, eps, y, y_code, scales, h):
+    torch = _torch()
+    rows, dim, ldx = _rows_of(x, "x")
+    args = _RmsNormArgs(x=x.data_ptr(), weight=_dense(weight, (dim,), "weight"), rows=rows, dim=dim,
+                        ldx=ldx, ldy=dim, eps=eps, y_dtype=y_code, y=y.data_ptr(),
+                        x_dtype=_dtype_code(x.dtype), weight_dtype=_dtype_code(weight.dtype))
+    args.h_dtype = args.x_dtype
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is written only with a residual")
+        h = x
+    else:
+        args.ld_residual = _like_rows(residual, x.shape, "residual")
+        args.residual = residual.data_ptr()
+        args.h_dtype = _dtype_code(residual.dtype)
+        if h is None:
+            h = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+            args.ldh = dim
+        else:
+            args.ldh = _like_rows(h, x.shape, "h", residual.dtype)
+        args.h = h.data_ptr()
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    args.rstd = rstd.data_ptr()
+    if scales is not None:
+        args.scales = scales.data_ptr()
+    _check(library().ns_rms_norm(ctypes.byref(args), _stream_ptr(x)), "ns_rms_norm")
+    return h, rstd
+
+
+def ns_rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, h=None):
+    """RMS norm of the last dimension, of x + residual if that is given.
+    Returns (y, h, rstd): y in out_dtype (x's by default), h the stored sum
+    that was normalised (x itself without a residual) and 1 / rms of each row
+    (fp32), both for ns_rms_norm_grad. The residual may be x's type or fp32;
+    the sum has its type, and `h` may name its buffer (the residual's own, or
+    x's where the types agree)."""
+    torch = _torch()
+    _device_tensor(x, "x")
+    y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    h, rstd = _rms_norm(x, weight, residual, eps, y, _dtype_code(y.dtype), None, h)
+    return y, h, rstd
+
+
+def ns_rms_norm_fp8(x, weight, residual=None, eps: float = 1e-6, h=None):
+    """ns_rms_norm with the output as e4m3 codes and one fp32 scale for each
+    row (y is code * scale). Returns (codes, scales, h, rstd)."""
+    torch = _torch()
+    _device_tensor(x, "x")
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    h, rstd = _rms_norm(x, weight, residual, eps, q, NS_DT_E4M3, scales, h)
+    return q, scales, h, rstd
+
+
+def ns_rms_norm_grad_workspace_size(rows: int, dim: int) -> int:
+    return _sized("ns_rms_norm_grad_workspace_size", rows, dim)
+
+
+def ns_rms_norm_grad(dy, h, weight, rstd, dh=None, dx=None, dx_dtype=None, dweight_dtype=None,
+                     workspace=None):
+    """Gradients of ns_rms_norm (of ns_rms_norm_fp8 too): (dx, dweight), where
+    dx is the gradient of x and of the residual. `h` and `rstd` are the norm's
+    own; dh is the gradient that reaches h past the norm, of dx's type (dx may
+    be its buffer). dweight has weight's type unless dweight_dtype says so."""
+    torch = _torch()
+    rows, dim, lddy = _rows_of(dy, "dy")
+    if dx is None:
+        dx = torch.empty(dy.shape, dtype=dx_dtype or (dh.dtype if dh is not None else dy.dtype),
+                         device=dy.device)
+        lddx = dim
+    else:
+        lddx = _like_rows(dx, dy.shape, "dx", dx_dtype)
+    dweight = torch.empty(dim, dtype=dweight_dtype or weight.dtype, device=dy.device)
+    args = _RmsNormGradArgs(
+        dy=dy.data_ptr(), h=h.data_ptr(), weight=_dense(weight, (dim,), "weight"),
+        rstd=_dense(rstd, dy.shape[:-1], "rstd", torch.float32), dx=dx.data_ptr(),
+        dweight=dweight.data_ptr(), rows=rows, dim=dim, lddy=lddy,
+        ldh=_like_rows(h, dy.shape, "h"), lddx=lddx, dy_dtype=_dtype_code(dy.dtype),
+        h_dtype=_dtype_code(h.dtype), weight_dtype=_dtype_code(weight.dtype),
+        dx_dtype=_dtype_code(dx.dtype), dweight_dtype=_dtype_code(dweight.dtype))
+    if dh is not None:
+        args.lddh = _like_rows(dh, dy.shape, "dh", dx.dtype)
+        args.dh = dh.data_ptr()
+    workspace = _given_or_new(workspace, ns_rms_norm_grad_workspace_size(rows, dim), dy.device)
+    _check(library().ns_rms_norm_grad(ctypes.byref(args), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(),
+                                      _stream_ptr(dy)), "ns_rms_norm_grad")
+    return dx, dweight
+
+
+# ------------------------------------------------------------ preference loss
+
+def _preference_args(logits, labels, beta, label_smoothing):
+    if logits.dim() != 3 or logits.shape[0] % 2:
+        raise ValueError("logits must be (2 * pairs, length, vocab): the preferred sequences, then "
+                         "the others")
+    _, vocab, ld = _rows_of(logits, "logits")
+    label_type = _ids_type(labels, "labels")
+    return _PreferenceArgs(logits.data_ptr(), _dense(labels, logits.shape[:2], "labels"),
+                           logits.shape[0] // 2, logits.shape[1], vocab, max(ld, vocab),
+                           _dtype_code(logits.dtype), label_type, beta, label_smoothing)
+
+
+def ns_preference_loss_workspace_size(pairs: int, length: int, vocab: int) -> int:
+    return _sized("ns_preference_loss_workspace_size", pairs, length, vocab)
+
+
+def ns_preference_loss(logits, labels, ref_logps, beta: float = 0.1, label_smoothing: float = 0.0,
+                       workspace=None):
+    """Preference loss of paired sequences from the policy's logits (2 pairs,
+    length, vocab), the labels (2 pairs, length; a position whose label is not
+    in the vocabulary, such as -100, does not count) and the reference's log
+    probability of each sequence (2 pairs, fp32). Returns fp32 tensors
+    (losses, margins, logps, lse): the loss and margin of each pair, the
+    policy's log probability of each sequence, and each position's log sum of
+    exponentials, which the gradient needs."""
+    torch = _torch()
+    args = _preference_args(logits, labels, beta, label_smoothing)
+    pairs, length, dev = args.pairs, args.length, logits.device
+    ref = _dense(ref_logps, (2 * pairs,), "ref_logps", torch.float32)
+    out = torch.empty(2 * pairs * (length + 2), dtype=torch.float32, device=dev)
+    losses, margins, logps, lse = out.split([pairs, pairs, 2 * pairs, 2 * pairs * length])
+    workspace = _given_or_new(workspace,
+                              ns_preference_loss_workspace_size(pairs, length, args.vocab), dev)
+    _check(library().ns_preference_loss(
+        ctypes.byref(args), ref, losses.data_ptr(), margins.data_ptr(), logps.data_ptr(),
+        lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream_ptr(logits)), "ns_preference_loss")
+    return losses, margins, logps, lse.view(2 * pairs, length)
+
+
+def ns_preference_loss_grad(logits, labels, margins, lse, dlosses, beta: float = 0.1,
+                            label_smoothing: float = 0.0, out=None):
+    """Gradient of ns_preference_loss's losses with respect to the logits, for
+    margins and lse as it returned them and the gradient of each loss, dlosses
+    (pairs, fp32). `out` may be the logits themselves."""
+    torch = _torch()
+    args = _preference_args(logits, labels, beta, label_smoothing)
+    pairs = args.pairs
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        ld_out = args.vocab
+    else:
+        ld_out = _like_rows(out, logits.shape, "out", logits.dtype)
+    _check(library().ns_preference_loss_grad(
+        ctypes.byref(args), _dense(margins, (pairs,), "margins", torch.float32),
+        _dense(lse, logits.shape[:2], "lse", torch.float32),
+        _dense(dlosses, (pairs,), "dlosses", torch.float32), out.data_ptr(), max(ld_out, args.vocab),
+        _stream_ptr(logits)), "ns_preference_loss_grad")
+    return out
+
+
+# ---------------------------------------------------------------------- AdamW
+
+def ns_adamw_step(params: List, grads: List, exp_avgs: List, exp_avg_sqs: List, step: int,
+                  lr: float, betas: Sequence[float] = (0.9, 0.999), eps: float = 1e-8,
+                  weight_decays: Optional[Sequence[float]] = None,
+                  masters: Optional[List] = None) -> None:
+    """One AdamW step, in place, of the parameters that are not matrices of
+    the Newton-Schulz update. Tensors are dense and of any shape; `masters`
+    are fp32 copies that hold the weights, whose rounded values the params
+    then receive (None entries: no copy). weight_decays: one for each tensor
+    (0 by default)."""
+    count = len(params)
+    if count == 0:
+        return
+    weight_decays = [0.0] * count if weight_decays is None else list(weight_decays)
+    masters = [None] * count if masters is None else list(masters)
+    if not (len(grads) == len(exp_avgs) == len(exp_avg_sqs) == len(weight_decays) == len(masters)
+            == count):
+        raise ValueError("params, grads, exp_avgs, exp_avg_sqs, weight_decays and masters must have "
+                         "the same length")
+    torch = _torch()
+    tensors = (_AdamwTensor * count)()
+    for i, (p, g, m, v, w) in enumerate(zip(params, grads, exp_avgs, exp_avg_sqs, masters)):
+        shape = p.shape
+        tensors[i] = _AdamwTensor(
+            _dense(p, shape, f"param {i}"), _dense(g, shape, f"grad {i}"),
+            _dense(m, shape, f"exp_avg {i}"), _dense(v, shape, f"exp_avg_sq {i}"),
+            _dense(w, shape, f"master {i}", torch.float32) if w is not None else None, p.numel(),
+            _dtype_code(p.dtype), _dtype_code(g.dtype), _dtype_code(m.dtype), _dtype_code(v.dtype),
+            weight_decays[i])
+    _check(library().ns_adamw_step(tensors, count, step, lr, betas[0], betas[1], eps,
+                                   _stream_ptr(params[0])), "ns_adamw_step")
+
+
+__all__ = ["NS_DT_E4M3", "NS_IDS_I32", "NS_IDS_I64", "NS_MAX_ROWS", "ns_embedding",
+           "ns_embedding_grad", "ns_embedding_grad_workspace_size", "ns_rms_norm",
+           "ns_rms_norm_fp8", "ns_rms_norm_grad", "ns_rms_norm_grad_workspace_size",
+           "ns_preference_loss", "ns_preference_loss_grad", "ns_preference_loss_workspace_size",
+           "ns_adamw_step"]
