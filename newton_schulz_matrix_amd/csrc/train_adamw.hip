@@ -17,44 +17,42 @@ namespace nsmi {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int GROUPS = 2;                              // vectors of a thread
-constexpr int BLOCK_ELEMS = THREADS * VEC * GROUPS;
+constexpr int LANE = 4;                                // elements of a thread
+constexpr int BLOCK_ELEMS = THREADS * LANE;
 
-// Eight elements as loaded, in 16 or 32 bytes.
-struct Raw {
-  uint4 lo, hi;
-};
-__device__ __forceinline__ Raw load_raw(const void* p, int type, int64_t at) {
-  Raw r;
-  r.hi = make_uint4(0, 0, 0, 0);
-  if (type == OUT_F32) {
-    const float* f = static_cast<const float*>(p) + at;
-    __builtin_memcpy(&r.lo, f, 16);
-    __builtin_memcpy(&r.hi, f + 4, 16);
-  } else {
-    __builtin_memcpy(&r.lo, static_cast<const uint16_t*>(p) + at, 16);
-  }
-  return r;
+// LANE elements as loaded, in 16 or 8 bytes; each is read once in a call.
+typedef uint32_t Words __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ Words load_raw(const void* p, int type, int64_t at) {
+  typedef uint32_t Pair __attribute__((ext_vector_type(2), aligned(2)));
+  if (type == OUT_F32)
+    return __builtin_nontemporal_load(reinterpret_cast<const Quad*>(static_cast<const float*>(p) + at));
+  const Pair h =
+      __builtin_nontemporal_load(reinterpret_cast<const Pair*>(static_cast<const uint16_t*>(p) + at));
+  return Words{h.x, h.y, 0, 0};
 }
-__device__ __forceinline__ void widen(const Raw& r, int type, float (&v)[VEC]) {
-  if (type == OUT_F32) {
-    __builtin_memcpy(v, &r, 32);
-  } else if (type == OUT_BF16) {
-    __bf16 b[VEC];
-    __builtin_memcpy(b, &r.lo, 16);
+template <class T>
+__device__ __forceinline__ void widen_from(const Words& r, float (&v)[LANE]) {
+  T b[LANE];
+  __builtin_memcpy(b, &r, sizeof(b));
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = static_cast<float>(b[e]);
-  } else {
-    _Float16 b[VEC];
-    __builtin_memcpy(b, &r.lo, 16);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = static_cast<float>(b[e]);
-  }
+  for (int e = 0; e < LANE; ++e) v[e] = static_cast<float>(b[e]);
 }
-__device__ __forceinline__ void store_as(void* p, int type, int64_t at, const float (&v)[VEC]) {
-  if (type == OUT_F32) store8(static_cast<float*>(p) + at, v);
-  else if (type == OUT_BF16) store8(static_cast<__bf16*>(p) + at, v);
-  else store8(static_cast<_Float16*>(p) + at, v);
+__device__ __forceinline__ void widen(const Words& r, int type, float (&v)[LANE]) {
+  if (type == OUT_F32) widen_from<float>(r, v);
+  else if (type == OUT_BF16) widen_from<__bf16>(r, v);
+  else widen_from<_Float16>(r, v);
+}
+template <class T>
+__device__ __forceinline__ void store_lane(T* p, const float (&v)[LANE]) {
+  T b[LANE];
+#pragma unroll
+  for (int e = 0; e < LANE; ++e) b[e] = static_cast<T>(v[e]);
+  __builtin_memcpy(p, b, sizeof(b));
+}
+__device__ __forceinline__ void store_as(void* p, int type, int64_t at, const float (&v)[LANE]) {
+  if (type == OUT_F32) store_lane(static_cast<float*>(p) + at, v);
+  else if (type == OUT_BF16) store_lane(static_cast<__bf16*>(p) + at, v);
+  else store_lane(static_cast<_Float16*>(p) + at, v);
 }
 __device__ __forceinline__ float load_one(const void* p, int type, int64_t at) {
   if (type == OUT_F32) return static_cast<const float*>(p)[at];
@@ -76,37 +74,31 @@ __device__ __forceinline__ void update(const AdamwArgs& a, float decay, float g,
 }
 
 __global__ __launch_bounds__(THREADS) void adamw_kernel(const AdamwArgs a) {
-  int i = 0;
-  while (i + 1 < a.count && a.t[i + 1].block_begin <= blockIdx.x) ++i;
+  // the tensors that begin at or before this workgroup, counted by the lanes of a wave
+  const int lane = threadIdx.x & 63;
+  const bool begun = lane < a.count && a.begin[min(lane, ADAMW_TENSORS - 1)] <= blockIdx.x;
+  const int i = __popcll(__ballot(begun)) - 1;
   const AdamwTensor& t = a.t[i];
-  const int64_t base = static_cast<int64_t>(blockIdx.x - t.block_begin) * BLOCK_ELEMS;
+  const int64_t base = static_cast<int64_t>(blockIdx.x - a.begin[i]) * BLOCK_ELEMS;
   const void* from = t.master ? t.master : t.param;
   const int from_type = t.master ? static_cast<int>(OUT_F32) : t.param_type;
   if (base + BLOCK_ELEMS <= t.elems) {
-    Raw rw[GROUPS], rg[GROUPS], rm[GROUPS], rv[GROUPS];
+    const int64_t at = base + threadIdx.x * LANE;
+    const Words rg = load_raw(t.grad, t.grad_type, at);
+    const Words rm = load_raw(t.exp_avg, t.exp_avg_type, at);
+    const Words rv = load_raw(t.exp_avg_sq, t.exp_avg_sq_type, at);
+    const Words rw = load_raw(from, from_type, at);
+    float w[LANE], g[LANE], m[LANE], v[LANE];
+    widen(rg, t.grad_type, g);
+    widen(rm, t.exp_avg_type, m);
+    widen(rv, t.exp_avg_sq_type, v);
+    widen(rw, from_type, w);
 #pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-      const int64_t at = base + (j * THREADS + threadIdx.x) * VEC;
-      rg[j] = load_raw(t.grad, t.grad_type, at);
-      rm[j] = load_raw(t.exp_avg, t.exp_avg_type, at);
-      rv[j] = load_raw(t.exp_avg_sq, t.exp_avg_sq_type, at);
-      rw[j] = load_raw(from, from_type, at);
-    }
-#pragma unroll
-    for (int j = 0; j < GROUPS; ++j) {
-      const int64_t at = base + (j * THREADS + threadIdx.x) * VEC;
-      float w[VEC], g[VEC], m[VEC], v[VEC];
-      widen(rw[j], from_type, w);
-      widen(rg[j], t.grad_type, g);
-      widen(rm[j], t.exp_avg_type, m);
-      widen(rv[j], t.exp_avg_sq_type, v);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) update(a, t.decay, g[e], w[e], m[e], v[e]);
-      store_as(t.exp_avg, t.exp_avg_type, at, m);
-      store_as(t.exp_avg_sq, t.exp_avg_sq_type, at, v);
-      if (t.master) store8(t.master + at, w);
-      store_as(t.param, t.param_type, at, w);
-    }
+    for (int e = 0; e < LANE; ++e) update(a, t.decay, g[e], w[e], m[e], v[e]);
+    store_as(t.exp_avg, t.exp_avg_type, at, m);
+    store_as(t.exp_avg_sq, t.exp_avg_sq_type, at, v);
+    if (t.master) store_lane(t.master + at, w);
+    store_as(t.param, t.param_type, at, w);
     return;
   }
   // the last workgroup of a tensor: neighbouring threads take neighbouring elements

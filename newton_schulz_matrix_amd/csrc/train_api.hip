@@ -104,13 +104,13 @@ namespace nsmi {
 namespace {
 struct EmbedGradPlan {
   EmbedSort sort;
-  size_t order, start, partial, total;   // byte offsets, bytes
+  size_t sorted, start, partial, total;   // byte offsets, bytes
 };
 EmbedGradPlan embed_grad_plan(int64_t rows, int64_t dim, int64_t count) {
   EmbedGradPlan p;
   p.sort = embed_sort_plan(rows, count);
-  p.order = 0;
-  p.start = align_up(sizeof(int) * static_cast<size_t>(count));
+  p.sorted = 0;
+  p.start = align_up(sizeof(int2) * static_cast<size_t>(count));
   p.partial = align_up(p.start + sizeof(int) * (static_cast<size_t>(p.sort.slots) + 1));
   p.total = align_up(p.partial + sizeof(float) * static_cast<size_t>(p.sort.windows) * dim);
   return p;
@@ -154,7 +154,7 @@ NS_API ns_status ns_embedding_grad(const void* grad_out, ns_dtype grad_out_dtype
   a.grad_out = grad_out;
   a.ids = ids;
   a.grad = grad;
-  a.order = reinterpret_cast<int*>(w + p.order);
+  a.sorted = reinterpret_cast<int2*>(w + p.sorted);
   a.start = reinterpret_cast<int*>(w + p.start);
   a.partial = reinterpret_cast<float*>(w + p.partial);
   a.ld_grad_out = ld_grad_out;
@@ -460,9 +460,10 @@ NS_API ns_status ns_adamw_step(const ns_adamw_tensor* tensors, int count, int64_
       a.count = 0;
       blocks = 0;
     }
+    a.begin[a.count] = blocks;
     a.t[a.count++] = {t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.master, t.elems,
                       t.param_dtype, t.grad_dtype, t.exp_avg_dtype, t.exp_avg_sq_dtype,
-                      static_cast<float>(lr * t.weight_decay), blocks};
+                      static_cast<float>(lr * t.weight_decay)};
     blocks += more;
   }
   return from_hip(launch_adamw(a, blocks, st));

@@ -3,9 +3,17 @@
 // out[i] = scale * table[ids[i]];  grad[v] = scale * sum_{i: ids[i] = v} grad_out[i].
 //
 // Both are bound by memory: the lookup moves count x dim elements in and out,
-// the gradient reads count x dim and writes the rows x dim table once. A
+// the gradient reads count x dim and writes rows x dim, most of them zeros. A
 // thread owns eight columns; TX threads (a power of two) lie along a row and
-// 256 / TX rows share a workgroup, so narrow tables fill the lanes too.
+// the other threads of a workgroup take further rows, so narrow tables fill
+// the lanes too.
+//
+// The gradient is three launches: one sorts the ids; one sums whole windows of
+// the sorted places that belong to one id (the few ids that a large share of
+// the places name) and, in further workgroups, clears the table; one adds up
+// each id's run and writes its row. The rows that some id names are written
+// twice: a clearing workgroup that first looked up whether its row is named
+// would wait for that longer than the row's zeros take.
 #include <algorithm>
 
 #include "train_device.h"
@@ -13,6 +21,35 @@
 
 namespace nsmi {
 namespace {
+
+// Eight columns of R rows of a table, all in flight together (row numbers must
+// be valid); then as fp32, zeros for a row that is not `used`.
+template <int R, class T>
+__device__ __forceinline__ void fetch_rows(const T* table, int64_t ld, const int (&rows)[R],
+                                           int dim, int col, Raw<T> (&raw)[R]) {
+  if (dim < VEC) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) raw[r] = fetch_at(table + rows[r] * ld, dim, col);
+}
+template <int R, class T>
+__device__ __forceinline__ void widen_rows(const Raw<T> (&raw)[R], const T* table, int64_t ld,
+                                           const int (&rows)[R], const bool (&used)[R], int dim,
+                                           int col, float (&v)[R][VEC]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    widen_at(raw[r], table + rows[r] * ld, dim, col, v[r]);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[r][e] = used[r] ? v[r][e] : 0.f;
+  }
+}
+template <int R, class T>
+__device__ __forceinline__ void gather(const T* table, int64_t ld, const int (&rows)[R],
+                                       const bool (&used)[R], int dim, int col,
+                                       float (&v)[R][VEC]) {
+  Raw<T> raw[R];
+  fetch_rows(table, ld, rows, dim, col, raw);
+  widen_rows(raw, table, ld, rows, used, dim, col, v);
+}
 
 // ---------------------------------------------------------------- lookup
 
@@ -24,19 +61,17 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int tx_log2
   if (col >= a.dim) return;
   const int first = blockIdx.x * (R * teams) + ty;
   int64_t id[R];
+  int row[R];
+  bool used[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) id[r] = static_cast<const I*>(a.ids)[min(first + r * teams, a.count - 1)];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int i = first + r * teams;
-    id[r] = i < a.count ? static_cast<int64_t>(static_cast<const I*>(a.ids)[i]) : -1;
+    used[r] = id[r] >= 0 && id[r] < a.rows;
+    row[r] = used[r] ? static_cast<int>(id[r]) : 0;
   }
   float v[R][VEC];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[r][e] = 0.f;
-    if (id[r] >= 0 && id[r] < a.rows)
-      load8_upto(static_cast<const TI*>(a.table) + id[r] * a.ld_table + col, a.dim - col, v[r]);
-  }
+  gather(static_cast<const TI*>(a.table), a.ld_table, row, used, a.dim, col, v);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int i = first + r * teams;
@@ -52,19 +87,21 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int tx_log2
 constexpr int SORT_THREADS = 1024;
 constexpr int SORT_WAVES = SORT_THREADS / 64;
 constexpr int SORT_RANGE = 512;    // most slots of a group: 32 KB of counters
-constexpr int SORT_BATCH = 4;      // windows of 64 ids loaded ahead
+constexpr int SORT_BATCH = 16;     // windows of 64 ids loaded together
 
 // A stable counting sort in one launch. Workgroup g takes the ids whose low
 // bits are g. It counts them per slot, and how many ids belong to groups
-// before it, so it knows where its part of `order` begins without hearing
+// before it, so it knows where its part of `sorted` begins without hearing
 // from another workgroup; then it goes over the ids again and puts each
-// position in its place. Every workgroup reads all ids (twice): they are a
-// thousandth of the gradient's bytes and come from the caches. Each wave takes a contiguous part of the ids
-// and keeps its own counters, so positions of one row stay in order.
+// position in its place. Every workgroup reads all ids: they are a thousandth
+// of the gradient's bytes and come from the caches, and up to 16384 of them
+// are read once and stay in registers in between. Each wave takes a
+// contiguous part of the ids and keeps its own counters, so positions of one
+// id stay in order.
 template <class I>
 __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(EmbedGradArgs a) {
   extern __shared__ int counters[];            // (SORT_WAVES, range)
-  __shared__ int wave_total[SORT_WAVES], wave_below[SORT_WAVES];
+  __shared__ int wave_total[SORT_WAVES], wave_below[SORT_WAVES], counted;
   const int range = a.sort.range, gl = a.sort.groups_log2;
   const int group = blockIdx.x, mask = (1 << gl) - 1;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -75,16 +112,16 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(EmbedGradArgs a) {
   const I* ids = static_cast<const I*>(a.ids);
   const int per = ((a.count + SORT_WAVES * 64 - 1) / (SORT_WAVES * 64)) * 64;
   const int begin = min(a.count, wave * per), end = min(a.count, begin + per);
-  // id at position i, -1 where it does not count
+  // id at position i, -1 where it does not count (no branch before the load:
+  // a batch's loads are in flight together)
   auto id_at = [&](int i) -> int {
-    if (i >= end) return -1;
-    const int64_t id = static_cast<int64_t>(ids[i]);
-    return id >= 0 && id < a.rows && id != a.padding_id ? static_cast<int>(id) : -1;
+    const int64_t id = static_cast<int64_t>(ids[min(i, end - 1)]);
+    return i < end && id >= 0 && id < a.rows && id != a.padding_id ? static_cast<int>(id) : -1;
   };
 
   int below = 0;
+  int id[SORT_BATCH];
   for (int base = begin; base < end; base += 64 * SORT_BATCH) {
-    int id[SORT_BATCH];
 #pragma unroll
     for (int u = 0; u < SORT_BATCH; ++u) id[u] = id_at(base + u * 64 + lane);
 #pragma unroll
@@ -125,15 +162,21 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(EmbedGradArgs a) {
   if (r < range) {
     a.start[group * range + r] = at;
     for (int w = 0; w < SORT_WAVES; ++w) counters[w * range + r] += at;
-    if (group == mask && r == range - 1) a.start[a.sort.slots] = at + total;
+    if (group == mask && r == range - 1) {
+      a.start[a.sort.slots] = at + total;
+      counted = at + total;
+    }
   }
   __syncthreads();
+  if (group == mask)   // the places behind the last counted id
+    for (int k = counted + threadIdx.x; k < a.count; k += SORT_THREADS)
+      a.sorted[k] = make_int2(0, -1);
 
   const uint64_t before = (uint64_t{1} << lane) - 1;
   for (int base = begin; base < end; base += 64 * SORT_BATCH) {
-    int id[SORT_BATCH];
+    if (per > 64 * SORT_BATCH)
 #pragma unroll
-    for (int u = 0; u < SORT_BATCH; ++u) id[u] = id_at(base + u * 64 + lane);
+      for (int u = 0; u < SORT_BATCH; ++u) id[u] = id_at(base + u * 64 + lane);
 #pragma unroll
     for (int u = 0; u < SORT_BATCH; ++u) {
       const bool own = id[u] >= 0 && (id[u] & mask) == group;
@@ -146,7 +189,7 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(EmbedGradArgs a) {
         int first = 0;
         if (lane == leader) first = atomicAdd(&mine[which >> gl], __popcll(peers));
         first = __shfl(first, leader, 64);
-        if (same) a.order[first + __popcll(peers & before)] = base + u * 64 + lane;
+        if (same) a.sorted[first + __popcll(peers & before)] = make_int2(base + u * 64 + lane, which);
         todo &= ~peers;
       }
     }
@@ -155,88 +198,159 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(EmbedGradArgs a) {
 
 // --------------------------------------------------------------- gradient
 
-// Adds the gradients of sorted places [from, to), in order, to sum.
-template <class T>
-__device__ __forceinline__ void add_terms(const EmbedGradArgs& a, int from, int to, int col,
-                                          float (&sum)[VEC]) {
-  constexpr int U = 4;
-  const T* g = static_cast<const T*>(a.grad_out) + col;
-  int k = from;
-  for (; k + U <= to; k += U) {
-    int i[U];
+// Adds rows of `from`, at index(k) for k in [k0, k1), to sum, in order. A
+// batch's rows are in flight together; the places past k1 in the last batch
+// repeat its last row (which is then at hand) and do not count.
+template <class T, class F>
+__device__ __forceinline__ void add_rows(const T* from, int64_t ld, int dim, int col, int k0, int k1,
+                                         F index, float (&sum)[VEC]) {
+  constexpr int U = 8;
+  for (int k = k0; k < k1; k += U) {
+    int row[U];
+    bool used[U];
     float v[U][VEC];
 #pragma unroll
-    for (int u = 0; u < U; ++u) i[u] = a.order[k + u];
-#pragma unroll
-    for (int u = 0; u < U; ++u) load8_upto(g + i[u] * a.ld_grad_out, a.dim - col, v[u]);
+    for (int u = 0; u < U; ++u) {
+      used[u] = k + u < k1;
+      row[u] = index(min(k + u, k1 - 1));
+    }
+    gather(from, ld, row, used, dim, col, v);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) sum[e] += v[u][e];
   }
-  for (; k < to; ++k) {
-    float v[VEC];
-    load8_upto(g + a.order[k] * a.ld_grad_out, a.dim - col, v);
+}
+
+// Adds the gradients of sorted places [k0, k1).
+template <class T>
+__device__ __forceinline__ void add_terms(const EmbedGradArgs& a, int k0, int k1, int col,
+                                          float (&sum)[VEC]) {
+  add_rows(static_cast<const T*>(a.grad_out), a.ld_grad_out, a.dim, col, k0, k1,
+           [&](int k) { return a.sorted[k].x; }, sum);
+}
+
+// What there is to clear: `rows` of `cols` elements; a dense table is one row.
+struct Clear {
+  int64_t rows, cols, across;   // across: workgroups along a row
+};
+constexpr int CLEAR_STEP = 256 * VEC * 4;   // elements of a workgroup
+
+template <class T>
+__device__ __forceinline__ void clear_rows(T* table, int64_t ld, const Clear& c, int64_t block,
+                                           int64_t blocks) {
+  const float zero[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (; block < c.rows * c.across; block += blocks) {
+    const int64_t row = c.rows == 1 ? 0 : block / c.across;
+    const int64_t from = (block - row * c.across) * CLEAR_STEP;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) sum[e] += v[e];
+    for (int j = 0; j < 4; ++j) {
+      const int64_t col = from + (j * 256 + threadIdx.x) * VEC;
+      if (col + VEC <= c.cols) store8(table + row * ld + col, zero);
+      else if (col < c.cols) store8_upto(table + row * ld + col, static_cast<int>(c.cols - col), zero);
+    }
   }
 }
 
-// Sums of the windows of `window` sorted places that belong to one row
-// altogether: a row that a large share of the ids name is summed by many
-// workgroups. Other windows are left alone.
-template <class T, class I>
-__global__ __launch_bounds__(256) void window_kernel(EmbedGradArgs a, int tx_log2) {
-  const int tx = threadIdx.x & ((1 << tx_log2) - 1);
-  const int w = blockIdx.x * (256 >> tx_log2) + (threadIdx.x >> tx_log2);
-  const int col = ((blockIdx.y << tx_log2) + tx) * VEC;
+// The first `summing` workgroups: sums of the windows of `window` sorted
+// places that name one id altogether, so that an id that a large share of the
+// places name is summed by many workgroups. Other windows are left alone. The
+// others clear the table in the order of the addresses: 1 GB is written at
+// 5.8 to 6.7 TB/s so, at 5.4 by fewer workgroups that go round.
+template <class T, class TO>
+__global__ __launch_bounds__(256) void window_clear_kernel(EmbedGradArgs a, int tx_log2,
+                                                           unsigned summing, Clear clear) {
+  if (blockIdx.x >= summing) {
+    clear_rows(static_cast<TO*>(a.grad), a.ld_grad, clear, blockIdx.x - summing,
+               gridDim.x - summing);
+    return;
+  }
+  const int tx = threadIdx.x & ((1 << tx_log2) - 1), ty = threadIdx.x >> tx_log2;
+  const int teams = 256 >> tx_log2, across = (a.dim + (VEC << tx_log2) - 1) / (VEC << tx_log2);
+  const int w = static_cast<int>(blockIdx.x / across) * teams + ty;
+  const int col = (static_cast<int>(blockIdx.x % across) * (1 << tx_log2) + tx) * VEC;
   if (col >= a.dim || w >= a.sort.windows) return;
   const int from = w * a.sort.window, to = from + a.sort.window;
-  if (to > a.start[a.sort.slots]) return;
-  const I* ids = static_cast<const I*>(a.ids);
-  if (ids[a.order[from]] != ids[a.order[to - 1]]) return;
+  const int id = a.sorted[from].y;
+  if (id < 0 || id != a.sorted[to - 1].y) return;
   float sum[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   add_terms<T>(a, from, to, col, sum);
   store8_upto(a.partial + static_cast<int64_t>(w) * a.dim + col, a.dim - col, sum);
 }
 
-// Every row of the table's gradient: its terms up to the first whole window,
+// Adds the places [k, end) of one id: the terms up to the first whole window,
 // the whole windows' sums, the terms after the last.
-template <class T, class TO>
-__global__ __launch_bounds__(256) void rows_kernel(EmbedGradArgs a, int tx_log2) {
-  const int tx = threadIdx.x & ((1 << tx_log2) - 1);
-  const int teams = 256 >> tx_log2;
-  const int col = ((blockIdx.y << tx_log2) + tx) * VEC;
-  if (col >= a.dim) return;
-  const int left = a.dim - col, S = a.sort.window;
-  for (int v = blockIdx.x * teams + (threadIdx.x >> tx_log2); v < a.rows; v += gridDim.x * teams) {
-    const int p = sorted_slot(v, a.sort);
-    const int s = a.start[p], e = a.start[p + 1];
-    TO* out = static_cast<TO*>(a.grad) + v * a.ld_grad + col;
-    float sum[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (s == e) {
-      if (!a.accumulate) store8_upto(out, left, sum);
-      continue;
-    }
-    const int w0 = (s + S - 1) / S, w1 = e / S;
-    if (w0 < w1) {
-      add_terms<T>(a, s, w0 * S, col, sum);
-      for (int w = w0; w < w1; ++w) {
-        float part[VEC];
-        load8_upto(a.partial + static_cast<int64_t>(w) * a.dim + col, left, part);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) sum[i] += part[i];
-      }
-      add_terms<T>(a, w1 * S, e, col, sum);
-    } else {
-      add_terms<T>(a, s, e, col, sum);
-    }
-    float old[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (a.accumulate) load8_upto(static_cast<const TO*>(out), left, old);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) sum[i] = fmaf(a.scale, sum[i], old[i]);
-    store8_upto(out, left, sum);
+template <class T>
+__device__ __forceinline__ void add_run(const EmbedGradArgs& a, int k, int end, int col,
+                                        float (&sum)[VEC]) {
+  const int S = a.sort.window, w0 = (k + S - 1) / S, w1 = end / S;
+  const bool windows = w0 < w1;
+  add_terms<T>(a, k, windows ? w0 * S : end, col, sum);
+  if (windows) {
+    add_rows(a.partial, a.dim, a.dim, col, w0, w1, [](int w) { return w; }, sum);
+    add_terms<T>(a, w1 * S, end, col, sum);
   }
+}
+
+// A team takes PLACES sorted places and the runs (places of one id) that
+// begin there: all its rows are read at once and summed run by run; a run
+// that goes on past the team's places is followed to its end.
+template <class T, class TO, bool ADD>
+__global__ __launch_bounds__(256) void runs_kernel(EmbedGradArgs a, int tx_log2) {
+  constexpr int PLACES = ADD || sizeof(T) == 4 ? 4 : 8;
+  const int tx = threadIdx.x & ((1 << tx_log2) - 1);
+  const int first = (blockIdx.x * (256 >> tx_log2) + (threadIdx.x >> tx_log2)) * PLACES;
+  const int col = ((blockIdx.y << tx_log2) + tx) * VEC;
+  if (col >= a.dim || first >= a.count) return;
+  const int left = a.dim - col, last = a.count - 1;
+  int2 place[PLACES];
+#pragma unroll
+  for (int u = 0; u < PLACES; ++u) place[u] = a.sorted[min(first + u, last)];
+  const int before = first > 0 ? a.sorted[first - 1].y : -1;
+  const int after = first + PLACES <= last ? a.sorted[first + PLACES].y : -1;
+  // id of the run each place belongs to, if that run begins here
+  int id[PLACES], row[PLACES], head[PLACES];
+  bool used[PLACES], heads[PLACES];
+  bool any = false;
+#pragma unroll
+  for (int u = 0; u < PLACES; ++u) {
+    id[u] = first + u <= last ? place[u].y : -1;
+    const int previous = u == 0 ? before : place[u - 1].y;
+    heads[u] = id[u] >= 0 && id[u] != previous;
+    used[u] = id[u] >= 0 && (heads[u] || (u > 0 && used[u - 1]));
+    row[u] = used[u] ? place[u].x : 0;
+    head[u] = heads[u] ? id[u] : 0;
+    any = any || used[u];
+  }
+  if (!any) return;
+  const T* from = static_cast<const T*>(a.grad_out);
+  float v[PLACES][VEC], old[ADD ? PLACES : 1][VEC];
+  Raw<T> raw[PLACES];
+  fetch_rows(from, a.ld_grad_out, row, a.dim, col, raw);
+  if constexpr (ADD)
+    gather(static_cast<const TO*>(a.grad), a.ld_grad, head, heads, a.dim, col, old);
+  widen_rows(raw, from, a.ld_grad_out, row, used, a.dim, col, v);
+  float sum[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, base[VEC];
+  auto write = [&](int which) {
+    float out[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) out[i] = fmaf(a.scale, sum[i], ADD ? base[i] : 0.f);
+    store8_upto(static_cast<TO*>(a.grad) + which * a.ld_grad + col, left, out);
+  };
+#pragma unroll
+  for (int u = 0; u < PLACES; ++u) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      sum[i] = heads[u] ? v[u][i] : sum[i] + v[u][i];
+      if constexpr (ADD) base[i] = heads[u] ? old[u][i] : base[i];
+    }
+    if (u + 1 < PLACES && used[u] && id[u + 1] != id[u]) write(id[u]);
+  }
+  const int open = id[PLACES - 1];
+  if (!used[PLACES - 1]) return;
+  if (after == open)
+    add_run<T>(a, first + PLACES, a.start[sorted_slot(open, a.sort) + 1], col, sum);
+  write(open);
 }
 
 // Threads along a row (log2) and workgroups along it.
@@ -248,6 +362,8 @@ Across across(int dim) {
   return {lg, static_cast<unsigned>((vecs + (1 << lg) - 1) >> lg)};
 }
 unsigned ceil_div(int64_t a, int64_t b) { return static_cast<unsigned>((a + b - 1) / b); }
+
+constexpr unsigned CLEAR_BLOCKS = 1u << 23;   // at most, of one launch; more take turns
 
 template <class TI, class TO, class I>
 void embedding_on(const EmbedArgs& a, hipStream_t stream) {
@@ -282,9 +398,10 @@ EmbedSort embed_sort_plan(int64_t rows, int64_t count) {
   while (s.groups_log2 > 0 && (int64_t{1} << s.groups_log2) > rows) --s.groups_log2;
   s.range = static_cast<int>(((rows - 1) >> s.groups_log2) + 1);
   s.slots = s.range << s.groups_log2;
-  // a row of c terms takes up to 2 window + c / window steps: about sqrt(count) of each
-  s.window = 32;
-  while (4 * int64_t{s.window} * s.window < count) s.window *= 2;
+  // a row of c terms takes up to 2 window + c / window steps; the most frequent
+  // token of a text is about every tenth
+  s.window = 16;
+  while (16 * int64_t{s.window} * s.window < count) s.window *= 2;
   s.windows = static_cast<int>(count / s.window);
   return s;
 }
@@ -296,23 +413,30 @@ hipError_t launch_embedding_grad(const EmbedGradArgs& a, int grad_out_type, bool
   const size_t lds = sizeof(int) * SORT_WAVES * s.range;
   if (ids64) hipLaunchKernelGGL(sort_kernel<int64_t>, groups, threads, lds, stream, a);
   else hipLaunchKernelGGL(sort_kernel<int32_t>, groups, threads, lds, stream, a);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   const Across x = across(a.dim);
   const int teams = 256 >> x.tx_log2;
+  const unsigned summing = ceil_div(s.windows, teams) * x.blocks;
+  Clear c{a.rows, a.dim, 0};
+  if (a.ld_grad == a.dim) c = {1, static_cast<int64_t>(a.rows) * a.dim, 0};
+  c.across = (c.cols + CLEAR_STEP - 1) / CLEAR_STEP;
+  const unsigned clearing =
+      a.accumulate ? 0 : static_cast<unsigned>(std::min<int64_t>(c.rows * c.across, CLEAR_BLOCKS));
   return by_type(grad_out_type, [&](auto t) {
-    using T = decltype(t);
-    if (s.windows > 0) {
-      const dim3 grid(ceil_div(s.windows, teams), x.blocks);
-      if (ids64) hipLaunchKernelGGL((window_kernel<T, int64_t>), grid, dim3(256), 0, stream, a, x.tx_log2);
-      else hipLaunchKernelGGL((window_kernel<T, int32_t>), grid, dim3(256), 0, stream, a, x.tx_log2);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
     return by_type(grad_type, [&](auto to) {
-      const unsigned blocks = std::min(ceil_div(a.rows, teams), 1u << 16);
-      hipLaunchKernelGGL((rows_kernel<T, decltype(to)>), dim3(blocks, x.blocks), dim3(256), 0,
-                         stream, a, x.tx_log2);
+      using T = decltype(t);
+      using TO = decltype(to);
+      if (summing + clearing > 0) {
+        hipLaunchKernelGGL((window_clear_kernel<T, TO>), dim3(summing + clearing), dim3(256), 0,
+                           stream, a, x.tx_log2, summing, c);
+        e = hipGetLastError();
+        if (e != hipSuccess || a.count == 0) return e;
+      }
+      const int places = a.accumulate || sizeof(T) == 4 ? 4 : 8;
+      const dim3 grid(ceil_div(a.count, places * teams), x.blocks);
+      if (a.accumulate) hipLaunchKernelGGL((runs_kernel<T, TO, true>), grid, dim3(256), 0, stream, a, x.tx_log2);
+      else hipLaunchKernelGGL((runs_kernel<T, TO, false>), grid, dim3(256), 0, stream, a, x.tx_log2);
       return hipGetLastError();
     });
   });

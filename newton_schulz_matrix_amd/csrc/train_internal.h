@@ -32,9 +32,10 @@ hipError_t launch_embedding(const EmbedArgs& a, int table_type, bool ids64, int 
                             hipStream_t stream);
 
 // Sorted ids of one gradient call, in the workspace:
-//   order[k]    the k-th position in sorted order (count ints);
+//   sorted[k]   position and id of the k-th place in sorted order; the places
+//               of ids that do not count come last, with id -1 (count pairs);
 //   start[p]    first k of table row v, with p = sorted_slot(v); the row's
-//               terms end at start[p + 1] (slots + 1 ints).
+//               places end at start[p + 1] (slots + 1 ints).
 // Rows are dealt to `groups` sorting workgroups by their low bits, `range`
 // consecutive slots to a workgroup, so that the most frequent ids (small ones,
 // in most vocabularies) do not meet in one workgroup.
@@ -54,7 +55,7 @@ struct EmbedGradArgs {
   const void* grad_out;
   const void* ids;
   void* grad;
-  int* order;
+  int2* sorted;
   int* start;
   float* partial;      // (windows, dim)
   int64_t ld_grad_out, ld_grad;
@@ -138,10 +139,10 @@ struct AdamwTensor {
   int64_t elems;
   int param_type, grad_type, exp_avg_type, exp_avg_sq_type;
   float decay;         // lr * weight_decay
-  unsigned block_begin;   // first workgroup of this tensor in the launch
 };
 struct AdamwArgs {
   AdamwTensor t[ADAMW_TENSORS];
+  unsigned begin[ADAMW_TENSORS];      // first workgroup of each tensor
   int count;
   float beta1, rest1, beta2, rest2;   // rest = 1 - beta, from 64 bits
   float step_size;                    // lr / (1 - beta1^step)

@@ -21,22 +21,29 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int UNROLL = 4;                           // vectors of a thread in flight
 constexpr int STEP = THREADS * VEC * UNROLL;        // elements of a workgroup's step
+constexpr float FAR = 150.f;                        // exp(-FAR) is 0 in fp32
 
-// exp(x), x <= 0, by the hardware's 2^x. The product with log2(e) carries the
-// constant's next 24 bits: without them every term of a sum would be off to
-// the same side, and the sums over a sequence would keep that error.
+// exp(x) by the hardware's 2^x. The product with log2(e) carries the
+// constant's next 24 bits.
 __device__ __forceinline__ float exp_neg(float x) {
   return __builtin_amdgcn_exp2f(fmaf(x, 1.925963033e-8f, x * 1.442695041f));
 }
 
-// Joins (m, s) with (m2, s2): sums of exp relative to their maxima. A maximum
-// of -inf stands for no terms (its sum is 0).
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-  const float top = fmaxf(m, m2);
-  const float safe = top == -INFINITY ? 0.f : top;
-  s = s * exp_neg(m - safe) + s2 * exp_neg(m2 - safe);
-  m = top;
+// The same without the rounding of the product p = x log2(e): exp(x) = 2^p
+// exp(x - p ln 2), where the second factor is 1 + c. bf16 logits take few
+// values, so the roundings of p do not average out over a row: left alone they
+// put 2e-8 on its sum, much the same for every row, which the difference of
+// two sequences' sums keeps. x is not below -FAR.
+__device__ __forceinline__ float exp_exact(float x) {
+  const float p = x * 1.442695041f;
+  const float c = fmaf(p, 1.904654299e-9f, fmaf(-p, 0.693147182f, x));
+  const float t = __builtin_amdgcn_exp2f(p);
+  return fmaf(t, c, t);
 }
+
+// The exponent's base for a maximum m: exp(z - m) for m = -inf (no terms yet,
+// or none but masked ones) is taken against 0 instead, which gives 0.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
 
 template <class I>
 __device__ __forceinline__ int64_t label_at(const PrefArgs& a, int64_t row) {
@@ -46,58 +53,97 @@ __device__ __forceinline__ bool counted(const PrefArgs& a, int64_t label) {
   return label >= 0 && label < a.vocab;
 }
 
-// Maximum and sum of one piece of a row.
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+// exp(m - base), 0 for m = -inf.
+__device__ __forceinline__ float factor(float m, float base) {
+  const float x = m - base;
+  return x < -FAR ? 0.f : exp_exact(x);
+}
+
+// Maximum and sum of one piece of a row. A thread keeps its own running
+// maximum and rescales its sum once a step; the threads' sums are brought to
+// the piece's maximum once, at the end, and added in 64 bits, so that a row's
+// sum carries one rounding where a sequence adds up hundreds of rows.
+template <class T>
+__device__ __forceinline__ void take(const float (&v)[UNROLL][VEC], float& m, float& s) {
+  float top = m, low = INFINITY;
+#pragma unroll
+  for (int j = 0; j < UNROLL; ++j)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      top = fmaxf(top, v[j][e]);
+      low = fminf(low, v[j][e]);
+    }
+  const float base = base_of(top);
+  float add = 0.f;
+  if (__any(low - base < -FAR)) {   // -inf - (-inf) in the correction: terms this far off are 0
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float x = v[j][e] - base;
+        add += exp_exact(x < -FAR ? -FAR : x);   // (a NaN stays one)
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) add += exp_exact(v[j][e] - base);
+  }
+  s = fmaf(s, factor(m, base), add);
+  m = top;
+}
 template <class T, class I>
 __global__ __launch_bounds__(THREADS) void pieces_kernel(PrefArgs a, PrefSplit sp, float2* parts) {
-  __shared__ float red_m[THREADS / 64], red_s[THREADS / 64];
+  __shared__ float red_m[THREADS / 64];
+  __shared__ double red_s[THREADS / 64];
   const int64_t row = blockIdx.x;
   if (!counted(a, label_at<I>(a, row))) return;
   const int begin = blockIdx.y * sp.piece, end = min(a.vocab, begin + sp.piece);
   const T* z = static_cast<const T*>(a.logits) + row * a.ld;
   float m = -INFINITY, s = 0.f;
-  for (int base = begin; base < end; base += STEP) {
+  const int col0 = threadIdx.x * VEC;
+  int base = begin;
+  for (; base + STEP <= end; base += STEP) {
     float v[UNROLL][VEC];
-    const bool whole = base + STEP <= end;
+    Raw<T> raw[UNROLL];
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
-      const int at = base + (j * THREADS + threadIdx.x) * VEC;
-      if (whole || at + VEC <= end) {
-        load8(z + at, v[j]);
-      } else {
+    for (int j = 0; j < UNROLL; ++j) raw[j] = fetch<Use::ONCE>(z + base + j * THREADS * VEC + col0);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[j][e] = at + e < end ? static_cast<float>(z[at + e]) : -INFINITY;
-      }
-    }
-    float top = m;
+    for (int j = 0; j < UNROLL; ++j) widen(raw[j], v[j]);
+    take<T>(v, m, s);
+  }
+  if (base < end) {
+    float v[UNROLL][VEC];
+    Raw<T> raw[UNROLL];
+    fetch_row<Use::ONCE>(z, end, base + col0, THREADS * VEC, raw);
+    widen_row(raw, z, end, base + col0, THREADS * VEC, v);
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) top = fmaxf(top, v[j][e]);
-    const float safe = top == -INFINITY ? 0.f : top;
-    float add = 0.f;
-#pragma unroll
-    for (int j = 0; j < UNROLL; ++j)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) add += exp_neg(v[j][e] - safe);
-    s = fmaf(s, exp_neg(m - safe), add);
-    m = top;
+      for (int e = 0; e < VEC; ++e)
+        v[j][e] = base + j * THREADS * VEC + col0 + e < end ? v[j][e] : -INFINITY;
+    take<T>(v, m, s);
   }
+  const int wave = threadIdx.x >> 6;
+  const float wave_top = wave_max(m);
+  if ((threadIdx.x & 63) == 0) red_m[wave] = wave_top;
+  __syncthreads();
+  float top = red_m[0];
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) join(m, s, __shfl_xor(m, off, 64), __shfl_xor(s, off, 64));
-  if ((threadIdx.x & 63) == 0) {
-    red_m[threadIdx.x >> 6] = m;
-    red_s[threadIdx.x >> 6] = s;
-  }
+  for (int w = 1; w < THREADS / 64; ++w) top = fmaxf(top, red_m[w]);
+  const double sum = wave_sum64(static_cast<double>(s * factor(m, base_of(top))));
+  if ((threadIdx.x & 63) == 0) red_s[wave] = sum;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  for (int w = 1; w < THREADS / 64; ++w) join(m, s, red_m[w], red_s[w]);
-  parts[row * sp.pieces + blockIdx.y] = make_float2(m, s);
-}
-
-__device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  double total = 0.0;
+  for (int w = 0; w < THREADS / 64; ++w) total += red_s[w];
+  parts[row * sp.pieces + blockIdx.y] = make_float2(top, static_cast<float>(total));
 }
 
 // log(1 + exp(x)) = -log sigmoid(-x)
@@ -124,12 +170,13 @@ __global__ __launch_bounds__(PAIR_THREADS) void pairs_kernel(PrefArgs a, PrefSpl
       const int64_t label = label_at<I>(a, row);
       float l = 0.f;
       if (counted(a, label)) {
-        float m = -INFINITY, s = 0.f;
-        for (int k = 0; k < sp.pieces; ++k) {
-          const float2 p = parts[row * sp.pieces + k];
-          join(m, s, p.x, p.y);
-        }
-        const double wide = static_cast<double>(m) + log(static_cast<double>(s));
+        const float2* p = parts + row * sp.pieces;
+        float m = p[0].x;
+        for (int k = 1; k < sp.pieces; ++k) m = fmaxf(m, p[k].x);
+        double s = 0.0;
+        for (int k = 0; k < sp.pieces; ++k)
+          s += static_cast<double>(p[k].y) * exp(static_cast<double>(p[k].x) - base_of(m));
+        const double wide = static_cast<double>(m) + log(s);
         l = static_cast<float>(wide);
         sum += static_cast<double>(static_cast<float>(static_cast<const T*>(a.logits)[row * a.ld + label])) - wide;
       }
@@ -165,50 +212,51 @@ __device__ __forceinline__ float sigmoid(float x) {
   return x >= 0.f ? 1.f / (1.f + e) : e / (1.f + e);
 }
 
-// One step of STEP elements of a row.
+// Workgroups take GRAD_STEP elements each, in the order of the addresses.
+constexpr int GRAD_UNROLL = 4;
+constexpr int GRAD_STEP = THREADS * VEC * GRAD_UNROLL;
 template <class T, class I>
 __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* margins,
                                                        const float* lse, const float* dlosses,
-                                                       T* dlogits, int64_t ld_dlogits) {
-  const int64_t row = blockIdx.x;
-  const int base = blockIdx.y * STEP;
-  const int64_t label = label_at<I>(a, row);
-  T* d = dlogits + row * ld_dlogits;
-  const bool whole = base + STEP <= a.vocab;
-  if (!counted(a, label)) {
-    const float zero[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                                                       T* dlogits, int64_t ld_dlogits, int steps) {
+  const int64_t all = int64_t{2} * a.pairs * a.length * steps;
+  for (int64_t block = blockIdx.x; block < all; block += gridDim.x) {
+    const int row = static_cast<int>(block / steps);
+    const int base = static_cast<int>(block - static_cast<int64_t>(row) * steps) * GRAD_STEP;
+    const int64_t label = label_at<I>(a, row);
+    T* d = dlogits + row * ld_dlogits;
+    if (!counted(a, label)) {
+      const float zero[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
+      for (int j = 0; j < GRAD_UNROLL; ++j) {
+        const int at = base + (j * THREADS + threadIdx.x) * VEC;
+        store8_upto(d + at, a.vocab - at, zero);
+      }
+      continue;
+    }
+    const int col0 = base + static_cast<int>(threadIdx.x) * VEC;
+    const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+    float v[GRAD_UNROLL][VEC];
+    Raw<T> raw[GRAD_UNROLL];
+    fetch_row<Use::ONCE>(z, a.vocab, col0, THREADS * VEC, raw);
+    widen_row(raw, z, a.vocab, col0, THREADS * VEC, v);
+    const int seq = row / a.length;
+    const int pair = seq < a.pairs ? seq : seq - a.pairs;
+    const float margin = margins[pair];
+    float k = dlosses[pair] * a.beta *
+              (a.smoothing * sigmoid(margin) - (1.f - a.smoothing) * sigmoid(-margin));
+    if (seq >= a.pairs) k = -k;
+    const float l = lse[row];
+#pragma unroll
+    for (int j = 0; j < GRAD_UNROLL; ++j) {
       const int at = base + (j * THREADS + threadIdx.x) * VEC;
-      store8_upto(d + at, a.vocab - at, zero);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float p = exp_neg(v[j][e] - l);
+        v[j][e] = at + e == label ? k * (1.f - p) : -k * p;
+      }
+      store8_upto(d + at, a.vocab - at, v[j]);
     }
-    return;
-  }
-  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-  float v[UNROLL][VEC];
-#pragma unroll
-  for (int j = 0; j < UNROLL; ++j) {
-    const int at = base + (j * THREADS + threadIdx.x) * VEC;
-    if (whole) load8(z + at, v[j]);
-    else load8_upto(z + at, a.vocab - at, v[j]);
-  }
-  const int seq = static_cast<int>(blockIdx.x) / a.length;
-  const int pair = seq < a.pairs ? seq : seq - a.pairs;
-  const float margin = margins[pair];
-  float k = dlosses[pair] * a.beta *
-            (a.smoothing * sigmoid(margin) - (1.f - a.smoothing) * sigmoid(-margin));
-  if (seq >= a.pairs) k = -k;
-  const float l = lse[row];
-#pragma unroll
-  for (int j = 0; j < UNROLL; ++j) {
-    const int at = base + (j * THREADS + threadIdx.x) * VEC;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float p = exp_neg(v[j][e] - l);
-      v[j][e] = at + e == label ? k * (1.f - p) : -k * p;
-    }
-    if (whole) store8(d + at, v[j]);
-    else store8_upto(d + at, a.vocab - at, v[j]);
   }
 }
 
@@ -251,11 +299,12 @@ hipError_t launch_preference_grad(const PrefArgs& a, int type, bool labels64,
                                   void* dlogits, int64_t ld_dlogits, hipStream_t stream) {
   const int64_t rows = int64_t{2} * a.pairs * a.length;
   if (rows <= 0) return hipSuccess;
-  const dim3 grid(static_cast<unsigned>(rows), (a.vocab + STEP - 1) / STEP);
+  const int steps = (a.vocab + GRAD_STEP - 1) / GRAD_STEP;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(rows * steps, 1 << 23)));
   auto on = [&](auto t, auto i) {
     using T = decltype(t);
     hipLaunchKernelGGL((grad_kernel<T, decltype(i)>), grid, dim3(THREADS), 0, stream, a, margins,
-                       lse, dlosses, static_cast<T*>(dlogits), ld_dlogits);
+                       lse, dlosses, static_cast<T*>(dlogits), ld_dlogits, steps);
     return hipGetLastError();
   };
   return by_type(type, [&](auto t) { return labels64 ? on(t, int64_t{}) : on(t, int32_t{}); });

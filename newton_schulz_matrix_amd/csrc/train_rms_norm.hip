@@ -56,176 +56,311 @@ __device__ __forceinline__ uint2 to_e4m3(const float (&v)[VEC]) {
 constexpr float E4M3_MAX = 448.f;
 constexpr float SCALE_MIN = 0x1p-126f;   // its reciprocal is finite
 
-template <class T>
-__device__ __forceinline__ void load_weight(const RmsArgs& a, bool w32, int col, float (&w)[VEC]) {
-  if (w32) load8_upto(static_cast<const float*>(a.weight) + col, a.dim - col, w);
-  else load8_upto(static_cast<const T*>(a.weight) + col, a.dim - col, w);
+// What a kernel knows of the row width: a multiple of a vector, any other of
+// at least a vector, or less. Decided at compile time, so that no branch
+// stands between a row's loads and their uses.
+enum class Width { EVEN, RAGGED, NARROW };
+
+template <Width S, Use U, int V, class T>
+__device__ __forceinline__ void fetch_vecs(const T* row, int dim, int col, int stride,
+                                           Raw<T> (&raw)[V]) {
+  if constexpr (S == Width::NARROW) return;
+#pragma unroll
+  for (int j = 0; j < V; ++j) raw[j] = fetch_at<U>(row, dim, col + j * stride);
+}
+template <Width S, int V, class T>
+__device__ __forceinline__ void widen_vecs(const Raw<T> (&raw)[V], const T* row, int dim, int col,
+                                           int stride, float (&v)[V][VEC]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if constexpr (S == Width::EVEN) widen(raw[j], v[j]);
+    else if constexpr (S == Width::RAGGED) widen_ragged(raw[j], dim, col + j * stride, v[j]);
+    else widen_narrow(row, dim, col + j * stride, v[j]);
+  }
+}
+template <Width S, class T>
+__device__ __forceinline__ void store_vec(T* row, int dim, int col, const float (&v)[VEC]) {
+  if constexpr (S == Width::EVEN) {
+    if (col < dim) store8(row + col, v);
+  } else {
+    store8_upto(row + col, dim - col, v);
+  }
 }
 
-template <class T, class H, int TEAM, int V>
-__global__ __launch_bounds__(block_of(TEAM)) void rms_norm_kernel(RmsArgs a, int y_type, bool w32) {
-  constexpr int TEAMS = block_of(TEAM) / TEAM;
-  // the weights stay in registers over the rows of a workgroup where they fit
-  constexpr bool KEEP = V <= 4;
-  __shared__ float red_sum[2][block_of(TEAM) / 64], red_max[block_of(TEAM) / 64];
-  const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
-  float w[KEEP ? V : 1][VEC];
-  if (KEEP)
+// Eight columns (or those left of the row) that this thread stored itself.
+template <class T>
+__device__ __forceinline__ void widen_own(const T* row, int dim, int col, float (&v)[VEC]) {
+  if (col + VEC <= dim) {
+    load8(row + col, v);
+  } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) load_weight<T>(a, w32, (j * TEAM + t) * VEC, w[KEEP ? j : 0]);
-  int turn = 0;
-  for (int row = blockIdx.x * TEAMS + team; row < a.rows; row += gridDim.x * TEAMS, turn ^= 1) {
-    float v[V][VEC];
+    for (int e = 0; e < VEC; ++e) v[e] = col + e < dim ? static_cast<float>(row[col + e]) : 0.f;
+  }
+}
+
+// The weights of a thread's columns, of type T or fp32.
+template <Width S, class T, int V>
+__device__ __forceinline__ void load_weight(const void* weight, bool f32, int dim, int col,
+                                            int stride, float (&w)[V][VEC]) {
+  if (f32) {
+    Raw<float> r[V];
+    fetch_vecs<S, Use::AGAIN>(static_cast<const float*>(weight), dim, col, stride, r);
+    widen_vecs<S>(r, static_cast<const float*>(weight), dim, col, stride, w);
+  } else {
+    Raw<T> r[V];
+    fetch_vecs<S, Use::AGAIN>(static_cast<const T*>(weight), dim, col, stride, r);
+    widen_vecs<S>(r, static_cast<const T*>(weight), dim, col, stride, w);
+  }
+}
+
+// Eight columns of y: the values, or their codes.
+template <Width S>
+__device__ __forceinline__ void store_y(const RmsArgs& a, int y_type, int row, int col,
+                                        const float (&v)[VEC]) {
+  const int64_t at = row * a.ldy;
+  if (y_type == OUT_F32) {
+    store_vec<S>(static_cast<float*>(a.y) + at, a.dim, col, v);
+  } else if (y_type == OUT_BF16) {
+    store_vec<S>(static_cast<__bf16*>(a.y) + at, a.dim, col, v);
+  } else if (y_type == OUT_F16) {
+    store_vec<S>(static_cast<_Float16*>(a.y) + at, a.dim, col, v);
+  } else {
+    const uint2 q = to_e4m3(v);
+    uint8_t* y = static_cast<uint8_t*>(a.y) + at + col;
+    const int left = a.dim - col;
+    if (left >= VEC) {
+      __builtin_memcpy(y, &q, sizeof(q));
+    } else if constexpr (S != Width::EVEN) {
+      uint8_t b[VEC];
+      __builtin_memcpy(b, &q, sizeof(q));
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int col = (j * TEAM + t) * VEC;
-      load8_upto(static_cast<const T*>(a.x) + row * a.ldx + col, a.dim - col, v[j]);
+      for (int e = 0; e < VEC; ++e)
+        if (e < left) y[e] = b[e];
     }
+  }
+}
+
+// A row's scale for its largest |y|. Dividing by it makes that one 448, by
+// two roundings more at most, which still rounds to the code of 448: no clamp.
+__device__ __forceinline__ float scale_of(float top) {
+  return top > 0.f ? fmaxf(top / E4M3_MAX, SCALE_MIN) : 1.f;
+}
+
+// A workgroup goes round the rows (by teams) and has the next row's loads in
+// flight while it reduces and writes the present one; the weights stay in
+// registers where they fit.
+template <Width S, class T, class H, int TEAM, int V>
+__global__ __launch_bounds__(block_of(TEAM)) void rms_norm_kernel(RmsArgs a, int y_type, bool w32) {
+  constexpr int TEAMS = block_of(TEAM) / TEAM, STRIDE = TEAM * VEC;
+  constexpr bool KEEP = V <= 2;
+  __shared__ float red_sum[2][block_of(TEAM) / 64], red_max[block_of(TEAM) / 64];
+  const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM, col0 = t * VEC;
+  const int step = gridDim.x * TEAMS;
+  int row = blockIdx.x * TEAMS + team;
+  if (TEAM == 64 && row >= a.rows) return;   // (a workgroup of one team has a row)
+  auto x_of = [&](int r) { return static_cast<const T*>(a.x) + r * a.ldx; };
+  auto res_of = [&](int r) { return static_cast<const H*>(a.residual) + r * a.ld_residual; };
+  Raw<T> rx[V];
+  Raw<H> rr[V];
+  fetch_vecs<S, Use::ONCE>(x_of(row), a.dim, col0, STRIDE, rx);
+  if (a.residual) fetch_vecs<S, Use::ONCE>(res_of(row), a.dim, col0, STRIDE, rr);
+  float w[KEEP ? V : 1][VEC];
+  if (KEEP) load_weight<S, T>(a.weight, w32, a.dim, col0, STRIDE, w);
+  int turn = 0;
+  for (; row < a.rows; row += step, turn ^= 1) {
+    float v[V][VEC];
+    widen_vecs<S>(rx, x_of(row), a.dim, col0, STRIDE, v);
     if (a.residual) {
       float r[V][VEC];
+      widen_vecs<S>(rr, res_of(row), a.dim, col0, STRIDE, r);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int col = (j * TEAM + t) * VEC;
-        load8_upto(static_cast<const H*>(a.residual) + row * a.ld_residual + col, a.dim - col, r[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int col = (j * TEAM + t) * VEC;
+      for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[j][e] = rounded<H>(v[j][e] + r[j][e]);
-        store8_upto(static_cast<H*>(a.h) + row * a.ldh + col, a.dim - col, v[j]);
-      }
+    }
+    if (row + step < a.rows) {
+      fetch_vecs<S, Use::ONCE>(x_of(row + step), a.dim, col0, STRIDE, rx);
+      if (a.residual) fetch_vecs<S, Use::ONCE>(res_of(row + step), a.dim, col0, STRIDE, rr);
+    }
+    if (a.residual) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        store_vec<S>(static_cast<H*>(a.h) + row * a.ldh, a.dim, j * STRIDE + col0, v[j]);
     }
     float ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j) {
+      float part = 0.f;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) ss = fmaf(v[j][e], v[j][e], ss);
+      for (int e = 0; e < VEC; ++e) part = fmaf(v[j][e], v[j][e], part);
+      ss += (j * TEAM + t) * VEC < a.dim ? part : 0.f;
+    }
     const float rstd = 1.f / sqrtf(team_sum<TEAM>(ss, red_sum[turn]) / a.dim + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float late[VEC];
-      if (!KEEP) load_weight<T>(a, w32, (j * TEAM + t) * VEC, late);
+      float late[1][VEC];
+      if (!KEEP) load_weight<S, T>(a.weight, w32, a.dim, j * STRIDE + col0, 0, late);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[j][e] = v[j][e] * rstd * (KEEP ? w[KEEP ? j : 0][e] : late[e]);
+      for (int e = 0; e < VEC; ++e) v[j][e] = v[j][e] * rstd * (KEEP ? w[KEEP ? j : 0][e] : late[0][e]);
     }
     if (y_type == OUT_E4M3) {
       float top = 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j)
+      for (int j = 0; j < V; ++j) {
+        float part = 0.f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) top = fmaxf(top, fabsf(v[j][e]));
+        for (int e = 0; e < VEC; ++e) part = fmaxf(part, fabsf(v[j][e]));
+        top = fmaxf(top, (j * TEAM + t) * VEC < a.dim ? part : 0.f);
+      }
       top = team_max<TEAM>(top, red_max);
-      const float scale = top > 0.f ? fmaxf(top / E4M3_MAX, SCALE_MIN) : 1.f;
-      const float inv = 1.f / scale;
+      const float scale = scale_of(top), inv = 1.f / scale;
       if (t == 0) a.scales[row] = scale;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int col = (j * TEAM + t) * VEC, left = a.dim - col;
-        // no clamp: |v * inv| exceeds 448 by two roundings at most, which
-        // still rounds to the code of 448
+      for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[j][e] *= inv;
-        const uint2 q = to_e4m3(v[j]);
-        uint8_t* y = static_cast<uint8_t*>(a.y) + row * a.ldy + col;
-        if (left >= VEC) {
-          __builtin_memcpy(y, &q, sizeof(q));
-        } else {
-          uint8_t b[VEC];
-          __builtin_memcpy(b, &q, sizeof(q));
+    }
 #pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (e < left) y[e] = b[e];
-        }
-      }
-    } else {
+    for (int j = 0; j < V; ++j) store_y<S>(a, y_type, row, j * STRIDE + col0, v[j]);
+  }
+}
+
+// Rows too wide for the registers of a workgroup: the sum, the largest |y|
+// (for codes) and the output are passes over the row, the later ones from the
+// caches; with a residual they read back the h that the first one stored.
+constexpr int WIDE = 1024;
+template <class T, class H>
+__global__ __launch_bounds__(WIDE) void rms_norm_wide_kernel(RmsArgs a, int y_type, bool w32) {
+  constexpr Width S = Width::RAGGED;
+  __shared__ float red_sum[2][WIDE / 64], red_max[WIDE / 64];
+  const int step = WIDE * VEC;
+  int turn = 0;
+  for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const H* res = static_cast<const H*>(a.residual) + row * a.ld_residual;
+    H* h = static_cast<H*>(a.h) + row * a.ldh;
+    float ss = 0.f;
+    for (int col = threadIdx.x * VEC; col < a.dim; col += step) {
+      float v[1][VEC], r[1][VEC];
+      Raw<T> rx[1];
+      Raw<H> rr[1];
+      fetch_vecs<S, Use::AGAIN>(x, a.dim, col, 0, rx);
+      if (a.residual) fetch_vecs<S, Use::ONCE>(res, a.dim, col, 0, rr);
+      widen_vecs<S>(rx, x, a.dim, col, 0, v);
+      if (a.residual) {
+        widen_vecs<S>(rr, res, a.dim, col, 0, r);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int col = (j * TEAM + t) * VEC, left = a.dim - col;
-        const int64_t at = row * a.ldy + col;
-        if (y_type == OUT_F32) store8_upto(static_cast<float*>(a.y) + at, left, v[j]);
-        else if (y_type == OUT_BF16) store8_upto(static_cast<__bf16*>(a.y) + at, left, v[j]);
-        else store8_upto(static_cast<_Float16*>(a.y) + at, left, v[j]);
+        for (int e = 0; e < VEC; ++e) v[0][e] = rounded<H>(v[0][e] + r[0][e]);
+        store_vec<S>(h, a.dim, col, v[0]);
       }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) ss = fmaf(v[0][e], v[0][e], ss);
+    }
+    const float rstd = 1.f / sqrtf(team_sum<WIDE>(ss, red_sum[turn]) / a.dim + a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+    // y of eight columns, before any scale; a thread reads back only what it stored
+    auto y_of = [&](int col, float (&v)[1][VEC]) {
+      float w[1][VEC];
+      if (a.residual) {
+        // the vector that crosses the row's end would begin among the
+        // neighbouring thread's columns
+        widen_own(h, a.dim, col, v[0]);
+      } else {
+        Raw<T> rx[1];
+        fetch_vecs<S, Use::AGAIN>(x, a.dim, col, 0, rx);
+        widen_vecs<S>(rx, x, a.dim, col, 0, v);
+      }
+      load_weight<S, T>(a.weight, w32, a.dim, col, 0, w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[0][e] = v[0][e] * rstd * w[0][e];
+    };
+    float inv = 1.f;
+    if (y_type == OUT_E4M3) {
+      float top = 0.f;
+      for (int col = threadIdx.x * VEC; col < a.dim; col += step) {
+        float v[1][VEC];
+        y_of(col, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) top = fmaxf(top, fabsf(v[0][e]));
+      }
+      const float scale = scale_of(team_max<WIDE>(top, red_max));
+      if (threadIdx.x == 0) a.scales[row] = scale;
+      inv = 1.f / scale;
+    }
+    for (int col = threadIdx.x * VEC; col < a.dim; col += step) {
+      float v[1][VEC];
+      y_of(col, v);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[0][e] *= inv;
+      store_y<S>(a, y_type, row, col, v[0]);
     }
   }
 }
 
 // --------------------------------------------------------------- gradient
 
-struct GradRow {   // eight columns of one row
-  float g[VEC], u[VEC], dwu[VEC];
-};
-
-template <class T>
-__device__ __forceinline__ void load_weight(const RmsGradArgs& a, bool w32, int col,
-                                            float (&w)[VEC]) {
-  if (w32) load8_upto(static_cast<const float*>(a.weight) + col, a.dim - col, w);
-  else load8_upto(static_cast<const T*>(a.weight) + col, a.dim - col, w);
-}
-
-// dx of eight columns, with the gradient that comes past the norm.
-template <class T>
-__device__ __forceinline__ void store_dx(const RmsGradArgs& a, bool dx32, int row, int col,
-                                         float (&d)[VEC]) {
-  const int left = a.dim - col;
-  if (a.dh) {
-    float p[VEC];
-    const int64_t at = row * a.lddh + col;
-    if (dx32) load8_upto(static_cast<const float*>(a.dh) + at, left, p);
-    else load8_upto(static_cast<const T*>(a.dh) + at, left, p);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) d[e] += p[e];
-  }
-  const int64_t at = row * a.lddx + col;
-  if (dx32) store8_upto(static_cast<float*>(a.dx) + at, left, d);
-  else store8_upto(static_cast<T*>(a.dx) + at, left, d);
-}
-
 // A workgroup takes every gridDim.x-th row (by teams) and keeps its share of
 // dw in registers; the shares are added up by dweight_kernel.
-template <class T, class H, int TEAM, int V>
-__global__ __launch_bounds__(block_of(TEAM)) void rms_grad_kernel(RmsGradArgs a, bool w32,
-                                                                  bool dx32) {
-  constexpr int TEAMS = block_of(TEAM) / TEAM;
+template <Width S, class T, class H, class D, int TEAM, int V>
+__global__ __launch_bounds__(block_of(TEAM)) void rms_grad_kernel(RmsGradArgs a, bool w32) {
+  constexpr int TEAMS = block_of(TEAM) / TEAM, STRIDE = TEAM * VEC;
   __shared__ float red[2][block_of(TEAM) / 64];
   __shared__ float share[TEAMS > 1 ? TEAM * V * VEC : 1];
-  const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+  const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM, col0 = t * VEC;
+  const int step = gridDim.x * TEAMS;
+  auto dy_of = [&](int r) { return static_cast<const T*>(a.dy) + r * a.lddy; };
+  auto h_of = [&](int r) { return static_cast<const H*>(a.h) + r * a.ldh; };
+  auto past_of = [&](int r) { return static_cast<const D*>(a.dh) + r * a.lddh; };
+  Raw<T> rg[V];
+  Raw<H> ru[V];
+  Raw<D> rp[V];
+  float next_rstd = 0.f;
+  auto begin = [&](int r) {   // the loads of a row
+    next_rstd = a.rstd[r];
+    fetch_vecs<S, Use::ONCE>(dy_of(r), a.dim, col0, STRIDE, rg);
+    fetch_vecs<S, Use::ONCE>(h_of(r), a.dim, col0, STRIDE, ru);
+    if (a.dh) fetch_vecs<S, Use::ONCE>(past_of(r), a.dim, col0, STRIDE, rp);
+  };
+  int row = blockIdx.x * TEAMS + team;
+  if (row < a.rows) begin(row);
   float w[V][VEC], dw[V][VEC];
+  load_weight<S, T>(a.weight, w32, a.dim, col0, STRIDE, w);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    load_weight<T>(a, w32, (j * TEAM + t) * VEC, w[j]);
+  for (int j = 0; j < V; ++j)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[j][e] = 0.f;
-  }
   int turn = 0;
-  for (int row = blockIdx.x * TEAMS + team; row < a.rows; row += gridDim.x * TEAMS, turn ^= 1) {
-    float g[V][VEC], u[V][VEC];
-    const float rstd = a.rstd[row];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int col = (j * TEAM + t) * VEC;
-      load8_upto(static_cast<const T*>(a.dy) + row * a.lddy + col, a.dim - col, g[j]);
-      load8_upto(static_cast<const H*>(a.h) + row * a.ldh + col, a.dim - col, u[j]);
-    }
+  for (; row < a.rows; row += step, turn ^= 1) {
+    float g[V][VEC], u[V][VEC], past[V][VEC];
+    const float rstd = next_rstd;
+    widen_vecs<S>(rg, dy_of(row), a.dim, col0, STRIDE, g);
+    widen_vecs<S>(ru, h_of(row), a.dim, col0, STRIDE, u);
+    if (a.dh) widen_vecs<S>(rp, past_of(row), a.dim, col0, STRIDE, past);
+    if (row + step < a.rows) begin(row + step);
     float dot = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j) {
+      float part = 0.f;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         u[j][e] *= rstd;
         dw[j][e] = fmaf(g[j][e], u[j][e], dw[j][e]);
         g[j][e] *= w[j][e];
-        dot = fmaf(g[j][e], u[j][e], dot);
+        part = fmaf(g[j][e], u[j][e], part);
       }
+      dot += (j * TEAM + t) * VEC < a.dim ? part : 0.f;
+    }
     const float mean = team_sum<TEAM>(dot, red[turn]) / a.dim;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       float d[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) d[e] = rstd * fmaf(-u[j][e], mean, g[j][e]);
-      store_dx<T>(a, dx32, row, (j * TEAM + t) * VEC, d);
+      for (int e = 0; e < VEC; ++e) {
+        d[e] = rstd * fmaf(-u[j][e], mean, g[j][e]);
+        if (a.dh) d[e] += past[j][e];
+      }
+      store_vec<S>(static_cast<D*>(a.dx) + row * a.lddx, a.dim, j * STRIDE + col0, d);
     }
   }
   if (!a.dweight) return;
@@ -247,17 +382,16 @@ __global__ __launch_bounds__(block_of(TEAM)) void rms_grad_kernel(RmsGradArgs a,
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int col = (j * TEAM + t) * VEC;
-    store8_upto(out + col, a.dim - col, dw[j]);
+    store_vec<S>(out, a.dim, j * STRIDE + col0, dw[j]);
   }
 }
 
 // Rows too wide for the registers of a workgroup: two passes over each row
 // (the second from the caches), dw's share kept in the workgroup's own row
 // of `partial`, whose columns each belong to one thread.
-constexpr int WIDE = 1024;
-template <class T, class H>
-__global__ __launch_bounds__(WIDE) void rms_grad_wide_kernel(RmsGradArgs a, bool w32, bool dx32) {
+template <class T, class H, class D>
+__global__ __launch_bounds__(WIDE) void rms_grad_wide_kernel(RmsGradArgs a, bool w32) {
+  constexpr Width S = Width::RAGGED;
   __shared__ float red[2][WIDE / 64];
   float* out = a.partial + static_cast<int64_t>(blockIdx.x) * a.dim;
   const int step = WIDE * VEC;
@@ -265,31 +399,47 @@ __global__ __launch_bounds__(WIDE) void rms_grad_wide_kernel(RmsGradArgs a, bool
   for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
     const H* h = static_cast<const H*>(a.h) + row * a.ldh;
+    const D* dh = static_cast<const D*>(a.dh) + row * a.lddh;
     const float rstd = a.rstd[row];
     float dot = 0.f;
     for (int col = threadIdx.x * VEC; col < a.dim; col += step) {
-      float g[VEC], u[VEC], w[VEC];
-      load8_upto(dy + col, a.dim - col, g);
-      load8_upto(h + col, a.dim - col, u);
-      load_weight<T>(a, w32, col, w);
+      float g[1][VEC], u[1][VEC], w[1][VEC];
+      Raw<T> rg[1];
+      Raw<H> ru[1];
+      fetch_vecs<S, Use::AGAIN>(dy, a.dim, col, 0, rg);
+      fetch_vecs<S, Use::AGAIN>(h, a.dim, col, 0, ru);
+      load_weight<S, T>(a.weight, w32, a.dim, col, 0, w);
+      widen_vecs<S>(rg, dy, a.dim, col, 0, g);
+      widen_vecs<S>(ru, h, a.dim, col, 0, u);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) dot = fmaf(g[e] * w[e], u[e] * rstd, dot);
+      for (int e = 0; e < VEC; ++e) dot = fmaf(g[0][e] * w[0][e], u[0][e] * rstd, dot);
     }
     const float mean = team_sum<WIDE>(dot, red[turn]) / a.dim;
     for (int col = threadIdx.x * VEC; col < a.dim; col += step) {
-      float g[VEC], u[VEC], w[VEC], d[VEC], s[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      load8_upto(dy + col, a.dim - col, g);
-      load8_upto(h + col, a.dim - col, u);
-      load_weight<T>(a, w32, col, w);
-      if (a.dweight && row != static_cast<int>(blockIdx.x)) load8_upto(out + col, a.dim - col, s);
+      float g[1][VEC], u[1][VEC], w[1][VEC], past[1][VEC], s[1][VEC], d[VEC];
+      Raw<T> rg[1];
+      Raw<H> ru[1];
+      Raw<D> rp[1];
+      Raw<float> rs[1];
+      const bool more = a.dweight && row != static_cast<int>(blockIdx.x);
+      fetch_vecs<S, Use::AGAIN>(dy, a.dim, col, 0, rg);
+      fetch_vecs<S, Use::AGAIN>(h, a.dim, col, 0, ru);
+      if (a.dh) fetch_vecs<S, Use::ONCE>(dh, a.dim, col, 0, rp);
+      if (more) fetch_vecs<S, Use::AGAIN>(static_cast<const float*>(out), a.dim, col, 0, rs);
+      load_weight<S, T>(a.weight, w32, a.dim, col, 0, w);
+      widen_vecs<S>(rg, dy, a.dim, col, 0, g);
+      widen_vecs<S>(ru, h, a.dim, col, 0, u);
+      if (a.dh) widen_vecs<S>(rp, dh, a.dim, col, 0, past);
+      if (more) widen_vecs<S>(rs, static_cast<const float*>(out), a.dim, col, 0, s);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        u[e] *= rstd;
-        s[e] = fmaf(g[e], u[e], s[e]);
-        d[e] = rstd * fmaf(-u[e], mean, g[e] * w[e]);
+        u[0][e] *= rstd;
+        s[0][e] = fmaf(g[0][e], u[0][e], more ? s[0][e] : 0.f);
+        d[e] = rstd * fmaf(-u[0][e], mean, g[0][e] * w[0][e]);
+        if (a.dh) d[e] += past[0][e];
       }
-      if (a.dweight) store8_upto(out + col, a.dim - col, s);
-      store_dx<T>(a, dx32, row, col, d);
+      if (a.dweight) store_vec<S>(out, a.dim, col, s[0]);
+      store_vec<S>(static_cast<D*>(a.dx) + row * a.lddx, a.dim, col, d);
     }
   }
 }
@@ -316,46 +466,61 @@ __global__ __launch_bounds__(DW_COLS * DW_GROUPS) void dweight_kernel(const floa
   dweight[col] = static_cast<TO>(s);
 }
 
-// The team and vector count of a row width: calls f<TEAM, V>().
-template <class F>
+// Calls f(team, vectors, width) for a row width, each as a type. Rows of up
+// to 1024 columns are one wave's, wider ones, up to 8192, a workgroup's. The
+// forward kernel is fastest with two vectors a thread (16384 rows of 4096 in
+// 79 us; 84 with one, in a team twice as large), the gradient, which holds
+// five operands of each, with one (93 us; 101 with two).
+template <int FULL, class F>
 hipError_t by_width(int dim, F f) {
-  if (dim <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  if (dim <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-  if (dim <= 2048) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
-  if (dim <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  if (dim <= 8192) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
-  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  using std::integral_constant;
+  const integral_constant<int, 1> one;
+  const integral_constant<int, 2> two;
+  const integral_constant<int, FULL> full;
+  auto shaped = [&](auto team, auto v) {
+    if (dim % VEC == 0) return f(team, v, integral_constant<Width, Width::EVEN>{});
+    return f(team, v, integral_constant<Width, Width::RAGGED>{});
+  };
+  if (dim < VEC) return f(integral_constant<int, 64>{}, one, integral_constant<Width, Width::NARROW>{});
+  if (dim <= 64 * VEC) return shaped(integral_constant<int, 64>{}, one);
+  if (dim <= 128 * VEC) return shaped(integral_constant<int, 64>{}, two);
+  if (dim <= 256 * VEC) return shaped(integral_constant<int, 256>{}, one);
+  if (dim <= 512 * VEC) return shaped(integral_constant<int, 512 / FULL>{}, full);
+  return shaped(integral_constant<int, 1024 / FULL>{}, full);
 }
-constexpr int REGISTER_DIM = 1024 * 2 * VEC;   // widest row of by_width
 
-constexpr int MAX_BLOCKS = 1 << 16;   // of the forward kernel; further rows go round
+// Workgroups of a kernel: as many as the chip holds at a time; for the
+// gradient half of that, which halves what their shares of dw cost and leaves
+// the loads as they were (93 us instead of 95).
+constexpr int CHIP_THREADS = 256 * 2048;
 
 template <class T, class H>
 hipError_t rms_norm_on(const RmsArgs& a, int y_type, bool w32, hipStream_t stream) {
-  auto go = [&](auto team, auto v) {
+  auto go = [&](auto team, auto v, auto width) {
     constexpr int TEAM = team(), V = v(), TEAMS = block_of(TEAM) / TEAM;
-    const int blocks = std::min((a.rows + TEAMS - 1) / TEAMS, MAX_BLOCKS);
-    hipLaunchKernelGGL((rms_norm_kernel<T, H, TEAM, V>), dim3(blocks), dim3(block_of(TEAM)), 0,
+    constexpr Width S = width();
+    const int blocks = std::min((a.rows + TEAMS - 1) / TEAMS, CHIP_THREADS / block_of(TEAM));
+    hipLaunchKernelGGL((rms_norm_kernel<S, T, H, TEAM, V>), dim3(blocks), dim3(block_of(TEAM)), 0,
                        stream, a, y_type, w32);
     return hipGetLastError();
   };
-  if (a.dim <= REGISTER_DIM) return by_width(a.dim, go);
-  if (a.dim <= 2 * REGISTER_DIM)
-    return go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
-  return go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 8>{});
+  if (a.dim <= WIDE * VEC) return by_width<2>(a.dim, go);
+  hipLaunchKernelGGL((rms_norm_wide_kernel<T, H>), dim3(std::min(a.rows, CHIP_THREADS / WIDE)),
+                     dim3(WIDE), 0, stream, a, y_type, w32);
+  return hipGetLastError();
 }
 
-template <class T, class H>
-hipError_t rms_grad_on(const RmsGradArgs& a, bool w32, bool dx32, hipStream_t stream) {
-  if (a.dim > REGISTER_DIM) {
-    hipLaunchKernelGGL((rms_grad_wide_kernel<T, H>), dim3(a.blocks), dim3(WIDE), 0, stream, a, w32,
-                       dx32);
+template <class T, class H, class D>
+hipError_t rms_grad_on(const RmsGradArgs& a, bool w32, hipStream_t stream) {
+  if (a.dim > WIDE * VEC) {
+    hipLaunchKernelGGL((rms_grad_wide_kernel<T, H, D>), dim3(a.blocks), dim3(WIDE), 0, stream, a, w32);
     return hipGetLastError();
   }
-  return by_width(a.dim, [&](auto team, auto v) {
+  return by_width<1>(a.dim, [&](auto team, auto v, auto width) {
     constexpr int TEAM = team(), V = v();
-    hipLaunchKernelGGL((rms_grad_kernel<T, H, TEAM, V>), dim3(a.blocks), dim3(block_of(TEAM)), 0,
-                       stream, a, w32, dx32);
+    constexpr Width S = width();
+    hipLaunchKernelGGL((rms_grad_kernel<S, T, H, D, TEAM, V>), dim3(a.blocks),
+                       dim3(block_of(TEAM)), 0, stream, a, w32);
     return hipGetLastError();
   });
 }
@@ -380,16 +545,20 @@ hipError_t launch_rms_norm(const RmsArgs& a, int x_type, int h_type, int weight_
 }
 
 int rms_grad_blocks(int64_t rows, int64_t dim) {
-  const int teams = dim <= 2048 ? 4 : 1;
-  return static_cast<int>(std::min<int64_t>((rows + teams - 1) / teams, 1024));
+  const int64_t teams = dim <= 128 * VEC ? 4 : 1;
+  const int64_t threads = dim <= 256 * VEC ? 256 : dim <= 512 * VEC ? 512 : 1024;
+  return static_cast<int>(std::min<int64_t>((rows + teams - 1) / teams, CHIP_THREADS / 2 / threads));
 }
 
 hipError_t launch_rms_norm_grad(const RmsGradArgs& a, int dy_type, int h_type, int weight_type,
                                 int dx_type, int dweight_type, hipStream_t stream) {
   if (a.rows > 0) {
     const hipError_t e = by_types(dy_type, h_type, [&](auto t, auto h) {
-      return rms_grad_on<decltype(t), decltype(h)>(a, weight_type == OUT_F32, dx_type == OUT_F32,
-                                                   stream);
+      using T = decltype(t);
+      using H = decltype(h);
+      const bool w32 = weight_type == OUT_F32;
+      if (dx_type == dy_type) return rms_grad_on<T, H, T>(a, w32, stream);
+      return rms_grad_on<T, H, float>(a, w32, stream);
     });
     if (e != hipSuccess) return e;
   }

@@ -18,8 +18,10 @@ from __future__ import annotations
 import ctypes
 from typing import List, Optional, Sequence, Tuple
 
+import torch
+
 from . import (NS_DT_BF16, NS_DT_F16, NS_DT_F32, _check, _device_tensor, _dtype_code,
-               _stream_ptr, _torch, _workspace, library)
+               _workspace, library)
 
 NS_DT_E4M3 = 3
 NS_IDS_I32, NS_IDS_I64 = 0, 1
@@ -74,18 +76,37 @@ SIGNATURES = {
 }
 
 
+# Small calls take about as long as their launch: the helpers below run for
+# every tensor of a call and are written for few steps.
+
+_CODES = {torch.float32: NS_DT_F32, torch.bfloat16: NS_DT_BF16, torch.float16: NS_DT_F16}
+_ID_TYPES = {torch.int32: NS_IDS_I32, torch.int64: NS_IDS_I64}
+# the current stream of a device as a pointer, without a Stream object
+_stream_of = torch._C._cuda_getCurrentRawStream
+
+
+def _device_of(t, name: str) -> int:
+    """Index of the device of a call: the first tensor's, which must be the current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _device_tensor(t, name)   # says what is wrong
+    return dev
+
+
+def _code(t) -> int:
+    return _CODES[t.dtype] if t.dtype in _CODES else _dtype_code(t.dtype)
+
+
 def _ids_type(t, name: str) -> int:
-    torch = _torch()
-    if t.dtype == torch.int64:
-        return NS_IDS_I64
-    if t.dtype == torch.int32:
-        return NS_IDS_I32
-    raise TypeError(f"{name} must be int32 or int64, not {t.dtype}")
+    if t.dtype not in _ID_TYPES:
+        raise TypeError(f"{name} must be int32 or int64, not {t.dtype}")
+    return _ID_TYPES[t.dtype]
 
 
-def _rows_of(t, name: str) -> Tuple[int, int, int]:
-    """(rows, columns, leading dimension) of a tensor of rows on the current device."""
-    _device_tensor(t, name)
+def _rows_of(t, name: str, dev: int) -> Tuple[int, int, int]:
+    """(rows, columns, leading dimension) of a tensor of rows on device `dev`."""
+    if t.get_device() != dev:
+        _device_tensor(t, name)
     shape = t.shape
     if len(shape) == 0:
         raise ValueError(f"{name} must have at least one dimension")
@@ -115,24 +136,27 @@ def _rows_of(t, name: str) -> Tuple[int, int, int]:
     return rows, cols, ld
 
 
-def _like_rows(t, shape, name: str, dtype=None) -> int:
-    """Leading dimension of a tensor that must have this shape (and type)."""
-    if tuple(t.shape) != tuple(shape):
+def _mismatch(t, shape, name: str, dtype):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    return _rows_of(t, name)[2]
-
-
-def _dense(t, shape, name: str, dtype=None) -> int:
-    """Pointer of a dense tensor that must have this shape (and type)."""
     _device_tensor(t, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _like_rows(t, shape, name: str, dev: int, dtype=None) -> int:
+    """Leading dimension of a tensor that must have this shape (and type)."""
+    if t.shape != shape or (dtype is not None and t.dtype != dtype):
+        _mismatch(t, shape, name, dtype)
+    return _rows_of(t, name, dev)[2]
+
+
+def _dense(t, shape, name: str, dev: int, dtype=None) -> int:
+    """Pointer of a dense tensor that must have this shape (and type)."""
+    if (t.shape != shape or t.get_device() != dev or not t.is_contiguous()
+            or (dtype is not None and t.dtype != dtype)):
+        _mismatch(t, shape, name, dtype)
     return t.data_ptr()
 
 
@@ -153,22 +177,23 @@ def _given_or_new(workspace, nbytes: int, device):
 def ns_embedding(table, ids, scale: float = 1.0, out_dtype=None, out=None):
     """scale * table[ids], for ids (int32 or int64) of any shape; an id outside
     the table gives zeros. Returns a tensor of shape ids.shape + (dim,)."""
-    torch = _torch()
     if table.dim() != 2:
         raise ValueError("table must be 2-D")
-    rows, dim, ld = _rows_of(table, "table")
-    id_type = _ids_type(_device_tensor(ids, "ids"), "ids")
+    dev = _device_of(table, "table")
+    rows, dim, ld = _rows_of(table, "table", dev)
+    id_type = _ids_type(ids, "ids")
+    if ids.get_device() != dev:
+        _device_tensor(ids, "ids")
     ids = ids if ids.is_contiguous() else ids.contiguous()
-    shape = (*ids.shape, dim)
+    shape = ids.shape + (dim,)
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or table.dtype, device=table.device)
         ld_out = dim
     else:
-        ld_out = _like_rows(out, shape, "out", out_dtype)
-    _check(library().ns_embedding(table.data_ptr(), _dtype_code(table.dtype), rows, dim, ld,
-                                  ids.data_ptr(), id_type, ids.numel(), scale, out.data_ptr(),
-                                  _dtype_code(out.dtype), ld_out, _stream_ptr(table)),
-           "ns_embedding")
+        ld_out = _like_rows(out, shape, "out", dev, out_dtype)
+    _check(library().ns_embedding(table.data_ptr(), _code(table), rows, dim, ld, ids.data_ptr(),
+                                  id_type, ids.numel(), scale, out.data_ptr(), _code(out), ld_out,
+                                  _stream_of(dev)), "ns_embedding")
     return out
 
 
@@ -183,10 +208,12 @@ def ns_embedding_grad(grad_out, ids, rows: int, scale: float = 1.0,
     grad_out over the places that name each row. With accumulate it is added
     to out, which must then be given. ids outside the table and padding_idx
     contribute nothing."""
-    torch = _torch()
-    count, dim, ld = _rows_of(grad_out, "grad_out")
-    id_type = _ids_type(_device_tensor(ids, "ids"), "ids")
-    if tuple(ids.shape) != tuple(grad_out.shape[:-1]):
+    dev = _device_of(grad_out, "grad_out")
+    count, dim, ld = _rows_of(grad_out, "grad_out", dev)
+    id_type = _ids_type(ids, "ids")
+    if ids.get_device() != dev:
+        _device_tensor(ids, "ids")
+    if ids.shape != grad_out.shape[:-1]:
         raise ValueError(f"ids have shape {tuple(ids.shape)}, grad_out {tuple(grad_out.shape)}")
     if padding_idx is not None and not 0 <= padding_idx < rows:
         raise ValueError(f"padding_idx {padding_idx} is not a row of the table (0 to {rows - 1})")
@@ -197,45 +224,42 @@ def ns_embedding_grad(grad_out, ids, rows: int, scale: float = 1.0,
         out = torch.empty((rows, dim), dtype=out_dtype or grad_out.dtype, device=grad_out.device)
         ld_out = dim
     else:
-        ld_out = _like_rows(out, (rows, dim), "out", out_dtype)
+        ld_out = _like_rows(out, (rows, dim), "out", dev, out_dtype)
     workspace = _given_or_new(workspace, ns_embedding_grad_workspace_size(rows, dim, count),
                               grad_out.device)
     _check(library().ns_embedding_grad(
-        grad_out.data_ptr(), _dtype_code(grad_out.dtype), ld, ids.data_ptr(), id_type, count, rows,
-        dim, scale, -1 if padding_idx is None else padding_idx, 1 if accumulate else 0,
-        out.data_ptr(), _dtype_code(out.dtype), ld_out, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream_ptr(grad_out)), "ns_embedding_grad")
+        grad_out.data_ptr(), _code(grad_out), ld, ids.data_ptr(), id_type, count, rows, dim, scale,
+        -1 if padding_idx is None else padding_idx, 1 if accumulate else 0, out.data_ptr(),
+        _code(out), ld_out, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream_of(dev)), "ns_embedding_grad")
     return out
 
 
 # ------------------------------------------------------------------- RMS norm
 
-def _rms_norm(x, weight, residual, eps, y, y_code, scales, h):
-    torch = _torch()
-    rows, dim, ldx = _rows_of(x, "x")
-    args = _RmsNormArgs(x=x.data_ptr(), weight=_dense(weight, (dim,), "weight"), rows=rows, dim=dim,
-                        ldx=ldx, ldy=dim, eps=eps, y_dtype=y_code, y=y.data_ptr(),
-                        x_dtype=_dtype_code(x.dtype), weight_dtype=_dtype_code(weight.dtype))
-    args.h_dtype = args.x_dtype
+def _rms_norm(x, weight, residual, eps, y, y_code, scales, h, dev):
+    rows, dim, ldx = _rows_of(x, "x", dev)
+    code = h_code = _code(x)
+    res_ptr, h_ptr, ld_residual, ldh = None, None, 0, 0
     if residual is None:
         if h is not None:
             raise ValueError("h is written only with a residual")
         h = x
     else:
-        args.ld_residual = _like_rows(residual, x.shape, "residual")
-        args.residual = residual.data_ptr()
-        args.h_dtype = _dtype_code(residual.dtype)
+        ld_residual = _like_rows(residual, x.shape, "residual", dev)
+        res_ptr, h_code = residual.data_ptr(), _code(residual)
         if h is None:
             h = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
-            args.ldh = dim
+            ldh = dim
         else:
-            args.ldh = _like_rows(h, x.shape, "h", residual.dtype)
-        args.h = h.data_ptr()
+            ldh = _like_rows(h, x.shape, "h", dev, residual.dtype)
+        h_ptr = h.data_ptr()
     rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    args.rstd = rstd.data_ptr()
-    if scales is not None:
-        args.scales = scales.data_ptr()
-    _check(library().ns_rms_norm(ctypes.byref(args), _stream_ptr(x)), "ns_rms_norm")
+    args = _RmsNormArgs(x.data_ptr(), res_ptr, h_ptr, _dense(weight, (dim,), "weight", dev),
+                        y.data_ptr(), scales.data_ptr() if scales is not None else None,
+                        rstd.data_ptr(), rows, dim, ldx, ld_residual, ldh, dim, code, h_code,
+                        _code(weight), y_code, eps)
+    _check(library().ns_rms_norm(args, _stream_of(dev)), "ns_rms_norm")
     return h, rstd
 
 
@@ -246,21 +270,19 @@ def ns_rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, h=N
     (fp32), both for ns_rms_norm_grad. The residual may be x's type or fp32;
     the sum has its type, and `h` may name its buffer (the residual's own, or
     x's where the types agree)."""
-    torch = _torch()
-    _device_tensor(x, "x")
+    dev = _device_of(x, "x")
     y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    h, rstd = _rms_norm(x, weight, residual, eps, y, _dtype_code(y.dtype), None, h)
+    h, rstd = _rms_norm(x, weight, residual, eps, y, _code(y), None, h, dev)
     return y, h, rstd
 
 
 def ns_rms_norm_fp8(x, weight, residual=None, eps: float = 1e-6, h=None):
     """ns_rms_norm with the output as e4m3 codes and one fp32 scale for each
     row (y is code * scale). Returns (codes, scales, h, rstd)."""
-    torch = _torch()
-    _device_tensor(x, "x")
+    dev = _device_of(x, "x")
     q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    h, rstd = _rms_norm(x, weight, residual, eps, q, NS_DT_E4M3, scales, h)
+    h, rstd = _rms_norm(x, weight, residual, eps, q, NS_DT_E4M3, scales, h, dev)
     return q, scales, h, rstd
 
 
@@ -274,43 +296,42 @@ def ns_rms_norm_grad(dy, h, weight, rstd, dh=None, dx=None, dx_dtype=None, dweig
     dx is the gradient of x and of the residual. `h` and `rstd` are the norm's
     own; dh is the gradient that reaches h past the norm, of dx's type (dx may
     be its buffer). dweight has weight's type unless dweight_dtype says so."""
-    torch = _torch()
-    rows, dim, lddy = _rows_of(dy, "dy")
+    dev = _device_of(dy, "dy")
+    rows, dim, lddy = _rows_of(dy, "dy", dev)
+    shape = dy.shape
     if dx is None:
-        dx = torch.empty(dy.shape, dtype=dx_dtype or (dh.dtype if dh is not None else dy.dtype),
+        dx = torch.empty(shape, dtype=dx_dtype or (dh.dtype if dh is not None else dy.dtype),
                          device=dy.device)
         lddx = dim
     else:
-        lddx = _like_rows(dx, dy.shape, "dx", dx_dtype)
+        lddx = _like_rows(dx, shape, "dx", dev, dx_dtype)
+    dh_ptr, lddh = None, 0
+    if dh is not None:
+        dh_ptr, lddh = dh.data_ptr(), _like_rows(dh, shape, "dh", dev, dx.dtype)
     dweight = torch.empty(dim, dtype=dweight_dtype or weight.dtype, device=dy.device)
     args = _RmsNormGradArgs(
-        dy=dy.data_ptr(), h=h.data_ptr(), weight=_dense(weight, (dim,), "weight"),
-        rstd=_dense(rstd, dy.shape[:-1], "rstd", torch.float32), dx=dx.data_ptr(),
-        dweight=dweight.data_ptr(), rows=rows, dim=dim, lddy=lddy,
-        ldh=_like_rows(h, dy.shape, "h"), lddx=lddx, dy_dtype=_dtype_code(dy.dtype),
-        h_dtype=_dtype_code(h.dtype), weight_dtype=_dtype_code(weight.dtype),
-        dx_dtype=_dtype_code(dx.dtype), dweight_dtype=_dtype_code(dweight.dtype))
-    if dh is not None:
-        args.lddh = _like_rows(dh, dy.shape, "dh", dx.dtype)
-        args.dh = dh.data_ptr()
+        dy.data_ptr(), h.data_ptr(), _dense(weight, (dim,), "weight", dev),
+        _dense(rstd, shape[:-1], "rstd", dev, torch.float32), dh_ptr, dx.data_ptr(),
+        dweight.data_ptr(), rows, dim, lddy, _like_rows(h, shape, "h", dev), lddh, lddx, _code(dy),
+        _code(h), _code(weight), _code(dx), _code(dweight))
     workspace = _given_or_new(workspace, ns_rms_norm_grad_workspace_size(rows, dim), dy.device)
-    _check(library().ns_rms_norm_grad(ctypes.byref(args), workspace.data_ptr(),
+    _check(library().ns_rms_norm_grad(args, workspace.data_ptr(),
                                       workspace.numel() * workspace.element_size(),
-                                      _stream_ptr(dy)), "ns_rms_norm_grad")
+                                      _stream_of(dev)), "ns_rms_norm_grad")
     return dx, dweight
 
 
 # ------------------------------------------------------------ preference loss
 
-def _preference_args(logits, labels, beta, label_smoothing):
-    if logits.dim() != 3 or logits.shape[0] % 2:
+def _preference_args(logits, labels, beta, label_smoothing, dev):
+    shape = logits.shape
+    if len(shape) != 3 or shape[0] % 2:
         raise ValueError("logits must be (2 * pairs, length, vocab): the preferred sequences, then "
                          "the others")
-    _, vocab, ld = _rows_of(logits, "logits")
-    label_type = _ids_type(labels, "labels")
-    return _PreferenceArgs(logits.data_ptr(), _dense(labels, logits.shape[:2], "labels"),
-                           logits.shape[0] // 2, logits.shape[1], vocab, max(ld, vocab),
-                           _dtype_code(logits.dtype), label_type, beta, label_smoothing)
+    _, vocab, ld = _rows_of(logits, "logits", dev)
+    return _PreferenceArgs(logits.data_ptr(), _dense(labels, shape[:2], "labels", dev), shape[0] // 2,
+                           shape[1], vocab, ld, _code(logits), _ids_type(labels, "labels"), beta,
+                           label_smoothing)
 
 
 def ns_preference_loss_workspace_size(pairs: int, length: int, vocab: int) -> int:
@@ -326,18 +347,18 @@ def ns_preference_loss(logits, labels, ref_logps, beta: float = 0.1, label_smoot
     (losses, margins, logps, lse): the loss and margin of each pair, the
     policy's log probability of each sequence, and each position's log sum of
     exponentials, which the gradient needs."""
-    torch = _torch()
-    args = _preference_args(logits, labels, beta, label_smoothing)
-    pairs, length, dev = args.pairs, args.length, logits.device
-    ref = _dense(ref_logps, (2 * pairs,), "ref_logps", torch.float32)
-    out = torch.empty(2 * pairs * (length + 2), dtype=torch.float32, device=dev)
-    losses, margins, logps, lse = out.split([pairs, pairs, 2 * pairs, 2 * pairs * length])
+    dev = _device_of(logits, "logits")
+    args = _preference_args(logits, labels, beta, label_smoothing, dev)
+    pairs, length, device = args.pairs, args.length, logits.device
+    ref = _dense(ref_logps, (2 * pairs,), "ref_logps", dev, torch.float32)
+    out = torch.empty(2 * pairs * (length + 2), dtype=torch.float32, device=device)
+    losses, margins, logps, lse = out.split((pairs, pairs, 2 * pairs, 2 * pairs * length))
     workspace = _given_or_new(workspace,
-                              ns_preference_loss_workspace_size(pairs, length, args.vocab), dev)
+                              ns_preference_loss_workspace_size(pairs, length, args.vocab), device)
+    at = out.data_ptr()
     _check(library().ns_preference_loss(
-        ctypes.byref(args), ref, losses.data_ptr(), margins.data_ptr(), logps.data_ptr(),
-        lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream_ptr(logits)), "ns_preference_loss")
+        args, ref, at, at + 4 * pairs, at + 8 * pairs, at + 16 * pairs, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_of(dev)), "ns_preference_loss")
     return losses, margins, logps, lse.view(2 * pairs, length)
 
 
@@ -346,19 +367,19 @@ def ns_preference_loss_grad(logits, labels, margins, lse, dlosses, beta: float =
     """Gradient of ns_preference_loss's losses with respect to the logits, for
     margins and lse as it returned them and the gradient of each loss, dlosses
     (pairs, fp32). `out` may be the logits themselves."""
-    torch = _torch()
-    args = _preference_args(logits, labels, beta, label_smoothing)
-    pairs = args.pairs
+    dev = _device_of(logits, "logits")
+    args = _preference_args(logits, labels, beta, label_smoothing, dev)
+    pairs, shape = args.pairs, logits.shape
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = torch.empty(shape, dtype=logits.dtype, device=logits.device)
         ld_out = args.vocab
     else:
-        ld_out = _like_rows(out, logits.shape, "out", logits.dtype)
+        ld_out = _like_rows(out, shape, "out", dev, logits.dtype)
     _check(library().ns_preference_loss_grad(
-        ctypes.byref(args), _dense(margins, (pairs,), "margins", torch.float32),
-        _dense(lse, logits.shape[:2], "lse", torch.float32),
-        _dense(dlosses, (pairs,), "dlosses", torch.float32), out.data_ptr(), max(ld_out, args.vocab),
-        _stream_ptr(logits)), "ns_preference_loss_grad")
+        args, _dense(margins, (pairs,), "margins", dev, torch.float32),
+        _dense(lse, shape[:2], "lse", dev, torch.float32),
+        _dense(dlosses, (pairs,), "dlosses", dev, torch.float32), out.data_ptr(), ld_out,
+        _stream_of(dev)), "ns_preference_loss_grad")
     return out
 
 
@@ -376,24 +397,28 @@ def ns_adamw_step(params: List, grads: List, exp_avgs: List, exp_avg_sqs: List, 
     count = len(params)
     if count == 0:
         return
-    weight_decays = [0.0] * count if weight_decays is None else list(weight_decays)
-    masters = [None] * count if masters is None else list(masters)
+    weight_decays = [0.0] * count if weight_decays is None else weight_decays
+    masters = [None] * count if masters is None else masters
     if not (len(grads) == len(exp_avgs) == len(exp_avg_sqs) == len(weight_decays) == len(masters)
             == count):
         raise ValueError("params, grads, exp_avgs, exp_avg_sqs, weight_decays and masters must have "
                          "the same length")
-    torch = _torch()
-    tensors = (_AdamwTensor * count)()
-    for i, (p, g, m, v, w) in enumerate(zip(params, grads, exp_avgs, exp_avg_sqs, masters)):
-        shape = p.shape
-        tensors[i] = _AdamwTensor(
-            _dense(p, shape, f"param {i}"), _dense(g, shape, f"grad {i}"),
-            _dense(m, shape, f"exp_avg {i}"), _dense(v, shape, f"exp_avg_sq {i}"),
-            _dense(w, shape, f"master {i}", torch.float32) if w is not None else None, p.numel(),
-            _dtype_code(p.dtype), _dtype_code(g.dtype), _dtype_code(m.dtype), _dtype_code(v.dtype),
-            weight_decays[i])
+    dev = _device_of(params[0], "param 0")
+    shapes = [p.shape for p in params]
+    columns = []
+    for name, group in (("param", params), ("grad", grads), ("exp_avg", exp_avgs),
+                        ("exp_avg_sq", exp_avg_sqs)):
+        for t, shape in zip(group, shapes):
+            if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+                _mismatch(t, shape, name, None)
+        columns.append([t.data_ptr() for t in group])
+    columns.append([None if w is None else _dense(w, shape, "master", dev, torch.float32)
+                    for w, shape in zip(masters, shapes)])
+    columns.append([p.numel() for p in params])
+    columns += [[_code(t) for t in group] for group in (params, grads, exp_avgs, exp_avg_sqs)]
+    tensors = (_AdamwTensor * count)(*zip(*columns, weight_decays))
     _check(library().ns_adamw_step(tensors, count, step, lr, betas[0], betas[1], eps,
-                                   _stream_ptr(params[0])), "ns_adamw_step")
+                                   _stream_of(dev)), "ns_adamw_step")
 
 
 __all__ = ["NS_DT_E4M3", "NS_IDS_I32", "NS_IDS_I64", "NS_MAX_ROWS", "ns_embedding",
