@@ -47,7 +47,10 @@ __device__ __forceinline__ void store_lane(T* p, const float (&v)[LANE]) {
   T b[LANE];
 #pragma unroll
   for (int e = 0; e < LANE; ++e) b[e] = static_cast<T>(v[e]);
-  __builtin_memcpy(p, b, sizeof(b));
+  typedef uint32_t Word __attribute__((ext_vector_type(sizeof(b) / 4), aligned(2)));
+  Word w;
+  __builtin_memcpy(&w, b, sizeof(b));
+  __builtin_nontemporal_store(w, reinterpret_cast<Word*>(p));
 }
 __device__ __forceinline__ void store_as(void* p, int type, int64_t at, const float (&v)[LANE]) {
   if (type == OUT_F32) store_lane(static_cast<float*>(p) + at, v);

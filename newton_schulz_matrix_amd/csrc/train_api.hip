@@ -112,7 +112,7 @@ EmbedGradPlan embed_grad_plan(int64_t rows, int64_t dim, int64_t count) {
   p.sorted = 0;
   p.start = align_up(sizeof(int2) * static_cast<size_t>(count));
   p.partial = align_up(p.start + sizeof(int) * (static_cast<size_t>(p.sort.slots) + 1));
-  p.total = align_up(p.partial + sizeof(float) * static_cast<size_t>(p.sort.windows) * dim);
+  p.total = align_up(p.partial + sizeof(float) * 2 * static_cast<size_t>(p.sort.windows) * dim);
   return p;
 }
 }  // namespace

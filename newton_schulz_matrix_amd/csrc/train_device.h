@@ -53,12 +53,18 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[VEC]) {
   widen(fetch(p), v);
 }
 
+// Stored as vectors by type: written as a copy of eight elements, it would be
+// taken apart and merged with the element stores of store8_upto below, into
+// two-byte and twelve-byte stores at two thirds of the rate.
 template <class T>
 __device__ __forceinline__ void store8(T* p, const float (&v)[VEC]) {
   T r[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) r[e] = static_cast<T>(v[e]);
-  __builtin_memcpy(p, r, sizeof(r));
+  Quad q[sizeof(r) / 16];
+  __builtin_memcpy(q, r, sizeof(r));
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) reinterpret_cast<Quad*>(p)[i] = q[i];
 }
 
 // The eight columns at `at` of a row of `dim`, in two steps. The vector that

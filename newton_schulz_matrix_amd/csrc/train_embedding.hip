@@ -8,12 +8,13 @@
 // the other threads of a workgroup take further rows, so narrow tables fill
 // the lanes too.
 //
-// The gradient is three launches: one sorts the ids; one sums whole windows of
-// the sorted places that belong to one id (the few ids that a large share of
-// the places name) and, in further workgroups, clears the table; one adds up
-// each id's run and writes its row. The rows that some id names are written
-// twice: a clearing workgroup that first looked up whether its row is named
-// would wait for that longer than the row's zeros take.
+// The gradient is three launches. One sorts the ids. One sums, in windows of
+// the sorted places, what belongs to runs (the places of one id) that cross a
+// window's border, and, in further workgroups, clears the table. One adds up
+// each run, from its terms or from its windows' sums, and writes its row. The
+// rows that some id names are written twice: a clearing workgroup that first
+// looked up whether its row is named would wait for that longer than the
+// row's zeros take.
 #include <algorithm>
 
 #include "train_device.h"
@@ -23,7 +24,7 @@ namespace nsmi {
 namespace {
 
 // Eight columns of R rows of a table, all in flight together (row numbers must
-// be valid); then as fp32, zeros for a row that is not `used`.
+// be valid).
 template <int R, class T>
 __device__ __forceinline__ void fetch_rows(const T* table, int64_t ld, const int (&rows)[R],
                                            int dim, int col, Raw<T> (&raw)[R]) {
@@ -31,26 +32,6 @@ __device__ __forceinline__ void fetch_rows(const T* table, int64_t ld, const int
 #pragma unroll
   for (int r = 0; r < R; ++r) raw[r] = fetch_at(table + rows[r] * ld, dim, col);
 }
-template <int R, class T>
-__device__ __forceinline__ void widen_rows(const Raw<T> (&raw)[R], const T* table, int64_t ld,
-                                           const int (&rows)[R], const bool (&used)[R], int dim,
-                                           int col, float (&v)[R][VEC]) {
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    widen_at(raw[r], table + rows[r] * ld, dim, col, v[r]);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[r][e] = used[r] ? v[r][e] : 0.f;
-  }
-}
-template <int R, class T>
-__device__ __forceinline__ void gather(const T* table, int64_t ld, const int (&rows)[R],
-                                       const bool (&used)[R], int dim, int col,
-                                       float (&v)[R][VEC]) {
-  Raw<T> raw[R];
-  fetch_rows(table, ld, rows, dim, col, raw);
-  widen_rows(raw, table, ld, rows, used, dim, col, v);
-}
-
 // ---------------------------------------------------------------- lookup
 
 template <class TI, class TO, class I, int R>
@@ -70,15 +51,18 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int tx_log2
     used[r] = id[r] >= 0 && id[r] < a.rows;
     row[r] = used[r] ? static_cast<int>(id[r]) : 0;
   }
-  float v[R][VEC];
-  gather(static_cast<const TI*>(a.table), a.ld_table, row, used, a.dim, col, v);
+  const TI* table = static_cast<const TI*>(a.table);
+  Raw<TI> raw[R];
+  fetch_rows(table, a.ld_table, row, a.dim, col, raw);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int i = first + r * teams;
     if (i >= a.count) break;
+    float v[VEC];
+    widen_at(raw[r], table + row[r] * a.ld_table, a.dim, col, v);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[r][e] *= a.scale;
-    store8_upto(static_cast<TO*>(a.out) + i * a.ld_out + col, a.dim - col, v[r]);
+    for (int e = 0; e < VEC; ++e) v[e] = used[r] ? v[e] * a.scale : 0.f;
+    store8_upto(static_cast<TO*>(a.out) + i * a.ld_out + col, a.dim - col, v);
   }
 }
 
@@ -199,26 +183,32 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(EmbedGradArgs a) {
 // --------------------------------------------------------------- gradient
 
 // Adds rows of `from`, at index(k) for k in [k0, k1), to sum, in order. A
-// batch's rows are in flight together; the places past k1 in the last batch
-// repeat its last row (which is then at hand) and do not count.
+// batch's rows are in flight together, the next batch's indices with them;
+// the places past k1 in the last batch repeat its last row (which is then at
+// hand) and do not count.
 template <class T, class F>
 __device__ __forceinline__ void add_rows(const T* from, int64_t ld, int dim, int col, int k0, int k1,
                                          F index, float (&sum)[VEC]) {
   constexpr int U = 8;
+  int next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) next[u] = k0 < k1 ? index(min(k0 + u, k1 - 1)) : 0;
   for (int k = k0; k < k1; k += U) {
     int row[U];
-    bool used[U];
-    float v[U][VEC];
+    Raw<T> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) row[u] = next[u];
+    fetch_rows(from, ld, row, dim, col, raw);
+    if (k + U < k1)
+#pragma unroll
+      for (int u = 0; u < U; ++u) next[u] = index(min(k + U + u, k1 - 1));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      used[u] = k + u < k1;
-      row[u] = index(min(k + u, k1 - 1));
+      float v[VEC];
+      widen_at(raw[u], from + row[u] * ld, dim, col, v);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum[e] += k + u < k1 ? v[e] : 0.f;
     }
-    gather(from, ld, row, used, dim, col, v);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) sum[e] += v[u][e];
   }
 }
 
@@ -252,11 +242,14 @@ __device__ __forceinline__ void clear_rows(T* table, int64_t ld, const Clear& c,
   }
 }
 
-// The first `summing` workgroups: sums of the windows of `window` sorted
-// places that name one id altogether, so that an id that a large share of the
-// places name is summed by many workgroups. Other windows are left alone. The
-// others clear the table in the order of the addresses: 1 GB is written at
-// 5.8 to 6.7 TB/s so, at 5.4 by fewer workgroups that go round.
+// The first `summing` workgroups take a window of the sorted places each (by
+// teams) and sum what in it belongs to a run that came in from the window
+// before (row 2 w of `partial`) and to one that begins here and goes on in the
+// window after (row 2 w + 1). A run is then the sum of its windows' rows: an id
+// that a tenth of the places name is summed by many workgroups, with no serial
+// remainder. The other workgroups clear the table in the order of the
+// addresses: 1 GB is written at 5.8 to 6.7 TB/s so, at 5.4 by fewer
+// workgroups that go round.
 template <class T, class TO>
 __global__ __launch_bounds__(256) void window_clear_kernel(EmbedGradArgs a, int tx_log2,
                                                            unsigned summing, Clear clear) {
@@ -270,31 +263,29 @@ __global__ __launch_bounds__(256) void window_clear_kernel(EmbedGradArgs a, int 
   const int w = static_cast<int>(blockIdx.x / across) * teams + ty;
   const int col = (static_cast<int>(blockIdx.x % across) * (1 << tx_log2) + tx) * VEC;
   if (col >= a.dim || w >= a.sort.windows) return;
-  const int from = w * a.sort.window, to = from + a.sort.window;
-  const int id = a.sorted[from].y;
-  if (id < 0 || id != a.sorted[to - 1].y) return;
-  float sum[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  add_terms<T>(a, from, to, col, sum);
-  store8_upto(a.partial + static_cast<int64_t>(w) * a.dim + col, a.dim - col, sum);
-}
-
-// Adds the places [k, end) of one id: the terms up to the first whole window,
-// the whole windows' sums, the terms after the last.
-template <class T>
-__device__ __forceinline__ void add_run(const EmbedGradArgs& a, int k, int end, int col,
-                                        float (&sum)[VEC]) {
-  const int S = a.sort.window, w0 = (k + S - 1) / S, w1 = end / S;
-  const bool windows = w0 < w1;
-  add_terms<T>(a, k, windows ? w0 * S : end, col, sum);
-  if (windows) {
-    add_rows(a.partial, a.dim, a.dim, col, w0, w1, [](int w) { return w; }, sum);
-    add_terms<T>(a, w1 * S, end, col, sum);
+  const int from = w * a.sort.window, to = min(from + a.sort.window, a.count);
+  const int head = a.sorted[from].y, tail = a.sorted[to - 1].y;
+  const int before = from > 0 ? a.sorted[from - 1].y : -1;
+  const int after = to < a.count ? a.sorted[to].y : -1;
+  float* out = a.partial + static_cast<int64_t>(2 * w) * a.dim + col;
+  int rest = from;   // first place behind the run that came in
+  if (head >= 0 && head == before) {
+    rest = min(to, a.start[sorted_slot(head, a.sort) + 1]);
+    float sum[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    add_terms<T>(a, from, rest, col, sum);
+    store8_upto(out, a.dim - col, sum);
+  }
+  if (tail >= 0 && tail == after && rest < to) {
+    float sum[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    add_terms<T>(a, max(from, a.start[sorted_slot(tail, a.sort)]), to, col, sum);
+    store8_upto(out + a.dim, a.dim - col, sum);
   }
 }
 
 // A team takes PLACES sorted places and the runs (places of one id) that
-// begin there: all its rows are read at once and summed run by run; a run
-// that goes on past the team's places is followed to its end.
+// begin there: all its rows are read at once and summed run by run. A run that
+// goes on past the team's places is followed to its end, if that lies in the
+// same window, and otherwise taken from its windows' sums.
 template <class T, class TO, bool ADD>
 __global__ __launch_bounds__(256) void runs_kernel(EmbedGradArgs a, int tx_log2) {
   constexpr int PLACES = ADD || sizeof(T) == 4 ? 4 : 8;
@@ -324,12 +315,11 @@ __global__ __launch_bounds__(256) void runs_kernel(EmbedGradArgs a, int tx_log2)
   }
   if (!any) return;
   const T* from = static_cast<const T*>(a.grad_out);
-  float v[PLACES][VEC], old[ADD ? PLACES : 1][VEC];
+  const TO* into = static_cast<const TO*>(a.grad);
   Raw<T> raw[PLACES];
+  Raw<TO> old[PLACES];
   fetch_rows(from, a.ld_grad_out, row, a.dim, col, raw);
-  if constexpr (ADD)
-    gather(static_cast<const TO*>(a.grad), a.ld_grad, head, heads, a.dim, col, old);
-  widen_rows(raw, from, a.ld_grad_out, row, used, a.dim, col, v);
+  if constexpr (ADD) fetch_rows(into, a.ld_grad, head, a.dim, col, old);
   float sum[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, base[VEC];
   auto write = [&](int which) {
     float out[VEC];
@@ -339,17 +329,32 @@ __global__ __launch_bounds__(256) void runs_kernel(EmbedGradArgs a, int tx_log2)
   };
 #pragma unroll
   for (int u = 0; u < PLACES; ++u) {
+    float v[VEC];
+    widen_at(raw[u], from + row[u] * a.ld_grad_out, a.dim, col, v);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      sum[i] = heads[u] ? v[u][i] : sum[i] + v[u][i];
-      if constexpr (ADD) base[i] = heads[u] ? old[u][i] : base[i];
+    for (int i = 0; i < VEC; ++i) sum[i] = heads[u] ? v[i] : sum[i] + v[i];
+    if constexpr (ADD) {
+      float o[VEC];
+      widen_at(old[u], into + head[u] * a.ld_grad, a.dim, col, o);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) base[i] = heads[u] ? o[i] : base[i];
     }
     if (u + 1 < PLACES && used[u] && id[u + 1] != id[u]) write(id[u]);
   }
   const int open = id[PLACES - 1];
   if (!used[PLACES - 1]) return;
-  if (after == open)
-    add_run<T>(a, first + PLACES, a.start[sorted_slot(open, a.sort) + 1], col, sum);
+  if (after == open) {
+    const int S = a.sort.window, w = first / S;
+    const int end = a.start[sorted_slot(open, a.sort) + 1];
+    if (end <= (w + 1) * S) {
+      add_terms<T>(a, first + PLACES, end, col, sum);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) sum[i] = 0.f;
+      add_rows(a.partial, a.dim, a.dim, col, w, (end - 1) / S + 1,
+               [&](int k) { return k == w ? 2 * w + 1 : 2 * k; }, sum);
+    }
+  }
   write(open);
 }
 
@@ -398,11 +403,11 @@ EmbedSort embed_sort_plan(int64_t rows, int64_t count) {
   while (s.groups_log2 > 0 && (int64_t{1} << s.groups_log2) > rows) --s.groups_log2;
   s.range = static_cast<int>(((rows - 1) >> s.groups_log2) + 1);
   s.slots = s.range << s.groups_log2;
-  // a row of c terms takes up to 2 window + c / window steps; the most frequent
+  // a run of c places takes up to window + c / window steps; the most frequent
   // token of a text is about every tenth
   s.window = 16;
   while (16 * int64_t{s.window} * s.window < count) s.window *= 2;
-  s.windows = static_cast<int>(count / s.window);
+  s.windows = static_cast<int>((count + s.window - 1) / s.window);
   return s;
 }
 

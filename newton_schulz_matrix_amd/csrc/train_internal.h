@@ -43,8 +43,8 @@ struct EmbedSort {
   int groups_log2;     // groups = 1 << groups_log2
   int range;           // slots of a group
   int slots;           // groups * range >= rows
-  int window;          // terms of one precomputed partial sum
-  int windows;         // count / window
+  int window;          // places of one window (a multiple of 8)
+  int windows;
 };
 __host__ __device__ inline int sorted_slot(int v, const EmbedSort& s) {
   return (v & ((1 << s.groups_log2) - 1)) * s.range + (v >> s.groups_log2);
@@ -57,7 +57,7 @@ struct EmbedGradArgs {
   void* grad;
   int2* sorted;
   int* start;
-  float* partial;      // (windows, dim)
+  float* partial;      // (2 windows, dim)
   int64_t ld_grad_out, ld_grad;
   int64_t padding_id;
   int rows, count, dim;
