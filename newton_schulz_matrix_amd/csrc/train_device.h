@@ -56,7 +56,9 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[VEC]) {
 // Stored as vectors by type: written as a copy of eight elements, it would be
 // taken apart and merged with the element stores of store8_upto below, into
 // two-byte and twelve-byte stores at two thirds of the rate.
-template <class T>
+// With ONCE the stores are non-temporal: for large outputs that this call does
+// not read back.
+template <Use U = Use::AGAIN, class T>
 __device__ __forceinline__ void store8(T* p, const float (&v)[VEC]) {
   T r[VEC];
 #pragma unroll
@@ -64,7 +66,11 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[VEC]) {
   Quad q[sizeof(r) / 16];
   __builtin_memcpy(q, r, sizeof(r));
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) reinterpret_cast<Quad*>(p)[i] = q[i];
+  for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) {
+    Quad* to = reinterpret_cast<Quad*>(p) + i;
+    if constexpr (U == Use::ONCE) __builtin_nontemporal_store(q[i], to);
+    else *to = q[i];
+  }
 }
 
 // The eight columns at `at` of a row of `dim`, in two steps. The vector that
@@ -121,10 +127,10 @@ __device__ __forceinline__ void widen_row(const Raw<T> (&raw)[V], const T* row, 
   for (int j = 0; j < V; ++j) widen_at(raw[j], row, dim, col + j * stride, v[j]);
 }
 
-template <class T>
+template <Use U = Use::AGAIN, class T>
 __device__ __forceinline__ void store8_upto(T* p, int left, const float (&v)[VEC]) {
   if (left >= VEC) {
-    store8(p, v);
+    store8<U>(p, v);
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e)

@@ -62,7 +62,9 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int tx_log2
     widen_at(raw[r], table + row[r] * a.ld_table, a.dim, col, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] = used[r] ? v[e] * a.scale : 0.f;
-    store8_upto(static_cast<TO*>(a.out) + i * a.ld_out + col, a.dim - col, v);
+    // a large output (R > 1) does not stay in the L2 caches anyway
+    store8_upto<R == 1 ? Use::AGAIN : Use::ONCE>(static_cast<TO*>(a.out) + i * a.ld_out + col,
+                                                 a.dim - col, v);
   }
 }
 
@@ -236,7 +238,7 @@ __device__ __forceinline__ void clear_rows(T* table, int64_t ld, const Clear& c,
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t col = from + (j * 256 + threadIdx.x) * VEC;
-      if (col + VEC <= c.cols) store8(table + row * ld + col, zero);
+      if (col + VEC <= c.cols) store8<Use::ONCE>(table + row * ld + col, zero);
       else if (col < c.cols) store8_upto(table + row * ld + col, static_cast<int>(c.cols - col), zero);
     }
   }
@@ -325,7 +327,7 @@ __global__ __launch_bounds__(256) void runs_kernel(EmbedGradArgs a, int tx_log2)
     float out[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) out[i] = fmaf(a.scale, sum[i], ADD ? base[i] : 0.f);
-    store8_upto(static_cast<TO*>(a.grad) + which * a.ld_grad + col, left, out);
+    store8_upto<Use::ONCE>(static_cast<TO*>(a.grad) + which * a.ld_grad + col, left, out);
   };
 #pragma unroll
   for (int u = 0; u < PLACES; ++u) {

@@ -19,7 +19,7 @@ namespace nsmi {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int UNROLL = 4;                           // vectors of a thread in flight
+constexpr int UNROLL = 8;                           // vectors of a thread in flight
 constexpr int STEP = THREADS * VEC * UNROLL;        // elements of a workgroup's step
 constexpr float FAR = 150.f;                        // exp(-FAR) is 0 in fp32
 
@@ -113,7 +113,7 @@ __global__ __launch_bounds__(THREADS) void pieces_kernel(PrefArgs a, PrefSplit s
     float v[UNROLL][VEC];
     Raw<T> raw[UNROLL];
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j) raw[j] = fetch<Use::ONCE>(z + base + j * THREADS * VEC + col0);
+    for (int j = 0; j < UNROLL; ++j) raw[j] = fetch(z + base + j * THREADS * VEC + col0);
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j) widen(raw[j], v[j]);
     take<T>(v, m, s);
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(THREADS) void pieces_kernel(PrefArgs a, PrefSplit s
   if (base < end) {
     float v[UNROLL][VEC];
     Raw<T> raw[UNROLL];
-    fetch_row<Use::ONCE>(z, end, base + col0, THREADS * VEC, raw);
+    fetch_row(z, end, base + col0, THREADS * VEC, raw);
     widen_row(raw, z, end, base + col0, THREADS * VEC, v);
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j)
@@ -213,7 +213,7 @@ __device__ __forceinline__ float sigmoid(float x) {
 }
 
 // Workgroups take GRAD_STEP elements each, in the order of the addresses.
-constexpr int GRAD_UNROLL = 4;
+constexpr int GRAD_UNROLL = 8;
 constexpr int GRAD_STEP = THREADS * VEC * GRAD_UNROLL;
 template <class T, class I>
 __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* margins,
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* 
 #pragma unroll
       for (int j = 0; j < GRAD_UNROLL; ++j) {
         const int at = base + (j * THREADS + threadIdx.x) * VEC;
-        store8_upto(d + at, a.vocab - at, zero);
+        store8_upto<Use::ONCE>(d + at, a.vocab - at, zero);
       }
       continue;
     }
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* 
         const float p = exp_neg(v[j][e] - l);
         v[j][e] = at + e == label ? k * (1.f - p) : -k * p;
       }
-      store8_upto(d + at, a.vocab - at, v[j]);
+      store8_upto<Use::ONCE>(d + at, a.vocab - at, v[j]);
     }
   }
 }
