@@ -88,6 +88,7 @@ template <class T>
 __device__ __forceinline__ void widen_ragged(const Raw<T>& raw, int dim, int at, float (&v)[VEC]) {
   widen(raw, v);
   const int past = max(at + VEC - dim, 0);
+  if (!__any(past > 0 && past < VEC)) return;   // most waves have no vector that crosses
 #pragma unroll
   for (int by = VEC / 2; by >= 1; by /= 2)
 #pragma unroll

@@ -78,12 +78,12 @@ __device__ __forceinline__ void widen_vecs(const Raw<T> (&raw)[V], const T* row,
     else widen_narrow(row, dim, col + j * stride, v[j]);
   }
 }
-template <Width S, class T>
+template <Width S, Use U = Use::AGAIN, class T>
 __device__ __forceinline__ void store_vec(T* row, int dim, int col, const float (&v)[VEC]) {
   if constexpr (S == Width::EVEN) {
-    if (col < dim) store8(row + col, v);
+    if (col < dim) store8<U>(row + col, v);
   } else {
-    store8_upto(row + col, dim - col, v);
+    store8_upto<U>(row + col, dim - col, v);
   }
 }
 
@@ -95,6 +95,18 @@ __device__ __forceinline__ void widen_own(const T* row, int dim, int col, float 
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] = col + e < dim ? static_cast<float>(row[col + e]) : 0.f;
+  }
+}
+
+// The two are kept apart: merged, as the compiler would, they lose the hint.
+template <Width S, class T>
+__device__ __forceinline__ void store_either(bool once, T* row, int dim, int col,
+                                             const float (&v)[VEC]) {
+  if (once) {
+    store_vec<S, Use::ONCE>(row, dim, col, v);
+    asm volatile("" ::: "memory");
+  } else {
+    store_vec<S>(row, dim, col, v);
   }
 }
 
@@ -121,9 +133,9 @@ __device__ __forceinline__ void store_y(const RmsArgs& a, int y_type, int row, i
   if (y_type == OUT_F32) {
     store_vec<S>(static_cast<float*>(a.y) + at, a.dim, col, v);
   } else if (y_type == OUT_BF16) {
-    store_vec<S>(static_cast<__bf16*>(a.y) + at, a.dim, col, v);
+    store_either<S>(a.stream, static_cast<__bf16*>(a.y) + at, a.dim, col, v);
   } else if (y_type == OUT_F16) {
-    store_vec<S>(static_cast<_Float16*>(a.y) + at, a.dim, col, v);
+    store_either<S>(a.stream, static_cast<_Float16*>(a.y) + at, a.dim, col, v);
   } else {
     const uint2 q = to_e4m3(v);
     uint8_t* y = static_cast<uint8_t*>(a.y) + at + col;
@@ -184,8 +196,10 @@ __global__ __launch_bounds__(block_of(TEAM)) void rms_norm_kernel(RmsArgs a, int
     }
     if (a.residual) {
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        store_vec<S>(static_cast<H*>(a.h) + row * a.ldh, a.dim, j * STRIDE + col0, v[j]);
+      for (int j = 0; j < V; ++j) {
+        H* h = static_cast<H*>(a.h) + row * a.ldh;
+        store_either<S>(a.stream && y_type == OUT_E4M3, h, a.dim, j * STRIDE + col0, v[j]);
+      }
     }
     float ss = 0.f;
 #pragma unroll
@@ -486,6 +500,7 @@ hipError_t by_width(int dim, F f) {
   if (dim <= 128 * VEC) return shaped(integral_constant<int, 64>{}, two);
   if (dim <= 256 * VEC) return shaped(integral_constant<int, 256>{}, one);
   if (dim <= 512 * VEC) return shaped(integral_constant<int, 512 / FULL>{}, full);
+  if (dim <= 768 * VEC) return shaped(integral_constant<int, 768 / FULL>{}, full);
   return shaped(integral_constant<int, 1024 / FULL>{}, full);
 }
 
@@ -536,9 +551,17 @@ hipError_t by_types(int type, int h_type, F f) {
 
 }  // namespace
 
-hipError_t launch_rms_norm(const RmsArgs& a, int x_type, int h_type, int weight_type, int y_type,
+// Elements from which on a call with a residual stores one of its two outputs
+// non-temporally, a 16-bit y or, beside e4m3 codes, h: two large outputs push
+// the inputs and each other through the caches. 16384 rows of 4096 in bf16
+// take 83 us so (both non-temporal 98, none 101), with codes 78 (none 92).
+// Without a residual it costs (49 us instead of 45).
+constexpr int64_t STREAM_ELEMS = int64_t{1} << 23;
+
+hipError_t launch_rms_norm(RmsArgs a, int x_type, int h_type, int weight_type, int y_type,
                            hipStream_t stream) {
   if (a.rows <= 0) return hipSuccess;
+  a.stream = a.residual && static_cast<int64_t>(a.rows) * a.dim >= STREAM_ELEMS;
   return by_types(x_type, h_type, [&](auto t, auto h) {
     return rms_norm_on<decltype(t), decltype(h)>(a, y_type, weight_type == OUT_F32, stream);
   });
@@ -546,7 +569,8 @@ hipError_t launch_rms_norm(const RmsArgs& a, int x_type, int h_type, int weight_
 
 int rms_grad_blocks(int64_t rows, int64_t dim) {
   const int64_t teams = dim <= 128 * VEC ? 4 : 1;
-  const int64_t threads = dim <= 256 * VEC ? 256 : dim <= 512 * VEC ? 512 : 1024;
+  const int64_t threads = dim <= 256 * VEC ? 256 : dim <= 512 * VEC ? 512
+                          : dim <= 768 * VEC ? 768 : 1024;
   return static_cast<int>(std::min<int64_t>((rows + teams - 1) / teams, CHIP_THREADS / 2 / threads));
 }
 
