@@ -100,9 +100,13 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(EmbedGradArgs a) {
   const int begin = min(a.count, wave * per), end = min(a.count, begin + per);
   // id at position i, -1 where it does not count (no branch before the load:
   // a batch's loads are in flight together)
+  const uint32_t rows = a.rows, padding = a.padding_id >= 0 && a.padding_id < a.rows
+                                              ? static_cast<uint32_t>(a.padding_id) : rows;
   auto id_at = [&](int i) -> int {
     const int64_t id = static_cast<int64_t>(ids[min(i, end - 1)]);
-    return i < end && id >= 0 && id < a.rows && id != a.padding_id ? static_cast<int>(id) : -1;
+    const uint32_t low = static_cast<uint32_t>(id);   // all of an id that counts
+    const bool high = static_cast<uint32_t>(static_cast<uint64_t>(id) >> 32) != 0;
+    return i < end && !high && low < rows && low != padding ? static_cast<int>(low) : -1;
   };
 
   int below = 0;

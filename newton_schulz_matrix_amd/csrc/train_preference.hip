@@ -18,9 +18,12 @@
 namespace nsmi {
 namespace {
 
-constexpr int THREADS = 256;
+// A workgroup is one wave for short vocabularies, else four: loss and gradient
+// of 32000 rows of 1001 take 57 us with the one, 116 with the four, which the
+// long rows need.
 constexpr int UNROLL = 8;                           // vectors of a thread in flight
-constexpr int STEP = THREADS * VEC * UNROLL;        // elements of a workgroup's step
+constexpr int SHORT_VOCAB = 64 * VEC * UNROLL / 2;
+constexpr int step_of(int threads) { return threads * VEC * UNROLL; }   // elements of a step
 constexpr float FAR = 150.f;                        // exp(-FAR) is 0 in fp32
 
 // exp(x) by the hardware's 2^x. The product with log2(e) carries the
@@ -69,11 +72,11 @@ __device__ __forceinline__ float factor(float m, float base) {
 // maximum and rescales its sum once a step; the threads' sums are brought to
 // the piece's maximum once, at the end, and added in 64 bits, so that a row's
 // sum carries one rounding where a sequence adds up hundreds of rows.
-template <class T>
-__device__ __forceinline__ void take(const float (&v)[UNROLL][VEC], float& m, float& s) {
+template <int U>
+__device__ __forceinline__ void take(const float (&v)[U][VEC], float& m, float& s) {
   float top = m, low = INFINITY;
 #pragma unroll
-  for (int j = 0; j < UNROLL; ++j)
+  for (int j = 0; j < U; ++j)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       top = fmaxf(top, v[j][e]);
@@ -83,7 +86,7 @@ __device__ __forceinline__ void take(const float (&v)[UNROLL][VEC], float& m, fl
   float add = 0.f;
   if (__any(low - base < -FAR)) {   // -inf - (-inf) in the correction: terms this far off are 0
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j)
+    for (int j = 0; j < U; ++j)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float x = v[j][e] - base;
@@ -91,15 +94,16 @@ __device__ __forceinline__ void take(const float (&v)[UNROLL][VEC], float& m, fl
       }
   } else {
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j)
+    for (int j = 0; j < U; ++j)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) add += exp_exact(v[j][e] - base);
   }
   s = fmaf(s, factor(m, base), add);
   m = top;
 }
-template <class T, class I>
+template <class T, class I, int THREADS>
 __global__ __launch_bounds__(THREADS) void pieces_kernel(PrefArgs a, PrefSplit sp, float2* parts) {
+  constexpr int STEP = step_of(THREADS);
   __shared__ float red_m[THREADS / 64];
   __shared__ double red_s[THREADS / 64];
   const int64_t row = blockIdx.x;
@@ -116,19 +120,25 @@ __global__ __launch_bounds__(THREADS) void pieces_kernel(PrefArgs a, PrefSplit s
     for (int j = 0; j < UNROLL; ++j) raw[j] = fetch(z + base + j * THREADS * VEC + col0);
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j) widen(raw[j], v[j]);
-    take<T>(v, m, s);
+    take(v, m, s);
   }
-  if (base < end) {
-    float v[UNROLL][VEC];
+  if (base < end) {   // the vectors left, all in flight, then one after the other
     Raw<T> raw[UNROLL];
-    fetch_row(z, end, base + col0, THREADS * VEC, raw);
-    widen_row(raw, z, end, base + col0, THREADS * VEC, v);
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j)
+    for (int j = 0; j < UNROLL; ++j) {
+      const int at = base + j * THREADS * VEC;
+      if (at < end && end >= VEC) raw[j] = fetch_at(z, end, at + col0);
+    }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        v[j][e] = base + j * THREADS * VEC + col0 + e < end ? v[j][e] : -INFINITY;
-    take<T>(v, m, s);
+    for (int j = 0; j < UNROLL; ++j) {
+      const int at = base + j * THREADS * VEC;
+      if (at >= end) break;
+      float v[1][VEC];
+      widen_at(raw[j], z, end, at + col0, v[0]);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[0][e] = at + col0 + e < end ? v[0][e] : -INFINITY;
+      take(v, m, s);
+    }
   }
   const int wave = threadIdx.x >> 6;
   const float wave_top = wave_max(m);
@@ -212,34 +222,35 @@ __device__ __forceinline__ float sigmoid(float x) {
   return x >= 0.f ? 1.f / (1.f + e) : e / (1.f + e);
 }
 
-// Workgroups take GRAD_STEP elements each, in the order of the addresses.
-constexpr int GRAD_UNROLL = 8;
-constexpr int GRAD_STEP = THREADS * VEC * GRAD_UNROLL;
-template <class T, class I>
+// Workgroups take a step each, in the order of the addresses.
+template <class T, class I, int THREADS>
 __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* margins,
                                                        const float* lse, const float* dlosses,
                                                        T* dlogits, int64_t ld_dlogits, int steps) {
   const int64_t all = int64_t{2} * a.pairs * a.length * steps;
   for (int64_t block = blockIdx.x; block < all; block += gridDim.x) {
     const int row = static_cast<int>(block / steps);
-    const int base = static_cast<int>(block - static_cast<int64_t>(row) * steps) * GRAD_STEP;
+    const int base = static_cast<int>(block - static_cast<int64_t>(row) * steps) * step_of(THREADS);
     const int64_t label = label_at<I>(a, row);
     T* d = dlogits + row * ld_dlogits;
+    const int col0 = static_cast<int>(threadIdx.x) * VEC;
     if (!counted(a, label)) {
       const float zero[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < GRAD_UNROLL; ++j) {
-        const int at = base + (j * THREADS + threadIdx.x) * VEC;
-        store8_upto<Use::ONCE>(d + at, a.vocab - at, zero);
+      for (int j = 0; j < UNROLL; ++j) {
+        const int at = base + j * THREADS * VEC;
+        if (at >= a.vocab) break;
+        store8_upto<Use::ONCE>(d + at + col0, a.vocab - at - col0, zero);
       }
       continue;
     }
-    const int col0 = base + static_cast<int>(threadIdx.x) * VEC;
     const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-    float v[GRAD_UNROLL][VEC];
-    Raw<T> raw[GRAD_UNROLL];
-    fetch_row<Use::ONCE>(z, a.vocab, col0, THREADS * VEC, raw);
-    widen_row(raw, z, a.vocab, col0, THREADS * VEC, v);
+    Raw<T> raw[UNROLL];
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j) {
+      const int at = base + j * THREADS * VEC;
+      if (at < a.vocab && a.vocab >= VEC) raw[j] = fetch_at<Use::ONCE>(z, a.vocab, at + col0);
+    }
     const int seq = row / a.length;
     const int pair = seq < a.pairs ? seq : seq - a.pairs;
     const float margin = margins[pair];
@@ -248,14 +259,17 @@ __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* 
     if (seq >= a.pairs) k = -k;
     const float l = lse[row];
 #pragma unroll
-    for (int j = 0; j < GRAD_UNROLL; ++j) {
-      const int at = base + (j * THREADS + threadIdx.x) * VEC;
+    for (int j = 0; j < UNROLL; ++j) {
+      const int at = base + j * THREADS * VEC;
+      if (at >= a.vocab) break;
+      float v[VEC];
+      widen_at(raw[j], z, a.vocab, at + col0, v);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float p = exp_neg(v[j][e] - l);
-        v[j][e] = at + e == label ? k * (1.f - p) : -k * p;
+        const float p = exp_neg(v[e] - l);
+        v[e] = at + col0 + e == label ? k * (1.f - p) : -k * p;
       }
-      store8_upto<Use::ONCE>(d + at, a.vocab - at, v[j]);
+      store8_upto<Use::ONCE>(d + at + col0, a.vocab - at - col0, v);
     }
   }
 }
@@ -264,6 +278,7 @@ __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* 
 
 PrefSplit pref_split(int64_t rows, int64_t vocab) {
   // pieces of at least one step; as many as give every CU a few workgroups
+  const int STEP = step_of(vocab <= SHORT_VOCAB ? 64 : 256);
   const int64_t steps = (vocab + STEP - 1) / STEP;
   const int64_t want = rows > 0 ? std::max<int64_t>(1, 2048 / rows) : 1;
   const int64_t pieces = std::min(steps, want);
@@ -282,8 +297,11 @@ hipError_t launch_preference_loss(const PrefArgs& a, int type, bool labels64, co
     using T = decltype(t);
     using I = decltype(i);
     if (rows > 0) {
-      hipLaunchKernelGGL((pieces_kernel<T, I>), dim3(static_cast<unsigned>(rows), sp.pieces),
-                         dim3(THREADS), 0, stream, a, sp, parts);
+      const dim3 grid(static_cast<unsigned>(rows), sp.pieces);
+      if (a.vocab <= SHORT_VOCAB)
+        hipLaunchKernelGGL((pieces_kernel<T, I, 64>), grid, dim3(64), 0, stream, a, sp, parts);
+      else
+        hipLaunchKernelGGL((pieces_kernel<T, I, 256>), grid, dim3(256), 0, stream, a, sp, parts);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
@@ -299,12 +317,18 @@ hipError_t launch_preference_grad(const PrefArgs& a, int type, bool labels64,
                                   void* dlogits, int64_t ld_dlogits, hipStream_t stream) {
   const int64_t rows = int64_t{2} * a.pairs * a.length;
   if (rows <= 0) return hipSuccess;
-  const int steps = (a.vocab + GRAD_STEP - 1) / GRAD_STEP;
+  const int threads = a.vocab <= SHORT_VOCAB ? 64 : 256, step = step_of(threads);
+  const int steps = (a.vocab + step - 1) / step;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(rows * steps, 1 << 23)));
   auto on = [&](auto t, auto i) {
     using T = decltype(t);
-    hipLaunchKernelGGL((grad_kernel<T, decltype(i)>), grid, dim3(THREADS), 0, stream, a, margins,
-                       lse, dlosses, static_cast<T*>(dlogits), ld_dlogits, steps);
+    using I = decltype(i);
+    if (threads == 64)
+      hipLaunchKernelGGL((grad_kernel<T, I, 64>), grid, dim3(64), 0, stream, a, margins, lse,
+                         dlosses, static_cast<T*>(dlogits), ld_dlogits, steps);
+    else
+      hipLaunchKernelGGL((grad_kernel<T, I, 256>), grid, dim3(256), 0, stream, a, margins, lse,
+                         dlosses, static_cast<T*>(dlogits), ld_dlogits, steps);
     return hipGetLastError();
   };
   return by_type(type, [&](auto t) { return labels64 ? on(t, int64_t{}) : on(t, int32_t{}); });
