@@ -439,7 +439,7 @@ ns_status ns_preference_loss_grad(const ns_preference_args* args, const float* m
  * The update uses m and v before they are rounded to their storage types. w
  * is `master` (fp32) where that is given, and param then receives w rounded
  * to its type (param is not read); otherwise w is param.
- *   Each buffer is dense with `elems` elements (0 is allowed); param, grad,
+ *   Each buffer is dense with `elems` elements (0 to 2^33); param, grad,
  *   exp_avg any type, exp_avg_sq fp32 or bf16 (fp16 cannot hold the square
  *   of a small gradient and is refused), master fp32 or NULL. Buffers of
  *   different tensors must not overlap either (the caller's to avoid).

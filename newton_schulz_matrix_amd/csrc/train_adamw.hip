@@ -23,7 +23,7 @@ constexpr int BLOCK_ELEMS = THREADS * LANE;
 // LANE elements as loaded, in 16 or 8 bytes; each is read once in a call.
 typedef uint32_t Words __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ Words load_raw(const void* p, int type, int64_t at) {
-  typedef uint32_t Pair __attribute__((ext_vector_type(2), aligned(2)));
+  typedef uint32_t Pair __attribute__((ext_vector_type(2), aligned(2), may_alias));
   if (type == OUT_F32)
     return __builtin_nontemporal_load(reinterpret_cast<const Quad*>(static_cast<const float*>(p) + at));
   const Pair h =
@@ -47,7 +47,7 @@ __device__ __forceinline__ void store_lane(T* p, const float (&v)[LANE]) {
   T b[LANE];
 #pragma unroll
   for (int e = 0; e < LANE; ++e) b[e] = static_cast<T>(v[e]);
-  typedef uint32_t Word __attribute__((ext_vector_type(sizeof(b) / 4), aligned(2)));
+  typedef uint32_t Word __attribute__((ext_vector_type(sizeof(b) / 4), aligned(2), may_alias));
   Word w;
   __builtin_memcpy(&w, b, sizeof(b));
   __builtin_nontemporal_store(w, reinterpret_cast<Word*>(p));

@@ -399,7 +399,7 @@ NS_API ns_status ns_preference_loss_grad(const ns_preference_args* p, const floa
 
 namespace nsmi {
 namespace {
-constexpr int64_t ADAMW_MAX_ELEMS = int64_t{1} << 35;   // of one tensor
+constexpr int64_t ADAMW_MAX_ELEMS = int64_t{1} << 33;   // of one tensor: ADAMW_MAX_BLOCKS of it
 constexpr unsigned ADAMW_MAX_BLOCKS = 1u << 23;         // of one launch
 
 ns_status check_adamw(const ns_adamw_tensor& t) {

@@ -22,7 +22,8 @@ enum class Use { AGAIN, ONCE };
 // Eight elements of type T as loaded. Loading and converting are separate
 // steps, so that a kernel can have all the loads of several operands in
 // flight before the first conversion waits for one.
-typedef uint32_t Quad __attribute__((ext_vector_type(4), aligned(2)));   // at any element
+// (any element's address; other types' memory)
+typedef uint32_t Quad __attribute__((ext_vector_type(4), aligned(2), may_alias));
 template <class T>
 struct Raw {
   Quad q[sizeof(T) * VEC / 16];

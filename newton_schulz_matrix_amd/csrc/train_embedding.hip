@@ -173,12 +173,12 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(EmbedGradArgs a) {
       uint64_t todo = __ballot(own);
       while (todo) {   // one distinct id at a time; few share a group
         const int leader = __ffsll(static_cast<unsigned long long>(todo)) - 1;
-        const int which = __shfl(id[u], leader, 64);
+        const int which = __builtin_amdgcn_readlane(id[u], leader);   // (leader is uniform)
         const bool same = own && id[u] == which;
         const uint64_t peers = __ballot(same);
         int first = 0;
         if (lane == leader) first = atomicAdd(&mine[which >> gl], __popcll(peers));
-        first = __shfl(first, leader, 64);
+        first = __builtin_amdgcn_readlane(first, leader);
         if (same) a.sorted[first + __popcll(peers & before)] = make_int2(base + u * 64 + lane, which);
         todo &= ~peers;
       }

@@ -113,7 +113,7 @@ def test_rows_of_zeros_infinities_and_nan():
 
 def test_norm_in_place_of_the_residual_and_of_x():
     require_gpu()
-    for dim in (96, 1000, 5000):
+    for dim in (5, 96, 1000, 4099, 5000, 20001):
         x, res, w = normal(1, (9, dim), BF), normal(2, (9, dim), BF), normal(3, (dim,), BF)
         y, h, rstd = nsmi.ns_rms_norm(x, w, residual=res)
         for target in ("res", "x"):

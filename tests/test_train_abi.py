@@ -200,7 +200,7 @@ def test_adamw_refusals():
     for kw in (dict(count=-1), dict(step=0), dict(step=-3), dict(lr=-0.1), dict(lr=nan), dict(lr=inf),
                dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=nan), dict(eps=-1e-9),
                dict(eps=inf), dict(param=None), dict(grad=None), dict(exp_avg=None),
-               dict(exp_avg_sq=None), dict(elems=-1), dict(elems=1 << 36), dict(param_dtype=3),
+               dict(exp_avg_sq=None), dict(elems=-1), dict(elems=(1 << 33) + 1), dict(param_dtype=3),
                dict(grad_dtype=4), dict(exp_avg_dtype=-1), dict(exp_avg_sq_dtype=F16),
                dict(weight_decay=-0.1), dict(weight_decay=nan), dict(param=P[0] + 1),
                dict(exp_avg=P[2] + 2), dict(master=P[4] + 2), dict(grad=P[0]), dict(exp_avg=P[3] + 400),
