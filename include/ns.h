@@ -398,7 +398,9 @@ ns_status ns_rms_norm_grad(const ns_rms_norm_grad_args* args, void* ws, size_t w
  * A position counts if its label lies in [0, vocab); logits of other
  * positions are not read, and their lse is 0. Sums over a sequence are
  * taken in 64 bits.
- *   logits   (2 * pairs * length, vocab): row s * length + t, ld >= vocab;
+ *   logits   (2 * pairs, length, vocab): positions ld >= vocab elements apart,
+ *            sequences ld_sequence (0: length * ld), at least
+ *            (length - 1) * ld + vocab;
  *   labels   (2 * pairs, length) dense;   ref_logps  (2 * pairs) fp32;
  *   losses, margins  (pairs) fp32;  logps  (2 * pairs) fp32;
  *   lse      (2 * pairs * length) fp32.
@@ -408,8 +410,9 @@ ns_status ns_rms_norm_grad(const ns_rms_norm_grad_args* args, void* ws, size_t w
  *   k_p = dloss_p * beta * (label_smoothing * sigmoid(margin_p)
  *                           - (1 - label_smoothing) * sigmoid(-margin_p)),
  *   k_{pairs+p} = -k_p
- * of logits' type, ld_dlogits >= vocab; dlogits may be the logits' own
- * buffer with the same leading dimension. length >= 0 (0: empty sequences,
+ * of logits' type, positions ld_dlogits >= vocab and sequences length *
+ * ld_dlogits apart; dlogits may be the logits' own buffer with ld_dlogits ==
+ * ld, and then has the logits' sequences. length >= 0 (0: empty sequences,
  * losses of the reference alone), pairs >= 0 (0 is a no-op), 2 * pairs *
  * length <= NS_MAX_ROWS, 1 <= vocab <= NS_MAX_ROWS; beta finite,
  * 0 <= label_smoothing <= 1. Workspace of the forward call:
@@ -421,6 +424,7 @@ typedef struct {
   ns_dtype dtype;
   ns_id_type label_type;
   float beta, label_smoothing;
+  int64_t ld_sequence;
 } ns_preference_args;
 ns_status ns_preference_loss_workspace_size(int64_t pairs, int64_t length, int64_t vocab,
                                             size_t* bytes);

@@ -302,12 +302,28 @@ bool pref_sizes_ok(int64_t pairs, int64_t length, int64_t vocab) {
 }
 size_t pref_workspace(int64_t pairs, int64_t length, int64_t vocab) {
   const int64_t rows = 2 * pairs * length;
-  return std::max(ALIGN, align_up(sizeof(float2) * static_cast<size_t>(rows) *
+  return std::max(ALIGN, align_up(sizeof(double2) * static_cast<size_t>(rows) *
                                   pref_split(rows, vocab).pieces));
+}
+// Sequences' bytes stay within 62 bits.
+constexpr int64_t MAX_SEQUENCE = int64_t{1} << 60;
+int64_t sequence_ld(const ns_preference_args& p) {
+  return p.ld_sequence != 0 ? p.ld_sequence : p.length * p.ld;
+}
+// The logits' buffer (not empty).
+Span logits_span(const ns_preference_args& p) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p.logits);
+  if (p.pairs < 1 || p.length < 1) return {a, a};
+  const int64_t last = (2 * p.pairs - 1) * sequence_ld(p) + (p.length - 1) * p.ld + p.vocab;
+  return {a, a + static_cast<uintptr_t>(last) * type_bytes(p.dtype)};
 }
 ns_status check_pref(const ns_preference_args* p) {
   if (!p || !type_ok(p->dtype) || !ids_ok(p->label_type)) return NS_ERR_INVALID_ARG;
   if (!pref_sizes_ok(p->pairs, p->length, p->vocab) || !ld_ok(p->ld, p->vocab))
+    return NS_ERR_INVALID_ARG;
+  const int64_t seqs = 2 * p->pairs, seq = sequence_ld(*p);
+  if (p->length > 0 && seqs > 1 &&
+      (seq < (p->length - 1) * p->ld + p->vocab || seq > MAX_SEQUENCE / seqs))
     return NS_ERR_INVALID_ARG;
   if (!std::isfinite(p->beta) || !(p->label_smoothing >= 0.f && p->label_smoothing <= 1.f))
     return NS_ERR_INVALID_ARG;
@@ -322,6 +338,7 @@ PrefArgs pref_args(const ns_preference_args& p) {
   a.logits = p.logits;
   a.labels = p.labels;
   a.ld = p.ld;
+  a.ld_seq = sequence_ld(p);
   a.pairs = static_cast<int>(p.pairs);
   a.length = static_cast<int>(p.length);
   a.vocab = static_cast<int>(p.vocab);
@@ -356,7 +373,7 @@ NS_API ns_status ns_preference_loss(const ns_preference_args* p, const float* re
   const Span writes[] = {floats(losses, p->pairs), floats(margins, p->pairs),
                          floats(logps, 2 * p->pairs), floats(lse, rows),
                          span(ws, 1, need, need, 1)};
-  const Span reads[] = {span(p->logits, rows, p->vocab, p->ld, type_bytes(p->dtype)),
+  const Span reads[] = {logits_span(*p),
                         span(p->labels, 1, rows, rows, id_bytes(p->label_type)),
                         floats(ref_logps, 2 * p->pairs)};
   if (clash(writes, reads)) return NS_ERR_INVALID_ARG;
@@ -364,7 +381,7 @@ NS_API ns_status ns_preference_loss(const ns_preference_args* p, const float* re
   s = device_status();
   if (s != NS_OK) return s;
   return from_hip(launch_preference_loss(pref_args(*p), p->dtype, p->label_type == NS_IDS_I64,
-                                         pref_split(rows, p->vocab), static_cast<float2*>(ws),
+                                         pref_split(rows, p->vocab), static_cast<double2*>(ws),
                                          ref_logps, losses, margins, logps, lse,
                                          static_cast<hipStream_t>(stream)));
 }
@@ -383,8 +400,8 @@ NS_API ns_status ns_preference_loss_grad(const ns_preference_args* p, const floa
   const size_t es = type_bytes(p->dtype);
   const bool in_place = dlogits == p->logits && ld_dlogits == p->ld;
   const Span none = {0, 0};
-  const Span writes[] = {span(dlogits, rows, p->vocab, ld_dlogits, es)};
-  const Span reads[] = {in_place ? none : span(p->logits, rows, p->vocab, p->ld, es),
+  const Span writes[] = {in_place ? logits_span(*p) : span(dlogits, rows, p->vocab, ld_dlogits, es)};
+  const Span reads[] = {in_place ? none : logits_span(*p),
                         span(p->labels, 1, rows, rows, id_bytes(p->label_type)),
                         floats(margins, p->pairs), floats(lse, rows), floats(dlosses, p->pairs)};
   if (clash(writes, reads)) return NS_ERR_INVALID_ARG;
@@ -392,6 +409,7 @@ NS_API ns_status ns_preference_loss_grad(const ns_preference_args* p, const floa
   if (s != NS_OK) return s;
   return from_hip(launch_preference_grad(pref_args(*p), p->dtype, p->label_type == NS_IDS_I64,
                                          margins, lse, dlosses, dlogits, ld_dlogits,
+                                         in_place ? sequence_ld(*p) : p->length * ld_dlogits,
                                          static_cast<hipStream_t>(stream)));
 }
 

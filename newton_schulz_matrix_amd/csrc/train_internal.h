@@ -111,7 +111,7 @@ hipError_t launch_rms_norm_grad(const RmsGradArgs& a, int dy_type, int h_type, i
 struct PrefArgs {
   const void* logits;
   const void* labels;
-  int64_t ld;
+  int64_t ld, ld_seq;  // from one position, one sequence to the next
   int pairs, length, vocab;
   float beta, smoothing;
 };
@@ -122,11 +122,12 @@ struct PrefSplit {
 };
 PrefSplit pref_split(int64_t rows, int64_t vocab);
 hipError_t launch_preference_loss(const PrefArgs& a, int type, bool labels64, const PrefSplit& sp,
-                                  float2* parts, const float* ref_logps, float* losses,
+                                  double2* parts, const float* ref_logps, float* losses,
                                   float* margins, float* logps, float* lse, hipStream_t stream);
 hipError_t launch_preference_grad(const PrefArgs& a, int type, bool labels64,
                                   const float* margins, const float* lse, const float* dlosses,
-                                  void* dlogits, int64_t ld_dlogits, hipStream_t stream);
+                                  void* dlogits, int64_t ld_dlogits, int64_t ld_dseq,
+                                  hipStream_t stream);
 
 // -------------------------------------------------------------- AdamW
 

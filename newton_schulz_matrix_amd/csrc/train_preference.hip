@@ -76,8 +76,9 @@ __device__ __forceinline__ float factor(float m, float base) {
 
 // Maximum and sum of one piece of a row. A thread keeps its own running
 // maximum and rescales its sum once a step; the threads' sums are brought to
-// the piece's maximum once, at the end, and added in 64 bits, so that a row's
-// sum carries one rounding where a sequence adds up hundreds of rows.
+// the piece's maximum once, at the end, and added and kept in 64 bits: a
+// sequence adds up the roundings of hundreds of rows, and the difference of two
+// sequences is small beside them.
 template <int U>
 __device__ __forceinline__ void take(const float (&v)[U][VEC], float& m, float& s) {
   float top = m, low = INFINITY;
@@ -108,14 +109,15 @@ __device__ __forceinline__ void take(const float (&v)[U][VEC], float& m, float& 
   m = top;
 }
 template <class T, class I, int THREADS>
-__global__ __launch_bounds__(THREADS) void pieces_kernel(PrefArgs a, PrefSplit sp, float2* parts) {
+__global__ __launch_bounds__(THREADS) void pieces_kernel(PrefArgs a, PrefSplit sp,
+                                                         double2* parts) {
   constexpr int STEP = step_of(THREADS);
   __shared__ float red_m[THREADS / 64];
   __shared__ double red_s[THREADS / 64];
-  const int64_t row = blockIdx.x;
+  const int row = blockIdx.x, seq = row / a.length;
   if (!counted(a, label_at<I>(a, row))) return;
   const int begin = blockIdx.y * sp.piece, end = min(a.vocab, begin + sp.piece);
-  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+  const T* z = static_cast<const T*>(a.logits) + seq * a.ld_seq + (row - seq * a.length) * a.ld;
   float m = -INFINITY, s = 0.f;
   const int col0 = threadIdx.x * VEC;
   int base = begin;
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(THREADS) void pieces_kernel(PrefArgs a, PrefSplit s
   if (threadIdx.x != 0) return;
   double total = 0.0;
   for (int w = 0; w < THREADS / 64; ++w) total += red_s[w];
-  parts[row * sp.pieces + blockIdx.y] = make_float2(top, static_cast<float>(total));
+  parts[static_cast<int64_t>(row) * sp.pieces + blockIdx.y] = make_double2(top, total);
 }
 
 // log(1 + exp(x)) = -log sigmoid(-x)
@@ -171,7 +173,7 @@ __device__ __forceinline__ double softplus(double x) {
 constexpr int PAIR_THREADS = 1024;
 template <class T, class I>
 __global__ __launch_bounds__(PAIR_THREADS) void pairs_kernel(PrefArgs a, PrefSplit sp,
-                                                             const float2* parts,
+                                                             const double2* parts,
                                                              const float* ref_logps, float* losses,
                                                              float* margins, float* logps,
                                                              float* lse) {
@@ -179,22 +181,24 @@ __global__ __launch_bounds__(PAIR_THREADS) void pairs_kernel(PrefArgs a, PrefSpl
   double sums[2];
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
-    const int64_t first = static_cast<int64_t>(side * a.pairs + blockIdx.x) * a.length;
+    const int seq = side * a.pairs + blockIdx.x;
+    const int64_t first = static_cast<int64_t>(seq) * a.length;
+    const T* z = static_cast<const T*>(a.logits) + seq * a.ld_seq;
     double sum = 0.0;
     for (int t = threadIdx.x; t < a.length; t += PAIR_THREADS) {
       const int64_t row = first + t;
       const int64_t label = label_at<I>(a, row);
       float l = 0.f;
       if (counted(a, label)) {
-        const float2* p = parts + row * sp.pieces;
-        float m = p[0].x;
-        for (int k = 1; k < sp.pieces; ++k) m = fmaxf(m, p[k].x);
+        const double2* p = parts + row * sp.pieces;
+        double m = p[0].x;
+        for (int k = 1; k < sp.pieces; ++k) m = fmax(m, p[k].x);
         double s = 0.0;
         for (int k = 0; k < sp.pieces; ++k)
-          s += static_cast<double>(p[k].y) * exp(static_cast<double>(p[k].x) - base_of(m));
-        const double wide = static_cast<double>(m) + log(s);
+          s += p[k].y * exp(p[k].x - static_cast<double>(base_of(static_cast<float>(m))));
+        const double wide = m + log(s);
         l = static_cast<float>(wide);
-        sum += static_cast<double>(static_cast<float>(static_cast<const T*>(a.logits)[row * a.ld + label])) - wide;
+        sum += static_cast<double>(static_cast<float>(z[t * a.ld + label])) - wide;
       }
       lse[row] = l;
     }
@@ -232,13 +236,15 @@ __device__ __forceinline__ float sigmoid(float x) {
 template <class T, class I, int THREADS>
 __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* margins,
                                                        const float* lse, const float* dlosses,
-                                                       T* dlogits, int64_t ld_dlogits, int steps) {
+                                                       T* dlogits, int64_t ld_dlogits,
+                                                       int64_t ld_dseq, int steps) {
   const int64_t all = int64_t{2} * a.pairs * a.length * steps;
   for (int64_t block = blockIdx.x; block < all; block += gridDim.x) {
     const int row = static_cast<int>(block / steps);
     const int base = static_cast<int>(block - static_cast<int64_t>(row) * steps) * step_of(THREADS);
+    const int seq = row / a.length, t = row - seq * a.length;
     const int64_t label = label_at<I>(a, row);
-    T* d = dlogits + row * ld_dlogits;
+    T* d = dlogits + seq * ld_dseq + t * ld_dlogits;
     const int col0 = static_cast<int>(threadIdx.x) * VEC;
     if (!counted(a, label)) {
       const float zero[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -250,14 +256,13 @@ __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* 
       }
       continue;
     }
-    const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+    const T* z = static_cast<const T*>(a.logits) + seq * a.ld_seq + t * a.ld;
     Raw<T> raw[UNROLL];
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j) {
       const int at = base + j * THREADS * VEC;
       if (at < a.vocab && a.vocab >= VEC) raw[j] = fetch_at<Use::ONCE>(z, a.vocab, at + col0);
     }
-    const int seq = row / a.length;
     const int pair = seq < a.pairs ? seq : seq - a.pairs;
     const float margin = margins[pair];
     float k = dlosses[pair] * a.beta *
@@ -296,7 +301,7 @@ PrefSplit pref_split(int64_t rows, int64_t vocab) {
 }
 
 hipError_t launch_preference_loss(const PrefArgs& a, int type, bool labels64, const PrefSplit& sp,
-                                  float2* parts, const float* ref_logps, float* losses,
+                                  double2* parts, const float* ref_logps, float* losses,
                                   float* margins, float* logps, float* lse, hipStream_t stream) {
   const int64_t rows = int64_t{2} * a.pairs * a.length;
   auto on = [&](auto t, auto i) {
@@ -320,7 +325,8 @@ hipError_t launch_preference_loss(const PrefArgs& a, int type, bool labels64, co
 
 hipError_t launch_preference_grad(const PrefArgs& a, int type, bool labels64,
                                   const float* margins, const float* lse, const float* dlosses,
-                                  void* dlogits, int64_t ld_dlogits, hipStream_t stream) {
+                                  void* dlogits, int64_t ld_dlogits, int64_t ld_dseq,
+                                  hipStream_t stream) {
   const int64_t rows = int64_t{2} * a.pairs * a.length;
   if (rows <= 0) return hipSuccess;
   const int threads = a.vocab <= SHORT_VOCAB ? 64 : 256, step = step_of(threads);
@@ -331,10 +337,10 @@ hipError_t launch_preference_grad(const PrefArgs& a, int type, bool labels64,
     using I = decltype(i);
     if (threads == 64)
       hipLaunchKernelGGL((grad_kernel<T, I, 64>), grid, dim3(64), 0, stream, a, margins, lse,
-                         dlosses, static_cast<T*>(dlogits), ld_dlogits, steps);
+                         dlosses, static_cast<T*>(dlogits), ld_dlogits, ld_dseq, steps);
     else
       hipLaunchKernelGGL((grad_kernel<T, I, 256>), grid, dim3(256), 0, stream, a, margins, lse,
-                         dlosses, static_cast<T*>(dlogits), ld_dlogits, steps);
+                         dlosses, static_cast<T*>(dlogits), ld_dlogits, ld_dseq, steps);
     return hipGetLastError();
   };
   return by_type(type, [&](auto t) { return labels64 ? on(t, int64_t{}) : on(t, int32_t{}); });

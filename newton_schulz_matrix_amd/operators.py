@@ -49,7 +49,7 @@ class _RmsNormGradArgs(ctypes.Structure):
 class _PreferenceArgs(ctypes.Structure):
     _fields_ = [("logits", _vp), ("labels", _vp), ("pairs", _i64), ("length", _i64),
                 ("vocab", _i64), ("ld", _i64), ("dtype", _int), ("label_type", _int),
-                ("beta", _f32), ("label_smoothing", _f32)]
+                ("beta", _f32), ("label_smoothing", _f32), ("ld_sequence", _i64)]
 
 
 class _AdamwTensor(ctypes.Structure):
@@ -328,10 +328,21 @@ def _preference_args(logits, labels, beta, label_smoothing, dev):
     if len(shape) != 3 or shape[0] % 2:
         raise ValueError("logits must be (2 * pairs, length, vocab): the preferred sequences, then "
                          "the others")
-    _, vocab, ld = _rows_of(logits, "logits", dev)
-    return _PreferenceArgs(logits.data_ptr(), _dense(labels, shape[:2], "labels", dev), shape[0] // 2,
-                           shape[1], vocab, ld, _code(logits), _ids_type(labels, "labels"), beta,
-                           label_smoothing)
+    n, length, vocab = shape
+    ld, sequence = vocab, 0
+    if not logits.is_contiguous():   # positions and sequences may each lie further apart
+        apart, step, one = logits.stride()
+        if vocab > 1 and one != 1:
+            raise ValueError("logits: rows must be contiguous (stride(-1) == 1)")
+        ld = step if length > 1 else vocab
+        sequence = apart if n > 1 else 0
+        if ld < vocab or (n > 1 and sequence < (length - 1) * ld + vocab):
+            raise ValueError(f"logits: overlapping rows (shape {tuple(shape)}, strides "
+                             f"{tuple(logits.stride())})")
+    args = _PreferenceArgs(logits.data_ptr(), _dense(labels, shape[:2], "labels", dev), n // 2, length,
+                           vocab, ld, _code(logits), _ids_type(labels, "labels"), beta,
+                           label_smoothing, sequence)
+    return args
 
 
 def ns_preference_loss_workspace_size(pairs: int, length: int, vocab: int) -> int:
@@ -341,13 +352,14 @@ def ns_preference_loss_workspace_size(pairs: int, length: int, vocab: int) -> in
 def ns_preference_loss(logits, labels, ref_logps, beta: float = 0.1, label_smoothing: float = 0.0,
                        workspace=None):
     """Preference loss of paired sequences from the policy's logits (2 pairs,
-    length, vocab), the labels (2 pairs, length; a position whose label is not
+    length, vocab; a slice such as logits[:, :-1] is fine), the labels (2 pairs, length; a position whose label is not
     in the vocabulary, such as -100, does not count) and the reference's log
     probability of each sequence (2 pairs, fp32). Returns fp32 tensors
     (losses, margins, logps, lse): the loss and margin of each pair, the
     policy's log probability of each sequence, and each position's log sum of
     exponentials, which the gradient needs."""
     dev = _device_of(logits, "logits")
+    labels = labels if labels.is_contiguous() else labels.contiguous()
     args = _preference_args(logits, labels, beta, label_smoothing, dev)
     pairs, length, device = args.pairs, args.length, logits.device
     ref = _dense(ref_logps, (2 * pairs,), "ref_logps", dev, torch.float32)
@@ -368,11 +380,14 @@ def ns_preference_loss_grad(logits, labels, margins, lse, dlosses, beta: float =
     margins and lse as it returned them and the gradient of each loss, dlosses
     (pairs, fp32). `out` may be the logits themselves."""
     dev = _device_of(logits, "logits")
+    labels = labels if labels.is_contiguous() else labels.contiguous()
     args = _preference_args(logits, labels, beta, label_smoothing, dev)
     pairs, shape = args.pairs, logits.shape
     if out is None:
         out = torch.empty(shape, dtype=logits.dtype, device=logits.device)
         ld_out = args.vocab
+    elif out is logits:
+        ld_out = args.ld
     else:
         ld_out = _like_rows(out, shape, "out", dev, logits.dtype)
     _check(library().ns_preference_loss_grad(

@@ -187,6 +187,30 @@ def test_strided_unaligned_and_in_place():
         assert inplace is full and torch.equal(full, grad)
 
 
+def test_slices_of_positions_and_sequences():
+    """logits[:, :-1], every second sequence, and labels[:, 1:] as they are."""
+    require_gpu()
+    for dtype, vocab in ((BF, 1003), (SF, 64)):
+        full = normal(11, (8, 6, vocab), dtype)
+        all_labels = torch.from_numpy(_labels(4, 8, 6, vocab)).cuda()
+        ref, dl = normal(12, (4,)), normal(13, (2,))
+        for pick in (lambda t: t[::2, :-1], lambda t: t[:4, 1:], lambda t: t[:4, 2:3], lambda t: t[4:]):
+            logits, labels = pick(full), pick(all_labels)
+            want = _check(logits.contiguous(), labels.cpu().numpy(), ref, 0.1, 0.1, dlosses=dl)
+            out = nsmi.ns_preference_loss(logits, labels, ref, label_smoothing=0.1)
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+            g = nsmi.ns_preference_loss_grad(logits, labels, out[1], out[3], dl, label_smoothing=0.1)
+            assert torch.equal(g, want[4])
+            whole = full.clone()
+            part = pick(whole)
+            nsmi.ns_preference_loss_grad(part, labels, out[1], out[3], dl, label_smoothing=0.1, out=part)
+            assert torch.equal(part, want[4])
+            part.zero_()
+            rest = full.clone()
+            pick(rest).zero_()
+            assert torch.equal(whole, rest)          # nothing beside the slice was written
+
+
 def test_gradient_against_differences():
     """<gradient, t> against central differences of the fp64 forward."""
     require_gpu()

@@ -148,7 +148,7 @@ def test_rms_norm_grad_refusals():
 def pref(call="loss", ws=P[8], n=64 * MB, ref=P[2], losses=P[3], margins=P[4], logps=P[5], lse=P[6],
          dlosses=P[3], out=P[7], ld_out=100, **kw):
     a = dict(logits=P[0], labels=P[1], pairs=2, length=3, vocab=100, ld=100, dtype=BF16, label_type=1,
-             beta=0.1, label_smoothing=0.0)
+             beta=0.1, label_smoothing=0.0, ld_sequence=0)
     a.update(kw)
     args = ctypes.byref(ops._PreferenceArgs(*a.values()))
     if call == "loss":
@@ -176,6 +176,12 @@ def test_preference_refusals():
     for kw in (dict(ws=None), dict(n=8), dict(ws=P[8] + 8)):
         assert pref(**kw) == WS, kw
     assert pref("grad", out=P[0]) == UNSUPPORTED                               # in place
+    for call in ("loss", "grad"):
+        assert pref(call, ld_sequence=400) == UNSUPPORTED and pref(call, ld_sequence=300) == UNSUPPORTED
+        for bad in (299, 1, -5, 1 << 60):
+            assert pref(call, ld_sequence=bad) == BAD, bad
+    assert pref("grad", ld_sequence=MB, out=P[0] + 8 * MB) == UNSUPPORTED      # behind 4 sequences
+    assert pref("grad", ld_sequence=MB, out=P[0] + 3 * MB) == BAD
     assert pref("grad", length=0, logits=None, labels=None, out=None) == nsmi.NS_OK
     for kw in (dict(out=None), dict(dlosses=None), dict(ld_out=99), dict(out=P[0], ld_out=104),
                dict(out=P[0] + 2), dict(out=P[1]), dict(out=P[4]), dict(out=P[6]), dict(out=P[7] + 1)):
