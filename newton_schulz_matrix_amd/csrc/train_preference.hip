@@ -169,9 +169,10 @@ __device__ __forceinline__ double softplus(double x) {
   return fmax(x, 0.0) + log1p(exp(-fabs(x)));
 }
 
-// One workgroup for each pair: the rows' lse, the sequences' sums, the loss.
-constexpr int PAIR_THREADS = 1024;
-template <class T, class I>
+// One workgroup for each pair: the rows' lse, the sequences' sums, the loss. A
+// wave for sequences that short, of which there can be millions.
+constexpr int SHORT_LENGTH = 64;
+template <class T, class I, int PAIR_THREADS>
 __global__ __launch_bounds__(PAIR_THREADS) void pairs_kernel(PrefArgs a, PrefSplit sp,
                                                              const double2* parts,
                                                              const float* ref_logps, float* losses,
@@ -316,8 +317,12 @@ hipError_t launch_preference_loss(const PrefArgs& a, int type, bool labels64, co
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((pairs_kernel<T, I>), dim3(a.pairs), dim3(PAIR_THREADS), 0, stream, a, sp,
-                       parts, ref_logps, losses, margins, logps, lse);
+    if (a.length <= SHORT_LENGTH)
+      hipLaunchKernelGGL((pairs_kernel<T, I, 64>), dim3(a.pairs), dim3(64), 0, stream, a, sp, parts,
+                         ref_logps, losses, margins, logps, lse);
+    else
+      hipLaunchKernelGGL((pairs_kernel<T, I, 1024>), dim3(a.pairs), dim3(1024), 0, stream, a, sp,
+                         parts, ref_logps, losses, margins, logps, lse);
     return hipGetLastError();
   };
   return by_type(type, [&](auto t) { return labels64 ? on(t, int64_t{}) : on(t, int32_t{}); });

@@ -386,7 +386,9 @@ def ns_preference_loss_grad(logits, labels, margins, lse, dlosses, beta: float =
     if out is None:
         out = torch.empty(shape, dtype=logits.dtype, device=logits.device)
         ld_out = args.vocab
-    elif out is logits:
+    elif out.data_ptr() == logits.data_ptr():
+        if out.dtype != logits.dtype or out.shape != shape or out.stride() != logits.stride():
+            raise ValueError("out begins where the logits do, but is another view of that memory")
         ld_out = args.ld
     else:
         ld_out = _like_rows(out, shape, "out", dev, logits.dtype)

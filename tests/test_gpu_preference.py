@@ -211,6 +211,34 @@ def test_slices_of_positions_and_sequences():
             assert torch.equal(whole, rest)          # nothing beside the slice was written
 
 
+def test_very_many_pairs():
+    """More short sequences than a grid of large workgroups holds."""
+    require_gpu()
+    pairs = (1 << 22) - 1
+    logits = torch.zeros((2 * pairs, 1, 3), dtype=BF, device="cuda")
+    logits[5, 0, 1], logits[-1, 0, 2] = 2.0, 2.0
+    labels = torch.ones((2 * pairs, 1), dtype=torch.int32, device="cuda")
+    losses, margins, logps, lse = nsmi.ns_preference_loss(logits, labels, torch.zeros(2 * pairs, device="cuda"))
+    up, down, flat = 2 - np.log(2 + np.exp(2.0)), -np.log(2 + np.exp(2.0)), -np.log(3.0)
+    assert logps[5].item() == pytest.approx(up, rel=1e-6) and logps[-1].item() == pytest.approx(down, rel=1e-6)
+    assert margins[5].item() == pytest.approx(0.1 * (up - flat), rel=1e-5)
+    assert margins[-1].item() == pytest.approx(0.1 * (flat - down), rel=1e-5)
+    assert losses[7].item() == pytest.approx(np.log(2.0), rel=1e-6)
+    g = nsmi.ns_preference_loss_grad(logits, labels, margins, lse, torch.ones(pairs, device="cuda"))
+    assert g[7, 0, 1].item() == pytest.approx(-0.05 * 2 / 3, rel=2 ** -8)
+    assert g[pairs + 7, 0, 1].item() == pytest.approx(0.05 * 2 / 3, rel=2 ** -8)
+
+
+def test_out_that_is_another_view_is_refused():
+    require_gpu()
+    full = normal(1, (2, 4, 24), SF)
+    logits, labels = full[:, :-1], torch.zeros((2, 3), dtype=torch.int64, device="cuda")
+    out = nsmi.ns_preference_loss(logits, labels, torch.zeros(2, device="cuda"))
+    other = full.view(-1)[:144].view(2, 3, 24)
+    with pytest.raises(ValueError):
+        nsmi.ns_preference_loss_grad(logits, labels, out[1], out[3], out[0], out=other)
+
+
 def test_gradient_against_differences():
     """<gradient, t> against central differences of the fp64 forward."""
     require_gpu()
