@@ -114,32 +114,6 @@ __device__ __forceinline__ void widen_at(const Raw<T>& raw, const T* row, int di
   else widen_ragged(raw, dim, at, v);
 }
 
-// V such vectors, at columns col, col + stride, ....
-template <Use U = Use::AGAIN, int V, class T>
-__device__ __forceinline__ void fetch_row(const T* row, int dim, int col, int stride,
-                                          Raw<T> (&raw)[V]) {
-  if (dim < VEC) return;
-#pragma unroll
-  for (int j = 0; j < V; ++j) raw[j] = fetch_at<U>(row, dim, col + j * stride);
-}
-template <int V, class T>
-__device__ __forceinline__ void widen_row(const Raw<T> (&raw)[V], const T* row, int dim, int col,
-                                          int stride, float (&v)[V][VEC]) {
-#pragma unroll
-  for (int j = 0; j < V; ++j) widen_at(raw[j], row, dim, col + j * stride, v[j]);
-}
-
-template <Use U = Use::AGAIN, class T>
-__device__ __forceinline__ void store8_upto(T* p, int left, const float (&v)[VEC]) {
-  if (left >= VEC) {
-    store8<U>(p, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      if (e < left) p[e] = static_cast<T>(v[e]);
-  }
-}
-
 // v as it reads back after being stored as T.
 template <class T>
 __device__ __forceinline__ float rounded(float v) {
