@@ -114,6 +114,17 @@ __device__ __forceinline__ void widen_at(const Raw<T>& raw, const T* row, int di
   else widen_ragged(raw, dim, at, v);
 }
 
+template <Use U = Use::AGAIN, class T>
+__device__ __forceinline__ void store8_upto(T* p, int left, const float (&v)[VEC]) {
+  if (left >= VEC) {
+    store8<U>(p, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (e < left) p[e] = static_cast<T>(v[e]);
+  }
+}
+
 // v as it reads back after being stored as T.
 template <class T>
 __device__ __forceinline__ float rounded(float v) {
