@@ -300,6 +300,15 @@ def _workspace(nbytes: int, device):
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
+def _own_bytes(workspace):
+    """A given workspace, which the library writes from its first element on:
+    it must own those bytes (an expanded or strided view need not)."""
+    _device_tensor(workspace, "workspace")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
 def ns_workspace_size(shapes: Sequence[Sequence[int]], backend: str = "gram",
                       coefficients=POLAR_EXPRESS_COEFFICIENTS,
                       restart_iterations: Iterable[int] = DEFAULT_RESTARTS,
@@ -341,6 +350,8 @@ def ns_batched(Gs: List, backend: str = "gram",
                                  ctypes.byref(nbytes)), "ns_workspace_size")
     if workspace is None or workspace.numel() < nbytes.value:
         workspace = _workspace(nbytes.value, dev)
+    else:
+        _own_bytes(workspace)
     _check(lib.ns_batched(mats, len(Gs), BACKENDS[backend], ctypes.byref(p),
                           workspace.data_ptr(), workspace.numel(), _stream_ptr(Gs[0])),
            "ns_batched")
@@ -386,6 +397,8 @@ def ns_gram(G, coefficients=POLAR_EXPRESS_COEFFICIENTS,
                                  ctypes.byref(nbytes)), "ns_workspace_size")
     if workspace is None or workspace.numel() < nbytes.value:
         workspace = _workspace(nbytes.value, G.device)
+    else:
+        _own_bytes(workspace)
     _check(lib.ns_gram(ctypes.byref(mat), ctypes.byref(p), workspace.data_ptr(),
                        workspace.numel(), _stream_ptr(G)), "ns_gram")
     return out
@@ -444,6 +457,8 @@ def ns_muon_step(grads: List, momenta: List, params: List, beta: float, lr: floa
            "ns_muon_workspace_size")
     if workspace is None or workspace.numel() < nbytes.value:
         workspace = _workspace(nbytes.value, grads[0].device)
+    else:
+        _own_bytes(workspace)
     _check(lib.ns_muon_step(mats, len(grads), ctypes.byref(p), float(beta), float(lr),
                             workspace.data_ptr(), workspace.numel(), _stream_ptr(grads[0])),
            "ns_muon_step")
@@ -464,6 +479,8 @@ def ns_direct(G, coefficients=POLAR_EXPRESS_COEFFICIENTS, eps: float = DEFAULT_E
                                  ctypes.byref(nbytes)), "ns_workspace_size")
     if workspace is None or workspace.numel() < nbytes.value:
         workspace = _workspace(nbytes.value, G.device)
+    else:
+        _own_bytes(workspace)
     _check(lib.ns_direct(ctypes.byref(mat), ctypes.byref(p), workspace.data_ptr(),
                          workspace.numel(), _stream_ptr(G)), "ns_direct")
     return out

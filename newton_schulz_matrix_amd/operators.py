@@ -21,7 +21,7 @@ from typing import List, Optional, Sequence, Tuple
 import torch
 
 from . import (NS_DT_BF16, NS_DT_F16, NS_DT_F32, _check, _device_tensor, _dtype_code,
-               _workspace, library)
+               _own_bytes, _workspace, library)
 
 NS_DT_E4M3 = 3
 NS_IDS_I32, NS_IDS_I64 = 0, 1
@@ -169,7 +169,7 @@ def _sized(name: str, *args) -> int:
 def _given_or_new(workspace, nbytes: int, device):
     if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
         return _workspace(nbytes, device)
-    return _device_tensor(workspace, "workspace")
+    return _own_bytes(workspace)
 
 
 # ------------------------------------------------------------------ embedding
