@@ -18,10 +18,21 @@ from __future__ import annotations
 import ctypes
 from typing import List, Optional, Sequence, Tuple
 
-import torch
-
 from . import (NS_DT_BF16, NS_DT_F16, NS_DT_F32, _check, _device_tensor, _dtype_code,
                _own_bytes, _workspace, library)
+
+
+class _Torch:
+    """torch, loaded where a call first needs it: the package and its build
+    script import without it."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _Torch()
 
 NS_DT_E4M3 = 3
 NS_IDS_I32, NS_IDS_I64 = 0, 1
@@ -79,10 +90,19 @@ SIGNATURES = {
 # Small calls take about as long as their launch: the helpers below run for
 # every tensor of a call and are written for few steps.
 
-_CODES = {torch.float32: NS_DT_F32, torch.bfloat16: NS_DT_BF16, torch.float16: NS_DT_F16}
-_ID_TYPES = {torch.int32: NS_IDS_I32, torch.int64: NS_IDS_I64}
-# the current stream of a device as a pointer, without a Stream object
-_stream_of = torch._C._cuda_getCurrentRawStream
+_codes = {}      # of the tensor types met so far
+_id_types = {}
+_raw_stream = None
+
+
+def _stream_of(dev: int) -> int:
+    """The current stream of a device as a pointer; without a Stream object,
+    where this torch can say it so."""
+    global _raw_stream
+    if _raw_stream is None:
+        _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                       or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+    return _raw_stream(dev)
 
 
 def _device_of(t, name: str) -> int:
@@ -94,13 +114,20 @@ def _device_of(t, name: str) -> int:
 
 
 def _code(t) -> int:
-    return _CODES[t.dtype] if t.dtype in _CODES else _dtype_code(t.dtype)
+    code = _codes.get(t.dtype)
+    if code is None:
+        code = _codes[t.dtype] = _dtype_code(t.dtype)
+    return code
 
 
 def _ids_type(t, name: str) -> int:
-    if t.dtype not in _ID_TYPES:
-        raise TypeError(f"{name} must be int32 or int64, not {t.dtype}")
-    return _ID_TYPES[t.dtype]
+    code = _id_types.get(t.dtype)
+    if code is None:
+        code = {torch.int32: NS_IDS_I32, torch.int64: NS_IDS_I64}.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{name} must be int32 or int64, not {t.dtype}")
+        _id_types[t.dtype] = code
+    return code
 
 
 def _rows_of(t, name: str, dev: int) -> Tuple[int, int, int]:
