@@ -447,6 +447,12 @@ ns_status ns_preference_loss_grad(const ns_preference_args* args, const float* m
  *   exp_avg any type, exp_avg_sq fp32 or bf16 (fp16 cannot hold the square
  *   of a small gradient and is refused), master fp32 or NULL. Buffers of
  *   different tensors must not overlap either (the caller's to avoid).
+ * A state or a 16-bit param without master that a step changes by less than
+ * half of its type's rounding step keeps its value. For a bf16 exp_avg_sq
+ * that is a change of less than 2^-9 to 2^-8 of it: it settles within
+ * 2^-8 / (1 - beta2) of g^2, relative to itself, and above beta2 = 1 - 2^-8
+ * (0.9961) it stops falling under small gradients, above 1 - 2^-9 at once, so
+ * that large old ones stay in the denominator for good; keep it in fp32 there.
  * step >= 1; 0 <= beta1, beta2 < 1; lr, eps, weight_decay finite and >= 0.
  * The bias corrections are computed on the host in 64 bits: a captured call
  * replays the step it was captured with. */

@@ -16,6 +16,7 @@ of a larger tensor is fine; a transposed view is refused).
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import List, Optional, Sequence, Tuple
 
 from . import (NS_DT_BF16, NS_DT_F16, NS_DT_F32, _check, _device_tensor, _dtype_code,
@@ -37,6 +38,7 @@ torch = _Torch()
 NS_DT_E4M3 = 3
 NS_IDS_I32, NS_IDS_I64 = 0, 1
 NS_MAX_ROWS = 1 << 23
+BF16_SLOWEST = 1 - 2.0 ** -8     # beta2 above which a bf16 second moment can stand still
 
 _i64, _vp, _f32, _f64, _int = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_double,
                                ctypes.c_int)
@@ -437,7 +439,14 @@ def ns_adamw_step(params: List, grads: List, exp_avgs: List, exp_avg_sqs: List, 
     the Newton-Schulz update. Tensors are dense and of any shape; `masters`
     are fp32 copies that hold the weights, whose rounded values the params
     then receive (None entries: no copy). weight_decays: one for each tensor
-    (0 by default)."""
+    (0 by default).
+
+    exp_avg_sqs may be fp32 or bf16. In bf16 a step that changes one by less
+    than half a rounding step changes nothing: it settles within
+    2^-8 / (1 - betas[1]) of g^2, relative to itself (8% at 0.95, 39% at 0.99),
+    and above betas[1] = 1 - 2^-8 it stops falling under small gradients (at
+    the default 0.999 at once); a RuntimeWarning says so. Keep it in fp32
+    there."""
     count = len(params)
     if count == 0:
         return
@@ -460,6 +469,10 @@ def ns_adamw_step(params: List, grads: List, exp_avgs: List, exp_avg_sqs: List, 
                     for w, shape in zip(masters, shapes)])
     columns.append([p.numel() for p in params])
     columns += [[_code(t) for t in group] for group in (params, grads, exp_avgs, exp_avg_sqs)]
+    if betas[1] > BF16_SLOWEST and NS_DT_BF16 in columns[-1]:
+        warnings.warn(f"a bf16 exp_avg_sq stops falling with beta2 = {betas[1]}: a step of 1 - beta2 of "
+                      f"the value is below half a rounding step (up to 2^-8). Keep it in fp32, or take "
+                      f"beta2 <= {BF16_SLOWEST}", RuntimeWarning, stacklevel=2)
     tensors = (_AdamwTensor * count)(*zip(*columns, weight_decays))
     _check(library().ns_adamw_step(tensors, count, step, lr, betas[0], betas[1], eps,
                                    _stream_of(dev)), "ns_adamw_step")
