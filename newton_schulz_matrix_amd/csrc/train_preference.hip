@@ -228,9 +228,11 @@ __global__ __launch_bounds__(PAIR_THREADS) void pairs_kernel(PrefArgs a, PrefSpl
 
 // --------------------------------------------------------------- gradient
 
-__device__ __forceinline__ float sigmoid(float x) {
-  const float e = expf(-fabsf(x));
-  return x >= 0.f ? 1.f / (1.f + e) : e / (1.f + e);
+// s sigmoid(m) - (1 - s) sigmoid(-m), in 64 bits: the two terms all but cancel
+// where the smoothed loss is flat, and a whole row is multiplied by this.
+__device__ __forceinline__ double slope(double m, double s) {
+  const double e = exp(-fabs(m));
+  return (m >= 0.0 ? s - (1.0 - s) * e : s * e - (1.0 - s)) / (1.0 + e);
 }
 
 // Workgroups take a step each, in the order of the addresses.
@@ -257,6 +259,9 @@ __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* 
       }
       continue;
     }
+    // read first: k is computed while the logits are on their way
+    const int pair = seq < a.pairs ? seq : seq - a.pairs;
+    const float margin = margins[pair], dloss = dlosses[pair], l = lse[row];
     const T* z = static_cast<const T*>(a.logits) + seq * a.ld_seq + t * a.ld;
     Raw<T> raw[UNROLL];
 #pragma unroll
@@ -264,12 +269,8 @@ __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* 
       const int at = base + j * THREADS * VEC;
       if (at < a.vocab && a.vocab >= VEC) raw[j] = fetch_at<Use::ONCE>(z, a.vocab, at + col0);
     }
-    const int pair = seq < a.pairs ? seq : seq - a.pairs;
-    const float margin = margins[pair];
-    float k = dlosses[pair] * a.beta *
-              (a.smoothing * sigmoid(margin) - (1.f - a.smoothing) * sigmoid(-margin));
+    float k = static_cast<float>(static_cast<double>(dloss) * a.beta * slope(margin, a.smoothing));
     if (seq >= a.pairs) k = -k;
-    const float l = lse[row];
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j) {
       const int at = base + j * THREADS * VEC;
