@@ -410,6 +410,7 @@ ns_status ns_rms_norm_grad(const ns_rms_norm_grad_args* args, void* ws, size_t w
  *   k_p = dloss_p * beta * (label_smoothing * sigmoid(margin_p)
  *                           - (1 - label_smoothing) * sigmoid(-margin_p)),
  *   k_{pairs+p} = -k_p
+ * (in fp32, lse's own rounding puts up to |lse| 2^-24, relative, on a row)
  * of logits' type, positions ld_dlogits >= vocab and sequences length *
  * ld_dlogits apart; dlogits may be the logits' own buffer with ld_dlogits ==
  * ld, and then has the logits' sequences. length >= 0 (0: empty sequences,

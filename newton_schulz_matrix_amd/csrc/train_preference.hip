@@ -32,14 +32,9 @@ constexpr int SHORT_VOCAB = 64 * VEC * UNROLL / 2;
 constexpr int step_of(int threads) { return threads * VEC * UNROLL; }   // elements of a step
 constexpr float FAR = 150.f;                        // exp(-FAR) is 0 in fp32
 
-// exp(x) by the hardware's 2^x. The product with log2(e) carries the
-// constant's next 24 bits.
-__device__ __forceinline__ float exp_neg(float x) {
-  return __builtin_amdgcn_exp2f(fmaf(x, 1.925963033e-8f, x * 1.442695041f));
-}
-
-// The same without the rounding of the product p = x log2(e): exp(x) = 2^p
-// exp(x - p ln 2), where the second factor is 1 + c. bf16 logits take few
+// exp(x) by the hardware's 2^x, without the rounding of the product
+// p = x log2(e): exp(x) = 2^p exp(x - p ln 2), where the second factor is 1 + c. That
+// rounding is up to |x| half steps of the result. bf16 logits take few
 // values, so the roundings of p do not average out over a row: left alone they
 // put 2e-8 on its sum, much the same for every row, which the difference of
 // two sequences' sums keeps. x is not below -FAR.
@@ -198,6 +193,8 @@ __global__ __launch_bounds__(PAIR_THREADS) void pairs_kernel(PrefArgs a, PrefSpl
         for (int k = 0; k < sp.pieces; ++k)
           s += p[k].y * exp(p[k].x - static_cast<double>(base_of(static_cast<float>(m))));
         const double wide = m + log(s);
+        // lse is an fp32 output: its rounding, at most |lse| / 2^24, multiplies the
+        // row's gradient, which 16-bit gradients do not show
         l = static_cast<float>(wide);
         sum += static_cast<double>(static_cast<float>(z[t * a.ld + label])) - wide;
       }
@@ -279,7 +276,8 @@ __global__ __launch_bounds__(THREADS) void grad_kernel(PrefArgs a, const float* 
       widen_at(raw[j], z, a.vocab, at + col0, v);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float p = exp_neg(v[e] - l);
+        const float x = v[e] - l;
+        const float p = exp_exact(x < -FAR ? -FAR : x);   // (a NaN stays one)
         v[e] = at + col0 + e == label ? k * (1.f - p) : -k * p;
       }
       store8_upto<Use::ONCE>(d + at + col0, a.vocab - at - col0, v);

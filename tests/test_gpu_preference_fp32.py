@@ -46,3 +46,27 @@ def test_the_factor_of_a_pair(smoothing):
     assert_within(g[:, 0, 7], want, 1.01 * U32 * np.abs(want) + 2.0 ** -149, "k")
     plain = f64(dl) * float(np.float32(0.1)) * (s * O.sigmoid(f64(m)) - (1 - s) * O.sigmoid(-f64(m)))
     assert np.allclose(k, plain, rtol=1e-7, atol=1e-15)      # the formula of the header
+
+
+@pytest.mark.parametrize("vocab", [7, 1000, 20001])
+def test_the_probabilities(vocab):
+    """exp(z - lse): two roundings' worth from the hardware's power of two, one
+    for the correction, one for the product with k, and k's own."""
+    require_gpu()
+    rng = np.random.default_rng(vocab)
+    z = (LSE + rng.integers(-36 * 1024, 1, (2, 3, vocab)) / 1024).astype(np.float32)
+    z[:, 1, 0], z[0, 2, -1], z[1, 2, -1] = -np.inf, np.finfo(np.float32).min, LSE - 200
+    labels = torch.tensor([[1, 2, -100], [0, -100, vocab - 1]]).cuda()
+    margins, dl = torch.tensor([0.3]).cuda(), torch.tensor([1.7]).cuda()
+    lse = torch.full((2, 3), LSE, device="cuda")
+    g = f64(nsmi.ns_preference_loss_grad(torch.from_numpy(z).cuda(), labels, margins, lse, dl, beta=0.1))
+    k = f64(dl) * float(np.float32(0.1)) * _slope(f64(margins), 0.0)
+    k = np.concatenate([k, -k])[:, None, None]
+    keep = (labels >= 0).cpu().numpy()[..., None]
+    at = np.zeros(z.shape)
+    np.put_along_axis(at, labels.clamp(min=0).cpu().numpy()[..., None], 1.0, -1)
+    p = np.exp(z.astype(np.float64) - LSE)
+    want = np.where(keep, k * (at - p), 0.0)
+    # at a label, p's error counts and 1 - p and the product round
+    slack = np.abs(k) * np.where(at > 0, 3 * p + 3 * (1 - p), 5 * p) * U32 * 1.01 + 2.0 ** -126
+    assert_within(g, want, np.where(keep, slack, 0.0), "gradient")
