@@ -465,16 +465,18 @@ __global__ __launch_bounds__(WIDE) void rms_grad_wide_kernel(RmsGradArgs a, bool
 }
 
 // dweight[c] = sum over the workgroups' shares: 32 columns by 32 groups of
-// shares in a workgroup, the groups' sums joined in order.
+// shares in a workgroup, the groups' sums joined in order. In 64 bits: rounded to
+// fp32 at every share, the sum of 1031 rows was three times as far off as its
+// terms, and the kernel's time is that of its loads.
 constexpr int DW_COLS = 32, DW_GROUPS = 32;
 template <class TO>
 __global__ __launch_bounds__(DW_COLS * DW_GROUPS) void dweight_kernel(const float* partial,
                                                                       int blocks, int dim,
                                                                       TO* dweight) {
-  __shared__ float sums[DW_GROUPS][DW_COLS + 1];
+  __shared__ double sums[DW_GROUPS][DW_COLS + 1];
   const int tx = threadIdx.x % DW_COLS, ty = threadIdx.x / DW_COLS;
   const int col = blockIdx.x * DW_COLS + tx;
-  float s = 0.f;
+  double s = 0.0;
   if (col < dim) {
 #pragma unroll 4
     for (int b = ty; b < blocks; b += DW_GROUPS) s += partial[static_cast<int64_t>(b) * dim + col];
@@ -483,7 +485,7 @@ __global__ __launch_bounds__(DW_COLS * DW_GROUPS) void dweight_kernel(const floa
   __syncthreads();
   if (ty != 0 || col >= dim) return;
   for (int k = 1; k < DW_GROUPS; ++k) s += sums[k][tx];
-  dweight[col] = static_cast<TO>(s);
+  dweight[col] = static_cast<TO>(static_cast<float>(s));
 }
 
 // Calls f(team, vectors, width) for a row width, each as a type. Rows of up
