@@ -365,6 +365,10 @@ def _preference_args(logits, labels, beta, label_smoothing, dev):
             raise ValueError("logits: rows must be contiguous (stride(-1) == 1)")
         ld = step if length > 1 else vocab
         sequence = apart if n > 1 else 0
+        if n > 1 and length > 1 and vocab <= sequence and ld >= (n - 1) * sequence + vocab:
+            raise ValueError(f"logits: sequences must lie one behind the other (shape {tuple(shape)}, "
+                             f"strides {tuple(logits.stride())}): positions lie further apart than "
+                             f"sequences here; pass logits.contiguous()")
         if ld < vocab or (n > 1 and sequence < (length - 1) * ld + vocab):
             raise ValueError(f"logits: overlapping rows (shape {tuple(shape)}, strides "
                              f"{tuple(logits.stride())})")
@@ -381,8 +385,9 @@ def ns_preference_loss_workspace_size(pairs: int, length: int, vocab: int) -> in
 def ns_preference_loss(logits, labels, ref_logps, beta: float = 0.1, label_smoothing: float = 0.0,
                        workspace=None):
     """Preference loss of paired sequences from the policy's logits (2 pairs,
-    length, vocab; a slice such as logits[:, :-1] is fine), the labels (2 pairs, length; a position whose label is not
-    in the vocabulary, such as -100, does not count) and the reference's log
+    length, vocab; a slice such as logits[:, :-1] is fine, time-major logits
+    are not), the labels (2 pairs, length; a position whose label is not in
+    the vocabulary, such as -100, does not count) and the reference's log
     probability of each sequence (2 pairs, fp32). Returns fp32 tensors
     (losses, margins, logps, lse): the loss and margin of each pair, the
     policy's log probability of each sequence, and each position's log sum of
