@@ -166,11 +166,10 @@ __device__ __forceinline__ float scale_of(float top) {
 
 // A workgroup goes round the rows (by teams) and has the next row's loads in
 // flight while it reduces and writes the present one; the weights stay in
-// registers where they fit.
+// registers (V is 1 or 2).
 template <Width S, class T, class H, int TEAM, int V>
 __global__ __launch_bounds__(block_of(TEAM)) void rms_norm_kernel(RmsArgs a, int y_type, bool w32) {
   constexpr int TEAMS = block_of(TEAM) / TEAM, STRIDE = TEAM * VEC;
-  constexpr bool KEEP = V <= 2;
   __shared__ float red_sum[2][block_of(TEAM) / 64], red_max[block_of(TEAM) / 64];
   const int t = threadIdx.x % TEAM, team = threadIdx.x / TEAM, col0 = t * VEC;
   const int step = gridDim.x * TEAMS;
@@ -182,8 +181,8 @@ __global__ __launch_bounds__(block_of(TEAM)) void rms_norm_kernel(RmsArgs a, int
   Raw<H> rr[V];
   fetch_vecs<S, Use::ONCE>(x_of(row), a.dim, col0, STRIDE, rx);
   if (a.residual) fetch_vecs<S, Use::ONCE>(res_of(row), a.dim, col0, STRIDE, rr);
-  float w[KEEP ? V : 1][VEC];
-  if (KEEP) load_weight<S, T>(a.weight, w32, a.dim, col0, STRIDE, w);
+  float w[V][VEC];
+  load_weight<S, T>(a.weight, w32, a.dim, col0, STRIDE, w);
   int turn = 0;
   for (; row < a.rows; row += step, turn ^= 1) {
     float v[V][VEC];
@@ -218,12 +217,9 @@ __global__ __launch_bounds__(block_of(TEAM)) void rms_norm_kernel(RmsArgs a, int
     const float rstd = 1.f / sqrtf(team_sum<TEAM>(ss, red_sum[turn]) / a.dim + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float late[1][VEC];
-      if (!KEEP) load_weight<S, T>(a.weight, w32, a.dim, j * STRIDE + col0, 0, late);
+    for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[j][e] = v[j][e] * rstd * (KEEP ? w[KEEP ? j : 0][e] : late[0][e]);
-    }
+      for (int e = 0; e < VEC; ++e) v[j][e] = v[j][e] * rstd * w[j][e];
     if (y_type == OUT_E4M3) {
       float top = 0.f;
 #pragma unroll
