@@ -238,6 +238,14 @@ struct Clear {
 };
 constexpr int CLEAR_STEP = 256 * VEC * 4;   // elements of a workgroup
 
+// How a table's gradient is stored. Non-temporal in 16 bits, where a wave's
+// store is whole lines (160 to 190 us for the zeros of 1.05 GB). In fp32 a lane's
+// eight elements are two stores, each of every second 16 bytes of its lines: past
+// the caches those take 449 us for the same bytes, through them, which join the
+// halves, 182; 64000 rows of 4096 with 8192 tokens are 498 us in all and 240.
+template <class T>
+constexpr Use TABLE = sizeof(T) == 2 ? Use::ONCE : Use::AGAIN;
+
 template <class T>
 __device__ __forceinline__ void clear_rows(T* table, int64_t ld, const Clear& c, int64_t block,
                                            int64_t blocks) {
@@ -248,7 +256,7 @@ __device__ __forceinline__ void clear_rows(T* table, int64_t ld, const Clear& c,
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t col = from + (j * 256 + threadIdx.x) * VEC;
-      if (col + VEC <= c.cols) store8<Use::ONCE>(table + row * ld + col, zero);
+      if (col + VEC <= c.cols) store8<TABLE<T>>(table + row * ld + col, zero);
       else if (col < c.cols) store8_upto(table + row * ld + col, static_cast<int>(c.cols - col), zero);
     }
   }
@@ -337,7 +345,7 @@ __global__ __launch_bounds__(256) void runs_kernel(EmbedGradArgs a, int tx_log2)
     float out[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) out[i] = fmaf(a.scale, sum[i], ADD ? base[i] : 0.f);
-    store8_upto<Use::ONCE>(static_cast<TO*>(a.grad) + which * a.ld_grad + col, left, out);
+    store8_upto<TABLE<TO>>(static_cast<TO*>(a.grad) + which * a.ld_grad + col, left, out);
   };
 #pragma unroll
   for (int u = 0; u < PLACES; ++u) {
