@@ -81,7 +81,7 @@ struct RmsArgs {
   int64_t ldx, ld_residual, ldh, ldy;
   int rows, dim;
   float eps;
-  bool stream;         // set by the launch: h is stored past the caches
+  bool stream;         // set by the launch: a 16-bit y, or h beside codes, is stored past the caches
 };
 // x_type, h_type (x_type or fp32), weight_type (x_type or fp32), y_type (any, or OUT_E4M3)
 hipError_t launch_rms_norm(RmsArgs a, int x_type, int h_type, int weight_type, int y_type,

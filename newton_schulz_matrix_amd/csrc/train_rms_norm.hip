@@ -203,7 +203,8 @@ __global__ __launch_bounds__(block_of(TEAM)) void rms_norm_kernel(RmsArgs a, int
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         H* h = static_cast<H*>(a.h) + row * a.ldh;
-        store_either<S>(a.stream && y_type == OUT_E4M3, h, a.dim, j * STRIDE + col0, v[j]);
+        store_either<S>(sizeof(H) == 2 && a.stream && y_type == OUT_E4M3, h, a.dim, j * STRIDE + col0,
+                        v[j]);
       }
     }
     float ss = 0.f;
@@ -556,10 +557,11 @@ hipError_t by_types(int type, int h_type, F f) {
 }  // namespace
 
 // Elements from which on a call with a residual stores one of its two outputs
-// non-temporally, a 16-bit y or, beside e4m3 codes, h: two large outputs push
-// the inputs and each other through the caches. 16384 rows of 4096 in bf16
+// non-temporally, a 16-bit y or, beside e4m3 codes, a 16-bit h: two large outputs
+// push the inputs and each other through the caches. 16384 rows of 4096 in bf16
 // take 83 us so (both non-temporal 98, none 101), with codes 78 (none 92).
-// Without a residual it costs (49 us instead of 45).
+// Without a residual it costs (49 us instead of 45), and in fp32, where a wave's
+// store is not whole lines (8192 rows with codes: 86 us, 81 without).
 constexpr int64_t STREAM_ELEMS = int64_t{1} << 23;
 
 hipError_t launch_rms_norm(RmsArgs a, int x_type, int h_type, int weight_type, int y_type,
