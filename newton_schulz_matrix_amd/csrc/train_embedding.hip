@@ -18,8 +18,8 @@
 //
 // 16384 tokens of 4096 columns in bf16, 128000 rows: the lookup takes 34 us
 // (each row of the table is read once and found in the caches after that:
-// 6.4 TB/s), the gradient 235 to 240 us for 1.18 GB: 10 for the sort, 160 to
-// 180 for the clearing, which writes at 6 to 6.6 TB/s, 36 to 55 for the runs.
+// 6.4 TB/s), the gradient 235 to 240 us for 1.18 GB: 9 to 12 for the sort, 160
+// to 190 for the clearing (1.05 GB at 5.5 to 6.6 TB/s), 36 to 55 for the runs.
 #include <algorithm>
 
 #include "train_device.h"
@@ -67,7 +67,8 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int tx_log2
     widen_at(raw[r], table + row[r] * a.ld_table, a.dim, col, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] = used[r] ? v[e] * a.scale : 0.f;
-    // a large output (R > 1) does not stay in the L2 caches anyway
+    // a large output (R > 1) does not stay in the L2 caches anyway: 16384 rows of
+    // 4096 take 34 us so in bf16 (37 cached) and 80 in fp32 (90)
     store8_upto<R == 1 ? Use::AGAIN : Use::ONCE>(static_cast<TO*>(a.out) + i * a.ld_out + col,
                                                  a.dim - col, v);
   }
@@ -84,12 +85,17 @@ constexpr int SORT_BATCH = 16;     // windows of 64 ids loaded together
 // bits are g. It counts them per slot, and how many ids belong to groups
 // before it, so it knows where its part of `sorted` begins without hearing
 // from another workgroup; then it goes over the ids again and puts each
-// position in its place. Every workgroup reads all ids: they are a thousandth
-// of the gradient's bytes and come from the caches, and up to 16384 of them
-// are read once and stay in registers in between. Each wave takes a
-// contiguous part of the ids and keeps its own counters, so positions of one
-// id stay in order. 16384 ids take 8 to 11 us, most of it the latency of a
-// launch, two rounds of loads and three barriers; 65536 take 36.
+// position in its place. Each wave takes a contiguous part of the ids and
+// keeps its own counters, so positions of one id stay in order.
+//
+// Every workgroup reads all ids, from the caches, once up to 16384 of them
+// (they stay in registers in between) and twice above. Groups grow with the
+// table, from 256 up to 131072 rows to 16384 at 2^23, so the time goes as rows
+// times ids: made for batches of up to some 65536 ids, whose rows of hundreds of
+// columns and more take longer. 128000 rows: 16384 ids 9 to 12 us, most of it the
+// latency of a launch, two rounds of loads and three barriers, 65536 ids 29 to
+// 36, 2^20 ids 353. 2^18 rows, 2^20 ids: 629; 2^23 rows: 2^18 ids 4.4 ms, 2^20 17,
+// 2^23 135.
 template <class I>
 __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(EmbedGradArgs a) {
   extern __shared__ int counters[];            // (SORT_WAVES, range)
@@ -268,7 +274,7 @@ __device__ __forceinline__ void clear_rows(T* table, int64_t ld, const Clear& c,
 // window after (row 2 w + 1). A run is then the sum of its windows' rows: an id
 // that a tenth of the places name is summed by many workgroups, with no serial
 // remainder. The other workgroups clear the table in the order of the
-// addresses: 1 GB is written at 5.8 to 6.7 TB/s so, at 5.4 by fewer
+// addresses: 1.05 GB is written at 5.5 to 6.6 TB/s so, 1 GB at 5.4 by fewer
 // workgroups that go round.
 template <class T, class TO>
 __global__ __launch_bounds__(256) void window_clear_kernel(EmbedGradArgs a, int tx_log2,

@@ -158,8 +158,11 @@ __device__ __forceinline__ void store_y(const RmsArgs& a, int y_type, int row, i
   }
 }
 
-// A row's scale for its largest |y|. Dividing by it makes that one 448, by
-// two roundings more at most, which still rounds to the code of 448: no clamp.
+// A row's scale for its largest |y|. The codes are those of y times its rounded
+// reciprocal, which makes the largest 448, by three roundings more at most: that
+// still rounds to the code of 448, no clamp. A quotient within a rounding of fp32 of
+// the middle between two codes may take either; dividing instead decides 2886 of
+// 67 million codes otherwise, no nearer to 64 bits (2.6e-2 both), in 82 us, not 78.
 __device__ __forceinline__ float scale_of(float top) {
   return top > 0.f ? fmaxf(top / E4M3_MAX, SCALE_MIN) : 1.f;
 }

@@ -307,7 +307,8 @@ def ns_rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, h=N
 
 def ns_rms_norm_fp8(x, weight, residual=None, eps: float = 1e-6, h=None):
     """ns_rms_norm with the output as e4m3 codes and one fp32 scale for each
-    row (y is code * scale). Returns (codes, scales, h, rstd)."""
+    row: codes are those of y * (1 / scale), code * scale stands for y.
+    Returns (codes, scales, h, rstd)."""
     dev = _device_of(x, "x")
     q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
