@@ -439,6 +439,156 @@ ns_status ns_preference_loss_grad(const ns_preference_args* args, const float* m
                                   const float* lse, const float* dlosses, void* dlogits,
                                   int64_t ld_dlogits, void* stream);
 
+/* Log probabilities of given tokens, with the entropy of each row of logits and
+ * its likeliest entries:
+ *   lse[r] = log sum_v exp z[r][v]
+ *   logps[r] = z[r][token] - lse[r]
+ *   entropy[r] = - sum_v p[r][v] log p[r][v],   p = exp(z - lse)
+ *   top_logps[r][k], top_ids[r][k]: the k-th likeliest entry (k < top), its
+ *     z - lse and its index; of equal values the lowest index comes first.
+ * A row counts if its token lies in [0, vocab); the logits of other rows are
+ * not read, and their outputs are 0, their top_ids -1. An entry of -inf has no
+ * share in the sums and comes last among the likeliest; -0 equals 0. A NaN or
+ * +inf among a row's logits makes its lse, entropy and log probabilities NaN (a
+ * NaN is never among the likeliest; where fewer than top entries are left, the
+ * ids behind them are -1), and a row of nothing but -inf has lse -inf and NaN
+ * for the others.
+ *   logits  (rows, vocab), ld >= vocab;   tokens  (rows);
+ *   logps, lse, entropy  (rows) fp32;
+ *   top_logps  (rows, top) fp32, top_ids  (rows, top) of the tokens' type;
+ *              both NULL if top == 0.
+ * The gradient call takes lse and entropy of the forward call and the gradients
+ * of each row's log probability and entropy (NULL: none), and writes every
+ * element of
+ *   dlogits[r][v] = dlogps[r] ([v == token] - p) - dentropy[r] p (log p + entropy[r])
+ * (0 in rows that do not count) of logits' type, ld_dlogits >= vocab; dlogits
+ * may be the logits' own buffer with ld_dlogits == ld. entropy may be NULL
+ * without dentropy. (In fp32, lse's own rounding puts up to |lse| 2^-24, relative,
+ * on a row.)
+ * 0 <= rows <= NS_MAX_ROWS (0 is a no-op), 1 <= vocab <= NS_MAX_ROWS,
+ * 0 <= top <= min(vocab, NS_MAX_TOP); the gradient ignores top. Workspace of the
+ * forward call: ns_token_logps_workspace_size bytes, 256-byte aligned. */
+#define NS_MAX_TOP 64
+typedef struct {
+  const void* logits;
+  const void* tokens;
+  int64_t rows, vocab, ld, top;
+  ns_dtype dtype;
+  ns_id_type token_type;
+} ns_token_logps_args;
+ns_status ns_token_logps_workspace_size(int64_t rows, int64_t vocab, int64_t top, size_t* bytes);
+ns_status ns_token_logps(const ns_token_logps_args* args, float* logps, float* lse, float* entropy,
+                         float* top_logps, void* top_ids, void* ws, size_t ws_bytes, void* stream);
+ns_status ns_token_logps_grad(const ns_token_logps_args* args, const float* lse,
+                              const float* entropy, const float* dlogps, const float* dentropy,
+                              void* dlogits, int64_t ld_dlogits, void* stream);
+
+/* A tensor of heads, (tokens, heads, dim): element (t, h, d) at
+ * t * ld_token + h * ld_head + d. Queries, keys and values may be parts of one
+ * projection's output (tokens, heads of all, dim), and a call's outputs parts of
+ * one buffer. Of a tensor that is written, heads must not overlap: either
+ * ld_head >= dim and ld_token >= (heads - 1) * ld_head + dim, or ld_token >= dim
+ * and ld_head >= (tokens - 1) * ld_token + dim (one token or head: its stride
+ * does not count). One that is only read may have any strides from 0 on
+ * (a head or token that is repeated). */
+typedef struct {
+  void* data;                    /* const for an input */
+  int64_t ld_token, ld_head;
+} ns_heads;
+
+/* RMS norm of each query's and each key's head, with the rotation of its
+ * position in the same pass:
+ *   u = x * rstd * weight,  rstd = 1 / sqrt(mean(x^2) + eps)     (u = x without weights)
+ *   (y[a], y[b]) = (u[a] cos t - u[b] sin t, u[b] cos t + u[a] sin t)
+ * for the rotary / 2 pairs (a, b) of the first `rotary` columns: (i, i + rotary / 2),
+ * or, with interleaved != 0, (2 i, 2 i + 1); the columns behind them stay u. The
+ * angle of pair i at a token is t = position * inv_freq[i], taken in 64 bits,
+ * where position is the token's on the axis that i belongs to: with `axes` axes
+ * (time, height, width, ...) the pairs are cut into that many sections, one
+ * behind the other (sections[k] pairs of axis k, all together rotary / 2; with
+ * one axis sections is not read).
+ *   q, q_out  (tokens, q_heads, dim);  k, k_out  (tokens, k_heads, dim): all of
+ *             one type; q_out may be q itself (same strides), k_out k;
+ *   q_weight, k_weight  (dim), of that type or fp32; both or neither;
+ *   positions (axes, tokens) int32 or int64, rows ld_positions apart;
+ *   inv_freq  (rotary / 2) fp32 (NULL if rotary == 0).
+ * The gradient call takes q, k as they went in (the norm is worked out again,
+ * nothing is kept) and the gradients of the outputs, and writes
+ *   with g = the gradient turned back by its angle and n = x * rstd:
+ *   dq, dk  = rstd * (g * weight - n * mean(g * weight * n))   (g without weights)
+ *   dq_weight, dk_weight = sum over tokens and heads of g * n   (dim), any type, or NULL
+ * dq may be dq_out's own buffer, dk dk_out's (same strides). Without weights q and
+ * k are not read and may be NULL. Sums are added in a fixed order.
+ * 0 <= tokens <= NS_MAX_ROWS (0: the gradient of the weights is 0), 1 <= heads <=
+ * NS_MAX_HEADS each, dim a multiple of 4 up to 256, rotary a multiple of 4 from 0
+ * to dim, 1 <= axes <= 4, eps finite and >= 0. Sizes that are multiples of 16 are
+ * fastest. Workspace of the gradient call: ns_qk_norm_rope_grad_workspace_size
+ * bytes, 256-byte aligned. */
+#define NS_MAX_HEADS 1024
+typedef struct {
+  ns_heads q, k;
+  const void* q_weight;
+  const void* k_weight;
+  const void* positions;
+  const float* inv_freq;
+  int64_t tokens, q_heads, k_heads, dim, rotary, ld_positions;
+  int64_t axes, sections[4];
+  int interleaved;
+  ns_dtype dtype, weight_dtype;
+  ns_id_type position_type;
+  float eps;
+} ns_qk_norm_rope_args;
+ns_status ns_qk_norm_rope(const ns_qk_norm_rope_args* args, ns_heads q_out, ns_heads k_out,
+                          void* stream);
+ns_status ns_qk_norm_rope_grad_workspace_size(int64_t tokens, int64_t dim, size_t* bytes);
+ns_status ns_qk_norm_rope_grad(const ns_qk_norm_rope_args* args, ns_heads dq_out, ns_heads dk_out,
+                               ns_heads dq, ns_heads dk, void* dq_weight, void* dk_weight,
+                               ns_dtype dweight_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Causal attention over packed sequences with grouped heads. Sequence b is the
+ * rows offsets[b] .. offsets[b + 1] - 1; query head h reads key head
+ * h / (q_heads / k_heads). For a query i and the keys j <= i of its sequence:
+ *   S[i][j] = scale * q[i] . k[j],   P = softmax of a row,   out[i] = sum_j P[i][j] v[j]
+ *   lse[h][i] = log sum_j exp S[i][j]
+ *   q, out  (tokens, q_heads, dim);  k, v  (tokens, k_heads, dim): bf16 or fp16, all
+ *            of one type;
+ *   offsets (sequences + 1) int32 on the device, rising from 0 (equal neighbours:
+ *            an empty sequence); values outside [0, tokens] are taken as the
+ *            nearer end, and where they do not rise no row outside the tensors is
+ *            touched, but which values rows get is not said;
+ *   lse     (q_heads, tokens) fp32.
+ * Rows behind the last sequence are not read; of out and lse (of the gradients)
+ * they stay as they are, or, with clear_rest != 0, become 0. A NaN or infinity in a
+ * row of a sequence may reach earlier rows of the same sequence within 128 of
+ * it, never another sequence.
+ * S, the softmax and all sums are fp32; P and, in the gradient, P and dS are
+ * rounded to the tensors' type for the products with v, dout, k and q (fp16: scaled
+ * into its range first).
+ * The gradient call takes out and lse of the forward call and the gradient of out,
+ * and writes
+ *   delta[i] = dout[i] . out[i],   dS = P (dout v^T - delta)
+ *   dv = P^T dout,   dq = scale dS k,   dk = scale dS^T q
+ * (dk and dv summed over the heads of a group). Nothing depends on the order in
+ * which the device runs: results are reproducible.
+ * 0 <= tokens <= NS_MAX_ROWS (0 is a no-op), 0 <= sequences <= NS_MAX_ROWS, 1 <= k_heads,
+ * q_heads a multiple of it up to NS_MAX_HEADS, dim a multiple of 8 up to 128; scale finite
+ * and > 0. All tensors 16-byte aligned with strides that are multiples of 8; a
+ * tensor's ld_token >= dim (also of one that is only read) and at most 2^23. Workspace
+ * of the gradient call: ns_attention_grad_workspace_size bytes, 256-byte aligned. */
+typedef struct {
+  ns_heads q, k, v;
+  const int32_t* offsets;
+  int64_t tokens, sequences, q_heads, k_heads, dim;
+  ns_dtype dtype;
+  int clear_rest;
+  float scale;
+} ns_attention_args;
+ns_status ns_attention(const ns_attention_args* args, ns_heads out, float* lse, void* stream);
+ns_status ns_attention_grad_workspace_size(int64_t tokens, int64_t q_heads, size_t* bytes);
+ns_status ns_attention_grad(const ns_attention_args* args, ns_heads dout, ns_heads out,
+                            const float* lse, ns_heads dq, ns_heads dk, ns_heads dv, void* ws,
+                            size_t ws_bytes, void* stream);
+
 /* AdamW step of `count` tensors, in place, one launch for up to 32 of them:
  *   m <- beta1 m + (1 - beta1) g
  *   v <- beta2 v + (1 - beta2) g^2

@@ -9,7 +9,8 @@ Names follow the C ABI: ``ns_normalize``, ``ns_gram``, ``ns_direct``,
 ``ns_batched``, ``ns_workspace_size``, plus the building blocks ``ns_syrk``
 and ``ns_gemm_nt`` and the diagnostics ``ns_backend_info`` /
 ``ns_status_string``. The operators around the matrix update (embedding, RMS
-norm, preference loss, AdamW) are in ``operators`` and exported here.
+norm, preference loss, token log probabilities, AdamW) are in ``operators``,
+those on heads in ``heads``; both are exported here.
 
 The coefficient tables are the two 5-step sets of the DMuon page
 "Newton-Schulz 变体", section "系数集" (coefficient sets), as printed there;
@@ -158,6 +159,7 @@ def library() -> ctypes.CDLL:
                               vp, sz, ctypes.c_int, ctypes.c_char_p, sz],
         }
         sigs.update(operators.SIGNATURES)
+        sigs.update(heads.SIGNATURES)
         for name, args in sigs.items():
             f = getattr(lib, name)
             f.argtypes = args
@@ -675,3 +677,5 @@ class NewtonSchulz:
 
 from . import operators  # noqa: E402  (needs the names above)
 from .operators import *  # noqa: E402,F401,F403
+from . import heads  # noqa: E402
+from .heads import *  # noqa: E402,F401,F403

@@ -20,7 +20,9 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libnsmi.so")
 SOURCES = ["ns_api.hip", "norm_kernels.hip", "gemm_kernels.hip",
            "train_api.hip", "train_embedding.hip", "train_rms_norm.hip",
-           "train_preference.hip", "train_adamw.hip"]
+           "train_preference.hip", "train_adamw.hip", "train_logps.hip",
+           "heads_api.hip", "train_qk_norm.hip", "train_attention.hip",
+           "train_attention_grad.hip"]
 ARCH = "gfx950"
 
 COMPILE_FLAGS = [

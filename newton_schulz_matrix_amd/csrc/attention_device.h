@@ -1,0 +1,294 @@
+// Device helpers of attention and its gradient: tiles of rows in LDS, matrix
+// instructions on them, and where a workgroup's tile lies in the sequences.
+//
+// Matrix instructions are 32 x 32 x 16. Lane l holds of A the row l % 32 and of B
+// the column l % 32, each at k = 8 (l / 32) .. + 7, and of the result column
+// l % 32 in register r the row 8 (r / 4) + 4 (l / 32) + r % 4. A result that goes
+// on as the B operand of a next product therefore needs no exchange between lanes:
+// registers 8 c .. 8 c + 7 are its k chunk c, if the A operand brings its k in the
+// same order, which is four rows from 16 c + 4 (l / 32) and four from 8 further on.
+//
+// A tile is ROWS rows of DP 16-bit values, DP 64 or 128; columns past the head's
+// own are zeros. Its 16-byte chunk c of row r lies at chunk c ^ swizzle(r) of the
+// row, which spreads both ways of reading over all banks: 16 rows of one chunk,
+// and (transposed) four rows of four chunks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "heads_internal.h"
+
+namespace nsmi {
+
+typedef float Acc __attribute__((ext_vector_type(16)));
+typedef uint32_t U32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t U32x4 __attribute__((ext_vector_type(4)));
+typedef int I32x4 __attribute__((ext_vector_type(4)));
+typedef short S16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char LdsChar;
+
+template <class T>
+struct Eight {
+  typedef T type __attribute__((ext_vector_type(8)));
+};
+typedef Eight<_Float16>::type Half8;
+typedef Eight<__bf16>::type Brain8;
+
+__device__ __forceinline__ Acc product(Half8 a, Half8 b, Acc c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ Acc product(Brain8 a, Brain8 b, Acc c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ Acc no_sum() {
+  Acc a;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = 0.f;
+  return a;
+}
+
+// Registers 8 c .. 8 c + 7 of a result as the operand of a next product.
+template <class T>
+__device__ __forceinline__ typename Eight<T>::type operand(const Acc& a, int c) {
+  typename Eight<T>::type v;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = static_cast<T>(a[8 * c + i]);
+  return v;
+}
+
+// Value of the other half of the wave (lane l ^ 32) beside one's own.
+__device__ __forceinline__ void both_halves(float v, float& lower, float& upper) {
+  const uint32_t x = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  const uint32_t low = r[0], high = r[1];   // (a cast of an element itself takes the first)
+  lower = __builtin_bit_cast(float, low);
+  upper = __builtin_bit_cast(float, high);
+}
+
+// ------------------------------------------------------------------ tiles
+
+template <int DP>
+struct Tile {
+  static constexpr int CHUNKS = DP / 8;        // of a row
+  static constexpr int ROW = DP * 2;           // bytes
+  static constexpr int ROWS_A_COPY = 64 / CHUNKS;   // rows of one wave's copy instruction
+
+  __device__ static __forceinline__ int swizzle(int row) {
+    if (DP == 128) return (row & 3) << 2 | (row >> 2 & 3);
+    return (row >> 1 & 1) << 2 | (row >> 2 & 3);
+  }
+};
+
+// Buffer descriptor: reads past `bytes` return zeros. Every word is wave-uniform.
+__device__ __forceinline__ I32x4 descriptor(const void* p, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  I32x4 r = {__builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(a))),
+             __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(a >> 32) & 0xffff)),
+             __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00020000};
+  return r;
+}
+
+// Copies 16 (4) bytes a lane from memory to LDS: lane i's land at `lds` + 16 i (4 i).
+// In inline assembly, so that the only waits for them are copies_done()'s: the
+// compiler would wait for every copy in flight before any LDS read.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void copy16(I32x4 from, uint32_t lds, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(at), "s"(from) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(I32x4 from, uint32_t lds, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(at), "s"(from) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+__device__ __forceinline__ void copies_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
+}
+
+// A workgroup's copy of ROWS rows of a head into a tile: WAVES waves, each with
+// every WAVES-th copy instruction.
+template <int DP, int ROWS, int WAVES>
+struct Copier {
+  static constexpr int N = ROWS / Tile<DP>::ROWS_A_COPY / WAVES;   // instructions of a wave
+  uint32_t at[N];      // this lane's byte offset from the tile's first row
+  uint32_t lds;        // of the wave's first instruction, from the tile
+
+  // `step`: bytes from one row to the next; dim: the head's own columns.
+  __device__ __forceinline__ Copier(int wave, int lane, uint32_t step, int dim) {
+    constexpr int C = Tile<DP>::CHUNKS;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = (i * WAVES + wave) * Tile<DP>::ROWS_A_COPY + lane / C;
+      const int chunk = (lane % C) ^ Tile<DP>::swizzle(row);
+      at[i] = 8 * chunk < dim ? row * step + 16 * chunk : 0x80000000u;   // past every descriptor
+    }
+    lds = __builtin_amdgcn_readfirstlane(wave * 1024);
+  }
+  // `rows`: how many of the tile's rows there are.
+  __device__ __forceinline__ void copy(const void* first, int rows, uint32_t step, int dim,
+                                       uint32_t tile) const {
+    const int n = min(rows, ROWS);
+    const I32x4 from = descriptor(first, n > 0 ? (n - 1) * step + 2 * dim : 0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) copy16(from, tile + lds + i * WAVES * 1024, at[i]);
+  }
+};
+
+// This lane's offsets for reading rows: A (or B) operand of rows row .. row + 31 at
+// columns 16 k .. + 15 is at row * ROW + at[k].
+template <int DP>
+struct RowReader {
+  uint32_t at[DP / 16];
+  __device__ __forceinline__ explicit RowReader(int lane) {
+    const int row = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k)
+      at[k] = row * Tile<DP>::ROW + (((2 * k + half) ^ Tile<DP>::swizzle(row)) << 4);
+  }
+  template <class T>
+  __device__ __forceinline__ typename Eight<T>::type read(const LdsChar* tile, int row, int k) const {
+    const U32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) U32x4*>(
+        tile + row * Tile<DP>::ROW + at[k]);
+    return __builtin_bit_cast(typename Eight<T>::type, v);
+  }
+};
+
+// The same for reading transposed: A operand whose rows are columns 32 t .. + 31 and
+// whose k are rows 16 c .. + 15, in the order of a result's registers.
+// ds_read_b64_tr_b16: within each 16 lanes, lane j supplies the address of four
+// consecutive values M[j][0..3]; lane i receives M[4 q + i / 4][i % 4] in slot q.
+template <int DP>
+struct ColumnReader {
+  uint32_t at[DP / 32][2];
+  __device__ __forceinline__ explicit ColumnReader(int lane) {
+    const int j = lane & 15, group = lane >> 4;
+    const int half = group >> 1;
+#pragma unroll
+    for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int row = 8 * u + 4 * half + (j >> 2);
+        const int column = 32 * t + 16 * (group & 1) + 4 * (j & 3);
+        at[t][u] = row * Tile<DP>::ROW + (((column >> 3) ^ Tile<DP>::swizzle(row)) << 4) + (column & 4) * 2;
+      }
+  }
+  template <class T>
+  __device__ __forceinline__ typename Eight<T>::type read(const LdsChar* tile, int c, int t) const {
+    const LdsChar* p = tile + 16 * c * Tile<DP>::ROW;
+    const S16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) S16x4*)(p + at[t][0]));
+    const S16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) S16x4*)(p + at[t][1]));
+    const U32x2 a = __builtin_bit_cast(U32x2, x), b = __builtin_bit_cast(U32x2, y);
+    const U32x4 v = {a[0], a[1], b[0], b[1]};
+    return __builtin_bit_cast(typename Eight<T>::type, v);
+  }
+};
+
+// This lane's B operands of 32 rows of a head from memory (row: the lane's own, null
+// where there is none): k chunk k holds its columns 16 k + 8 (l / 32) .. + 7.
+template <class T, int DP>
+__device__ __forceinline__ void load_operands(const T* row, int dim, int half,
+                                              typename Eight<T>::type (&v)[DP / 16]) {
+#pragma unroll
+  for (int k = 0; k < DP / 16; ++k) {
+    const int column = 16 * k + 8 * half;
+    U32x4 x = {0, 0, 0, 0};
+    if (row && column < dim) x = *reinterpret_cast<const U32x4*>(row + column);
+    v[k] = __builtin_bit_cast(typename Eight<T>::type, x);
+  }
+}
+
+// Stores a result whose columns are rows of a head (row: the lane's own, null where
+// there is none) and whose rows are the head's columns, times `by`. The halves of the
+// wave exchange four values each, so that every store is 16 bytes.
+template <class T, int DP>
+__device__ __forceinline__ void store_columns(T* row, int dim, int half, const Acc (&a)[DP / 32], float by) {
+#pragma unroll
+  for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      T x[4], y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = static_cast<T>(a[t][4 * g + e] * by);
+        y[e] = static_cast<T>(a[t][4 * g + 4 + e] * by);
+      }
+      U32x2 p, q;
+      __builtin_memcpy(&p, x, 8);
+      __builtin_memcpy(&q, y, 8);
+      const auto r0 = __builtin_amdgcn_permlane32_swap(p[0], q[0], false, false);
+      const auto r1 = __builtin_amdgcn_permlane32_swap(p[1], q[1], false, false);
+      const U32x4 v = {r0[0], r1[0], r0[1], r1[1]};
+      const int column = 32 * t + 8 * (g + half);
+      if (row && column < dim) *reinterpret_cast<U32x4*>(row + column) = v;
+    }
+}
+
+// --------------------------------------------------------------- sequences
+
+// Offsets as they may be used whatever they hold: within the tokens.
+__device__ __forceinline__ int offset_at(const int* offsets, int b, int tokens) {
+  return min(max(offsets[b], 0), tokens);
+}
+
+// Where tile `t` of ROWS rows lies: tiles of sequence b begin at number
+// offsets[b] / ROWS + b, which leaves room for each sequence's own without a
+// count of them; b == sequences stands for the rows behind the last. The lanes of
+// a wave look through 64 places at a time. Numbers without rows have length 0.
+struct Place {
+  int begin, length, row;   // of the sequence; the tile's first row in it
+  bool rest;                // behind the last sequence
+};
+template <int ROWS>
+__device__ __forceinline__ Place place_of(const int* offsets, int sequences, int tokens, int t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = sequences + 1;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64, b = lo + lane * step;
+    const bool before = b < hi && offset_at(offsets, b, tokens) / ROWS + b <= t;
+    const int n = max(1, __popcll(__ballot(before)));
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  Place p;
+  p.begin = offset_at(offsets, lo, tokens);
+  const int end = lo < sequences ? offset_at(offsets, lo + 1, tokens) : tokens;
+  p.row = (t - p.begin / ROWS - lo) * ROWS;
+  p.rest = lo == sequences;
+  p.length = p.row >= 0 && p.row < end - p.begin ? end - p.begin : 0;
+  return p;
+}
+inline int64_t tiles_of(int64_t tokens, int64_t sequences, int rows) {
+  return tokens / rows + sequences + 1;
+}
+
+// Which head and tile a workgroup takes. Workgroups go to the eight XCDs in turn,
+// each with an L2 of its own: heads that read the same keys and values go to one
+// XCD, one behind the other, where the number of key heads allows it; tiles of the
+// ends of sequences, which are the longest, come first.
+struct Work {
+  int head, tile;
+};
+__device__ __forceinline__ Work work_of(int64_t block, int q_heads, int k_heads, int tiles) {
+  const int group = q_heads / k_heads;
+  int64_t n = block;
+  int kh;
+  if (k_heads % 8 == 0) {
+    kh = n % 8;
+    n /= 8;
+    const int g = n % group;
+    n /= group;
+    kh += 8 * (n % (k_heads / 8));
+    n /= k_heads / 8;
+    return {kh * group + g, static_cast<int>(tiles - 1 - n)};
+  }
+  return {static_cast<int>(n % q_heads), static_cast<int>(tiles - 1 - n / q_heads)};
+}
+
+}  // namespace nsmi

@@ -1,0 +1,69 @@
+// Launch interfaces of the operators on heads, (tokens, heads, dim) tensors:
+// norm of queries and keys with their rotation (train_qk_norm.hip) and
+// attention (train_attention.hip, train_attention_grad.hip), shared by their
+// C ABI (heads_api.hip) and their kernels. Not part of the C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/ns.h"
+
+namespace nsmi {
+
+// ------------------------------------- norm and rotation of queries and keys
+
+constexpr int QK_MAX_DIM = 256;
+constexpr int QK_AXES = 4;
+
+// The queries' or the keys' part of a call.
+struct QkPart {
+  const void* x;
+  const void* dy;      // gradient only
+  void* out;           // y, or dx
+  const void* weight;  // NULL: no norm
+  int64_t x_token, x_head, dy_token, dy_head, out_token, out_head;
+  int heads;
+};
+struct QkArgs {
+  QkPart part[2];      // queries, keys
+  const void* positions;       // (axes, tokens)
+  const float* inv_freq;
+  int64_t ld_positions;
+  int first[QK_AXES];  // first pair that turns with each axis (pairs, where there is no such axis)
+  int tokens, dim, rotary;
+  bool positions64, interleaved, weight32;
+  float eps;
+};
+hipError_t launch_qk_norm_rope(const QkArgs& a, int type, hipStream_t stream);
+// partial: (blocks, 2, dim), each workgroup's share of the weights' gradients
+int qk_grad_blocks(int64_t tokens);
+hipError_t launch_qk_norm_rope_grad(const QkArgs& a, int type, float* partial, void* dq_weight,
+                                    void* dk_weight, int dweight_type, hipStream_t stream);
+
+// -------------------------------------------------------------- attention
+
+constexpr int ATTN_MAX_DIM = 128;
+
+// A (tokens, heads, dim) tensor.
+struct HeadsAt {
+  void* p;
+  int64_t token, head;
+};
+struct AttnArgs {
+  HeadsAt q, k, v, out;
+  HeadsAt dout, dq, dk, dv;    // gradient only
+  float* lse;                  // (q_heads, tokens)
+  float* lse2;                 // lse log2(e), gradient only
+  float* delta;                // (q_heads, tokens), gradient only
+  const int* offsets;          // (sequences + 1)
+  int tokens, sequences, q_heads, k_heads, dim;
+  bool clear_rest;
+  float scale;
+};
+hipError_t launch_attention(const AttnArgs& a, int type, hipStream_t stream);
+// peaks: two words, fp16 only
+hipError_t launch_attention_grad(const AttnArgs& a, int type, uint32_t* peaks, hipStream_t stream);
+
+}  // namespace nsmi

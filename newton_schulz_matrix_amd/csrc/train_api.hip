@@ -7,63 +7,8 @@
 #include <cmath>
 
 #include "../../include/ns.h"
+#include "train_checks.h"
 #include "train_internal.h"
-
-#define NS_API extern "C" __attribute__((visibility("default")))
-
-namespace nsmi {
-namespace {
-
-constexpr size_t ALIGN = 256;
-size_t align_up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
-
-bool type_ok(int t) { return t == NS_DT_F32 || t == NS_DT_BF16 || t == NS_DT_F16; }
-size_t type_bytes(int t) { return t == NS_DT_E4M3 ? 1 : t == NS_DT_F32 ? 4 : 2; }
-bool ids_ok(int t) { return t == NS_IDS_I32 || t == NS_IDS_I64; }
-size_t id_bytes(int t) { return t == NS_IDS_I64 ? 8 : 4; }
-
-// Types that go with `type`: itself or fp32.
-bool same_or_f32(int t, int type) { return t == type || t == NS_DT_F32; }
-
-// A device buffer: (rows, cols) elements of `es` bytes, leading dimension ld.
-struct Span {
-  uintptr_t first, last;
-};
-Span span(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t es) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  if (!p || rows < 1 || cols < 1) return {a, a};
-  return {a, a + (static_cast<uintptr_t>(rows - 1) * ld + cols) * es};
-}
-bool overlap(Span x, Span y) { return x.first < y.last && y.first < x.last; }
-
-// Whether any of the written ranges meets a read one or another written one.
-template <int W, int R>
-bool clash(const Span (&out)[W], const Span (&in)[R]) {
-  for (int i = 0; i < W; ++i) {
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i], out[j])) return true;
-    for (int j = 0; j < R; ++j)
-      if (overlap(out[i], in[j])) return true;
-  }
-  return false;
-}
-
-bool aligned(const void* p, size_t es) { return reinterpret_cast<uintptr_t>(p) % es == 0; }
-bool rows_ok(int64_t r) { return r >= 0 && r <= NS_MAX_ROWS; }
-bool dim_ok(int64_t d) { return d >= 1 && d <= NS_MAX_DIM; }
-// Leading dimensions up to this keep every byte offset of a call in 63 bits.
-constexpr int64_t MAX_LD = int64_t{1} << 36;
-bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= MAX_LD; }
-
-ns_status from_hip(hipError_t e) { return e == hipSuccess ? NS_OK : NS_ERR_HIP; }
-
-// Workspace given, large enough and aligned.
-bool workspace_ok(const void* ws, size_t have, size_t need) {
-  return ws && have >= need && reinterpret_cast<uintptr_t>(ws) % ALIGN == 0;
-}
-
-}  // namespace
-}  // namespace nsmi
 
 using namespace nsmi;
 
@@ -411,6 +356,111 @@ NS_API ns_status ns_preference_loss_grad(const ns_preference_args* p, const floa
                                          margins, lse, dlosses, dlogits, ld_dlogits,
                                          in_place ? sequence_ld(*p) : p->length * ld_dlogits,
                                          static_cast<hipStream_t>(stream)));
+}
+
+// ------------------------------------------------- token log probabilities
+
+namespace nsmi {
+namespace {
+bool logps_sizes_ok(int64_t rows, int64_t vocab, int64_t top) {
+  return rows_ok(rows) && rows_ok(vocab) && vocab >= 1 && top >= 0 && top <= NS_MAX_TOP && top <= vocab;
+}
+struct LogpsPlan {
+  PrefSplit split;
+  size_t entries, total;   // byte offset, bytes
+};
+LogpsPlan logps_plan(int64_t rows, int64_t vocab, int64_t top) {
+  LogpsPlan p;
+  p.split = logps_split(rows, vocab, static_cast<int>(top));
+  const size_t parts = p.split.pieces > 1 ? static_cast<size_t>(rows) * p.split.pieces : 0;
+  p.entries = align_up(sizeof(LogpsPart) * parts);
+  p.total = std::max(ALIGN, align_up(p.entries + sizeof(uint64_t) * parts * top));
+  return p;
+}
+ns_status check_logps(const ns_token_logps_args* p) {
+  if (!p || !type_ok(p->dtype) || !ids_ok(p->token_type)) return NS_ERR_INVALID_ARG;
+  if (!logps_sizes_ok(p->rows, p->vocab, p->top) || !ld_ok(p->ld, p->vocab)) return NS_ERR_INVALID_ARG;
+  if (p->rows > 0 && (!p->logits || !p->tokens || !aligned(p->logits, type_bytes(p->dtype)) ||
+                      !aligned(p->tokens, id_bytes(p->token_type))))
+    return NS_ERR_INVALID_ARG;
+  return NS_OK;
+}
+LogpsArgs logps_args(const ns_token_logps_args& p) {
+  LogpsArgs a{};
+  a.logits = p.logits;
+  a.tokens = p.tokens;
+  a.ld = p.ld;
+  a.rows = static_cast<int>(p.rows);
+  a.vocab = static_cast<int>(p.vocab);
+  a.top = static_cast<int>(p.top);
+  a.tokens64 = p.token_type == NS_IDS_I64;
+  return a;
+}
+}  // namespace
+}  // namespace nsmi
+
+NS_API ns_status ns_token_logps_workspace_size(int64_t rows, int64_t vocab, int64_t top, size_t* bytes) {
+  if (!bytes || !logps_sizes_ok(rows, vocab, top)) return NS_ERR_INVALID_ARG;
+  *bytes = logps_plan(rows, vocab, top).total;
+  return NS_OK;
+}
+
+NS_API ns_status ns_token_logps(const ns_token_logps_args* p, float* logps, float* lse, float* entropy,
+                                float* top_logps, void* top_ids, void* ws, size_t ws_bytes,
+                                void* stream) {
+  ns_status s = check_logps(p);
+  if (s != NS_OK) return s;
+  if (p->rows == 0) return NS_OK;
+  const size_t ie = id_bytes(p->token_type);
+  if (!logps || !lse || !entropy || (p->top > 0) != (top_logps != nullptr) ||
+      (p->top > 0) != (top_ids != nullptr))
+    return NS_ERR_INVALID_ARG;
+  if (!aligned(logps, 4) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(top_logps, 4) ||
+      !aligned(top_ids, ie))
+    return NS_ERR_INVALID_ARG;
+  const LogpsPlan plan = logps_plan(p->rows, p->vocab, p->top);
+  const int64_t rows = p->rows;
+  const Span writes[] = {floats(logps, rows), floats(lse, rows), floats(entropy, rows),
+                         span(top_logps, rows, p->top, p->top, 4),
+                         span(top_ids, rows, p->top, p->top, ie),
+                         span(ws, 1, plan.total, plan.total, 1)};
+  const Span reads[] = {span(p->logits, rows, p->vocab, p->ld, type_bytes(p->dtype)),
+                        span(p->tokens, 1, rows, rows, ie)};
+  if (clash(writes, reads)) return NS_ERR_INVALID_ARG;
+  if (!workspace_ok(ws, ws_bytes, plan.total)) return NS_ERR_WORKSPACE;
+  s = device_status();
+  if (s != NS_OK) return s;
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  return from_hip(launch_token_logps(logps_args(*p), p->dtype, plan.split,
+                                     reinterpret_cast<LogpsPart*>(w),
+                                     reinterpret_cast<uint64_t*>(w + plan.entries),
+                                     {logps, lse, entropy, top_logps, top_ids},
+                                     static_cast<hipStream_t>(stream)));
+}
+
+NS_API ns_status ns_token_logps_grad(const ns_token_logps_args* p, const float* lse,
+                                     const float* entropy, const float* dlogps, const float* dentropy,
+                                     void* dlogits, int64_t ld_dlogits, void* stream) {
+  ns_status s = check_logps(p);
+  if (s != NS_OK) return s;
+  if (!ld_ok(ld_dlogits, p->vocab)) return NS_ERR_INVALID_ARG;
+  if (p->rows == 0) return NS_OK;
+  const size_t es = type_bytes(p->dtype);
+  if (!lse || !dlogits || (dentropy && !entropy) || !aligned(lse, 4) || !aligned(entropy, 4) ||
+      !aligned(dlogps, 4) || !aligned(dentropy, 4) || !aligned(dlogits, es))
+    return NS_ERR_INVALID_ARG;
+  const int64_t rows = p->rows;
+  const bool in_place = dlogits == p->logits && ld_dlogits == p->ld;
+  const Span none = {0, 0};
+  const Span writes[] = {span(dlogits, rows, p->vocab, ld_dlogits, es)};
+  const Span reads[] = {in_place ? none : span(p->logits, rows, p->vocab, p->ld, es),
+                        span(p->tokens, 1, rows, rows, id_bytes(p->token_type)), floats(lse, rows),
+                        floats(entropy, rows), floats(dlogps, rows), floats(dentropy, rows)};
+  if (clash(writes, reads)) return NS_ERR_INVALID_ARG;
+  s = device_status();
+  if (s != NS_OK) return s;
+  return from_hip(launch_token_logps_grad(logps_args(*p), p->dtype, lse, entropy, dlogps, dentropy,
+                                          dlogits, ld_dlogits, static_cast<hipStream_t>(stream)));
 }
 
 // -------------------------------------------------------------------- AdamW

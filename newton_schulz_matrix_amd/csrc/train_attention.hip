@@ -1,0 +1,174 @@
+// Causal attention over packed sequences with grouped heads.
+//
+//   S = scale q k^T (keys up to the query's own position), out = softmax(S) v,
+//   lse = log sum exp S
+//
+// Bound by the matrix units, and close behind them by the exponentials. A
+// workgroup takes 128 queries of one head, 32 a wave, and goes over the keys up
+// to its last query in tiles of 64, with the running maximum and sum of each row. Products are
+// taken transposed (keys x queries, columns x queries): a lane then holds one
+// query, a row's maximum and sum are its own registers and one exchange, and the
+// weights are the next product's operand as they stand. Keys and values come
+// into LDS directly, the next tile while this one is worked on.
+#include "attention_device.h"
+#include "train_device.h"
+#include "train_internal.h"
+
+namespace nsmi {
+namespace {
+
+constexpr int WAVES = 4, THREADS = 64 * WAVES;
+constexpr int QUERIES = 32 * WAVES;   // of a workgroup
+constexpr int KEYS = 64;              // of a tile
+
+// The weights of a row stand against a reference that trails its running maximum
+// by up to 2^LAG: the sums are rescaled only where it falls further behind. For fp16
+// the reference lies 2^7 lower, which keeps small weights out of its subnormals.
+constexpr float LAG = 8.f;
+template <class T>
+constexpr float LIFT = 0.f;
+template <>
+constexpr float LIFT<_Float16> = 7.f;
+
+// Rows behind the last sequence: zeros.
+template <class T>
+__device__ __forceinline__ void clear_rows(const AttnArgs& a, int head, int first, int last) {
+  T* out = static_cast<T*>(a.out.p) + head * a.out.head;
+  const int chunks = a.dim / 8, n = (last - first) * chunks;
+  const U32x4 zero = {0, 0, 0, 0};
+  for (int i = threadIdx.x; i < n; i += THREADS)
+    *reinterpret_cast<U32x4*>(out + (first + i / chunks) * a.out.token + i % chunks * 8) = zero;
+  for (int r = first + threadIdx.x; r < last; r += THREADS) a.lse[static_cast<int64_t>(head) * a.tokens + r] = 0.f;
+}
+
+template <class T, int DP>
+__global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int tiles) {
+  typedef typename Eight<T>::type V8;
+  constexpr int KC = DP / 16, DT = DP / 32;
+  constexpr int TILE = KEYS * Tile<DP>::ROW;
+  __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];   // keys, values, twice
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Work w = work_of(blockIdx.x, a.q_heads, a.k_heads, tiles);
+  const Place at = place_of<QUERIES>(a.offsets, a.sequences, a.tokens, w.tile);
+  if (at.length == 0) return;
+  if (at.rest) {
+    if (a.clear_rest) clear_rows<T>(a, w.head, at.begin + at.row, min(at.begin + at.row + QUERIES, at.begin + at.length));
+    return;
+  }
+  const int kv_head = w.head / (a.q_heads / a.k_heads);
+  const T* k = static_cast<const T*>(a.k.p) + at.begin * a.k.token + kv_head * a.k.head;
+  const T* v = static_cast<const T*>(a.v.p) + at.begin * a.v.token + kv_head * a.v.head;
+  const uint32_t k_step = static_cast<uint32_t>(a.k.token * 2), v_step = static_cast<uint32_t>(a.v.token * 2);
+  const Copier<DP, KEYS, WAVES> k_copy(wave, lane, k_step, a.dim), v_copy(wave, lane, v_step, a.dim);
+  const uint32_t lds = lds_address(smem);
+  const int keys = min(at.length, at.row + QUERIES);   // that any query here sees
+  const int steps = (keys + KEYS - 1) / KEYS;
+
+  auto fetch_tile = [&](int n) {
+    const uint32_t to = lds + (n & 1) * 2 * TILE;
+    const int first = n * KEYS;
+    k_copy.copy(k + first * a.k.token, at.length - first, k_step, a.dim, to);
+    v_copy.copy(v + first * a.v.token, at.length - first, v_step, a.dim, to + TILE);
+  };
+  fetch_tile(0);
+
+  const int first_query = at.row + 32 * wave, query = first_query + (lane & 31);
+  const bool there = query < at.length;
+  V8 q[KC];
+  load_operands<T, DP>(there ? static_cast<const T*>(a.q.p) + (at.begin + query) * a.q.token + w.head * a.q.head
+                             : nullptr,
+                       a.dim, half, q);
+  const RowReader<DP> rows(lane);
+  const ColumnReader<DP> columns(lane);
+  const float c = a.scale * 1.442695041f;   // weights as powers of two
+  Acc o[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) o[t] = no_sum();
+  float ref = -INFINITY, sum = 0.f;
+
+  for (int n = 0; n < steps; ++n) {
+    copies_done();
+    __syncthreads();   // tile n is there, and nobody reads the place of tile n + 1
+    if (n + 1 < steps) fetch_tile(n + 1);
+    const int first_key = n * KEYS;
+    if (first_key > first_query + 31) continue;
+    const LdsChar* const kt = (const LdsChar*)(smem) + (n & 1) * 2 * TILE;
+    const LdsChar* const vt = kt + TILE;
+    Acc s[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s[i] = no_sum();
+#pragma unroll
+      for (int j = 0; j < KC; ++j) s[i] = product(rows.template read<T>(kt, 32 * i, j), q[j], s[i]);
+    }
+    if (first_key + KEYS - 1 > first_query) {   // some keys lie behind some queries
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int key = first_key + 32 * i + 8 * (r / 4) + 4 * half + r % 4;
+          s[i][r] = key > query ? -INFINITY : s[i][r];
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[i][r]);
+    float lower, upper;
+    both_halves(top, lower, upper);
+    top = fmaxf(lower, upper) * c;
+    if (__any(top > ref + LAG + LIFT<T>)) {
+      const float to = fmaxf(ref, top - LIFT<T>);
+      const float by = __builtin_amdgcn_exp2f(ref - to);
+      ref = to;
+      sum *= by;
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[t][r] *= by;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[i][r] = __builtin_amdgcn_exp2f(fmaf(s[i][r], c, -ref));
+        sum += s[i][r];
+      }
+#pragma unroll
+    for (int j = 0; j < KEYS / 16; ++j) {
+      const V8 p = operand<T>(s[j / 2], j % 2);   // weights of at most 2^15, rounded to T: half a step each
+#pragma unroll
+      for (int t = 0; t < DT; ++t) o[t] = product(columns.template read<T>(vt, j, t), p, o[t]);
+    }
+  }
+
+  float lower, upper;
+  both_halves(sum, lower, upper);
+  sum = lower + upper;
+  T* out = static_cast<T*>(a.out.p) + (at.begin + query) * a.out.token + w.head * a.out.head;
+  store_columns<T, DP>(there ? out : nullptr, a.dim, half, o, 1.f / sum);
+  if (there && half == 0)
+    a.lse[static_cast<int64_t>(w.head) * a.tokens + at.begin + query] =
+        0.693147182f * (ref + __builtin_amdgcn_logf(sum));
+}
+
+}  // namespace
+
+hipError_t launch_attention(const AttnArgs& a, int type, hipStream_t stream) {
+  const int64_t tiles = tiles_of(a.tokens, a.sequences, QUERIES);
+  auto on = [&](auto t, auto dp) {
+    using T = decltype(t);
+    constexpr int DP = dp();
+    hipLaunchKernelGGL((attention_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.q_heads)), dim3(THREADS),
+                       0, stream, a, static_cast<int>(tiles));
+    return hipGetLastError();
+  };
+  auto shaped = [&](auto t) {
+    return a.dim <= 64 ? on(t, std::integral_constant<int, 64>{}) : on(t, std::integral_constant<int, 128>{});
+  };
+  return type == NS_DT_BF16 ? shaped(__bf16{}) : shaped(_Float16{});
+}
+
+}  // namespace nsmi

@@ -1,0 +1,319 @@
+// Gradient of causal attention over packed sequences with grouped heads.
+//
+//   P = exp(S - lse), S = scale q k^T;   delta = sum of dout out over a head's columns
+//   dv = P^T dout,  dS = P (dout v^T - delta),  dq = scale dS k,  dk = scale dS^T q
+//
+// Bound by the matrix units. Three launches: delta of each row; dk and dv, where a
+// workgroup keeps 128 keys of one key head and goes over the queries of its group's
+// heads behind them; dq, where it keeps 128 queries and goes over the keys before
+// them. S and dout v^T are worked out in both (seven products instead of five): the
+// alternative, adding to dq from every workgroup of keys, would need atomics, whose
+// order changes the sums, or a place for every pair of tiles. Everything is laid out
+// as in the forward pass: the weights of a lane are one row or column, and go on as
+// the next product's operand.
+//
+// fp16: weights and dS of a long row lie among its subnormals. Weights are taken
+// times 2^14, and dS times a power of two that keeps the largest one possible
+// (2 max |dout| max |v|, norms of a head's rows) below 2^15; both are taken back from
+// the sums in fp32.
+#include "attention_device.h"
+#include "train_device.h"
+#include "train_internal.h"
+
+namespace nsmi {
+namespace {
+
+constexpr int WAVES = 4, THREADS = 64 * WAVES;
+constexpr int ROWS = 32 * WAVES;      // queries or keys that a workgroup keeps
+constexpr int STEP = 64;              // rows of the tiles that it goes over
+constexpr float LOG2E = 1.442695041f;
+
+template <class T>
+constexpr bool NARROW = false;        // whether the type needs the scaling
+template <>
+constexpr bool NARROW<_Float16> = true;
+constexpr float LIFT = 14.f;
+
+// What dS is multiplied by, for fp16.
+__device__ __forceinline__ float ds_scale(const uint32_t* peaks) {
+  const float most = 2.f * __builtin_bit_cast(float, peaks[0]) * __builtin_bit_cast(float, peaks[1]);
+  if (!(most > 0.f && most < INFINITY)) return 1.f;
+  int e;
+  frexpf(most, &e);
+  return ldexpf(1.f, min(max(14 - e, -60), 60));
+}
+
+__global__ void clear_peaks_kernel(uint32_t* peaks) {
+  if (threadIdx.x < 2) peaks[threadIdx.x] = 0;
+}
+
+// Rows of heads: delta, and lse times log2(e) for the kernels below, 16 lanes a row,
+// 16 rows one behind the other a workgroup. For fp16 also the greatest norms of dout's
+// rows and v's; a maximum does not depend on the order in which it is taken.
+template <class T>
+__global__ __launch_bounds__(256) void delta_kernel(AttnArgs a, uint32_t* peaks) {
+  const int lane = threadIdx.x & 15;
+  const int token = blockIdx.x * 16 + threadIdx.x / 16, head = blockIdx.y;
+  const int first = offset_at(a.offsets, 0, a.tokens), last = offset_at(a.offsets, a.sequences, a.tokens);
+  const bool there = token >= first && token < last && 8 * lane < a.dim;
+  float dot = 0.f, norm = 0.f;
+  if (head < a.q_heads) {
+    if (there) {
+      float g[VEC], o[VEC];
+      load8(static_cast<const T*>(a.dout.p) + token * a.dout.token + head * a.dout.head + 8 * lane, g);
+      load8(static_cast<const T*>(a.out.p) + token * a.out.token + head * a.out.head + 8 * lane, o);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        dot = fmaf(g[e], o[e], dot);
+        norm = fmaf(g[e], g[e], norm);
+      }
+    }
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 64);
+    if (there && lane == 0) {
+      const int64_t at = static_cast<int64_t>(head) * a.tokens + token;
+      a.delta[at] = dot;
+      a.lse2[at] = a.lse[at] * LOG2E;
+    }
+  } else if (there) {
+    float x[VEC];
+    load8(static_cast<const T*>(a.v.p) + token * a.v.token + (head - a.q_heads) * a.v.head + 8 * lane, x);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) norm = fmaf(x[e], x[e], norm);
+  }
+  if constexpr (NARROW<T>) {
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) norm += __shfl_xor(norm, off, 64);
+    norm = wave_max(sqrtf(norm));   // (a NaN is passed over: its rows are NaN anyway)
+    if ((threadIdx.x & 63) == 0) atomicMax(peaks + (head < a.q_heads ? 0 : 1), __builtin_bit_cast(uint32_t, norm));
+  }
+}
+
+// Rows behind the last sequence: zeros.
+template <class T>
+__device__ __forceinline__ void clear_rows(const HeadsAt& to, int head, int dim, int first, int last) {
+  T* p = static_cast<T*>(to.p) + head * to.head;
+  const int chunks = dim / 8, n = (last - first) * chunks;
+  const U32x4 zero = {0, 0, 0, 0};
+  for (int i = threadIdx.x; i < n; i += THREADS)
+    *reinterpret_cast<U32x4*>(p + (first + i / chunks) * to.token + i % chunks * 8) = zero;
+}
+
+// ------------------------------------------------------------------------ dq
+
+template <class T, int DP>
+__global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32_t* peaks, int tiles) {
+  typedef typename Eight<T>::type V8;
+  constexpr int KC = DP / 16, DT = DP / 32;
+  constexpr int TILE = STEP * Tile<DP>::ROW;
+  __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];   // keys, values, twice
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Work w = work_of(blockIdx.x, a.q_heads, a.k_heads, tiles);
+  const Place at = place_of<ROWS>(a.offsets, a.sequences, a.tokens, w.tile);
+  if (at.length == 0) return;
+  if (at.rest) {
+    if (a.clear_rest)
+      clear_rows<T>(a.dq, w.head, a.dim, at.begin + at.row, min(at.begin + at.row + ROWS, at.begin + at.length));
+    return;
+  }
+  const int kv_head = w.head / (a.q_heads / a.k_heads);
+  const T* k = static_cast<const T*>(a.k.p) + at.begin * a.k.token + kv_head * a.k.head;
+  const T* v = static_cast<const T*>(a.v.p) + at.begin * a.v.token + kv_head * a.v.head;
+  const uint32_t k_step = static_cast<uint32_t>(a.k.token * 2), v_step = static_cast<uint32_t>(a.v.token * 2);
+  const Copier<DP, STEP, WAVES> k_copy(wave, lane, k_step, a.dim), v_copy(wave, lane, v_step, a.dim);
+  const uint32_t lds = lds_address(smem);
+  const int keys = min(at.length, at.row + ROWS);
+  const int steps = (keys + STEP - 1) / STEP;
+  auto fetch_tile = [&](int n) {
+    const uint32_t to = lds + (n & 1) * 2 * TILE;
+    const int first = n * STEP;
+    k_copy.copy(k + first * a.k.token, at.length - first, k_step, a.dim, to);
+    v_copy.copy(v + first * a.v.token, at.length - first, v_step, a.dim, to + TILE);
+  };
+  fetch_tile(0);
+
+  const int first_query = at.row + 32 * wave, query = first_query + (lane & 31);
+  const bool there = query < at.length;
+  const int64_t token = at.begin + query;
+  V8 q[KC], g[KC];
+  load_operands<T, DP>(there ? static_cast<const T*>(a.q.p) + token * a.q.token + w.head * a.q.head : nullptr,
+                       a.dim, half, q);
+  load_operands<T, DP>(there ? static_cast<const T*>(a.dout.p) + token * a.dout.token + w.head * a.dout.head : nullptr,
+                       a.dim, half, g);
+  const int64_t stat = static_cast<int64_t>(w.head) * a.tokens + token;
+  const float scaled = NARROW<T> ? ds_scale(peaks) : 1.f;
+  const float to_ds = NARROW<T> ? scaled * (1.f / 16384.f) : 1.f;
+  const float lse2 = (there ? a.lse2[stat] : 0.f) - (NARROW<T> ? LIFT : 0.f);
+  const float delta = (there ? a.delta[stat] : 0.f) * to_ds;
+  const RowReader<DP> rows(lane);
+  const ColumnReader<DP> columns(lane);
+  const float c = a.scale * LOG2E;
+  Acc dq[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) dq[t] = no_sum();
+
+  for (int n = 0; n < steps; ++n) {
+    copies_done();
+    __syncthreads();
+    if (n + 1 < steps) fetch_tile(n + 1);
+    const int first_key = n * STEP;
+    const LdsChar* const kt = (const LdsChar*)(smem) + (n & 1) * 2 * TILE;
+    const LdsChar* const vt = kt + TILE;
+#pragma unroll
+    for (int i = 0; i < STEP / 32; ++i) {
+      const int key0 = first_key + 32 * i;
+      if (key0 > first_query + 31) break;
+      Acc s = no_sum(), dp = no_sum();
+#pragma unroll
+      for (int j = 0; j < KC; ++j) s = product(rows.template read<T>(kt, 32 * i, j), q[j], s);
+#pragma unroll
+      for (int j = 0; j < KC; ++j) dp = product(rows.template read<T>(vt, 32 * i, j), g[j], dp);
+      const bool edge = key0 + 31 > first_query;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2));
+        const float d = p * (NARROW<T> ? fmaf(dp[r], to_ds, -delta) : dp[r] - delta);
+        const int key = key0 + 8 * (r / 4) + 4 * half + r % 4;
+        s[r] = edge && key > query ? 0.f : d;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const V8 ds = operand<T>(s, j);   // rounded to T, half a step each
+#pragma unroll
+        for (int t = 0; t < DT; ++t) dq[t] = product(columns.template read<T>(kt, 2 * i + j, t), ds, dq[t]);
+      }
+    }
+  }
+  T* to = static_cast<T*>(a.dq.p) + token * a.dq.token + w.head * a.dq.head;
+  store_columns<T, DP>(there ? to : nullptr, a.dim, half, dq, a.scale / scaled);
+}
+
+// ----------------------------------------------------------------- dk and dv
+
+template <class T, int DP>
+__global__ __launch_bounds__(THREADS, 2) void dkv_kernel(AttnArgs a, const uint32_t* peaks, int tiles) {
+  typedef typename Eight<T>::type V8;
+  constexpr int KC = DP / 16, DT = DP / 32;
+  constexpr int TILE = STEP * Tile<DP>::ROW, STATS = 2 * STEP * 4, STAGE = 2 * TILE + STATS;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];   // queries, dout, lse, delta, twice
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Work w = work_of(blockIdx.x, a.k_heads, a.k_heads, tiles);
+  const Place at = place_of<ROWS>(a.offsets, a.sequences, a.tokens, tiles - 1 - w.tile);   // the first are the longest
+  if (at.length == 0) return;
+  if (at.rest) {
+    if (a.clear_rest) {
+      const int first = at.begin + at.row, last = min(first + ROWS, at.begin + at.length);
+      clear_rows<T>(a.dk, w.head, a.dim, first, last);
+      clear_rows<T>(a.dv, w.head, a.dim, first, last);
+    }
+    return;
+  }
+  const int group = a.q_heads / a.k_heads;
+  const T* q = static_cast<const T*>(a.q.p) + at.begin * a.q.token + w.head * group * a.q.head;
+  const T* g = static_cast<const T*>(a.dout.p) + at.begin * a.dout.token + w.head * group * a.dout.head;
+  const int64_t stat0 = static_cast<int64_t>(w.head) * group * a.tokens + at.begin;
+  const uint32_t q_step = static_cast<uint32_t>(a.q.token * 2), g_step = static_cast<uint32_t>(a.dout.token * 2);
+  const Copier<DP, STEP, WAVES> q_copy(wave, lane, q_step, a.dim), g_copy(wave, lane, g_step, a.dim);
+  const uint32_t lds = lds_address(smem);
+  const int begin = at.row / STEP;
+  const int each = (at.length + STEP - 1) / STEP - begin, steps = each * group;   // each >= 1
+  auto fetch_tile = [&](int n) {
+    const uint32_t to = lds + (n & 1) * STAGE;
+    const int h = n / each, first = (begin + n - h * each) * STEP, rows = at.length - first;
+    q_copy.copy(q + h * a.q.head + first * a.q.token, rows, q_step, a.dim, to);
+    g_copy.copy(g + h * a.dout.head + first * a.dout.token, rows, g_step, a.dim, to + TILE);
+    if (wave < 2) {
+      const float* from = (wave == 0 ? a.lse2 : a.delta) + stat0 + static_cast<int64_t>(h) * a.tokens + first;
+      copy4(descriptor(from, 4 * min(rows, STEP)), to + 2 * TILE + wave * STEP * 4, 4 * lane);
+    }
+  };
+  fetch_tile(0);
+
+  const int first_key = at.row + 32 * wave, key = first_key + (lane & 31);
+  const bool there = key < at.length;
+  const int64_t token = at.begin + key;
+  V8 k[KC], v[KC];
+  load_operands<T, DP>(there ? static_cast<const T*>(a.k.p) + token * a.k.token + w.head * a.k.head : nullptr,
+                       a.dim, half, k);
+  load_operands<T, DP>(there ? static_cast<const T*>(a.v.p) + token * a.v.token + w.head * a.v.head : nullptr,
+                       a.dim, half, v);
+  const float scaled = NARROW<T> ? ds_scale(peaks) : 1.f;
+  const float to_ds = NARROW<T> ? scaled * (1.f / 16384.f) : 1.f;
+  const RowReader<DP> rows(lane);
+  const ColumnReader<DP> columns(lane);
+  const float c = a.scale * LOG2E;
+  Acc dk[DT], dv[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) dk[t] = dv[t] = no_sum();
+
+  for (int n = 0; n < steps; ++n) {
+    copies_done();
+    __syncthreads();
+    if (n + 1 < steps) fetch_tile(n + 1);
+    const int first_query = (begin + n % each) * STEP;
+    const LdsChar* const qt = (const LdsChar*)(smem) + (n & 1) * STAGE;
+    const LdsChar* const gt = qt + TILE;
+    const __attribute__((address_space(3))) float* const stats =
+        (const __attribute__((address_space(3))) float*)(gt + TILE);
+#pragma unroll
+    for (int i = 0; i < STEP / 32; ++i) {
+      const int query0 = first_query + 32 * i;
+      if (query0 + 31 < first_key) continue;
+      Acc s = no_sum(), dp = no_sum();
+#pragma unroll
+      for (int j = 0; j < KC; ++j) s = product(rows.template read<T>(qt, 32 * i, j), k[j], s);
+#pragma unroll
+      for (int j = 0; j < KC; ++j) dp = product(rows.template read<T>(gt, 32 * i, j), v[j], dp);
+      const bool edge = query0 < first_key + 31;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int at_row = 32 * i + 8 * (r / 4) + 4 * half + r % 4;
+        const float lse2 = stats[at_row] - (NARROW<T> ? LIFT : 0.f), delta = stats[STEP + at_row];
+        float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2));
+        float d = p * (NARROW<T> ? (dp[r] - delta) * to_ds : dp[r] - delta);
+        const bool hidden = edge && key > first_query + at_row;
+        s[r] = hidden ? 0.f : p;
+        dp[r] = hidden ? 0.f : d;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const V8 p = operand<T>(s, j), ds = operand<T>(dp, j);   // rounded to T, half a step each
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+          dv[t] = product(columns.template read<T>(gt, 2 * i + j, t), p, dv[t]);
+          dk[t] = product(columns.template read<T>(qt, 2 * i + j, t), ds, dk[t]);
+        }
+      }
+    }
+  }
+  T* to_k = static_cast<T*>(a.dk.p) + token * a.dk.token + w.head * a.dk.head;
+  T* to_v = static_cast<T*>(a.dv.p) + token * a.dv.token + w.head * a.dv.head;
+  store_columns<T, DP>(there ? to_k : nullptr, a.dim, half, dk, a.scale / scaled);
+  store_columns<T, DP>(there ? to_v : nullptr, a.dim, half, dv, NARROW<T> ? 1.f / 16384.f : 1.f);
+}
+
+}  // namespace
+
+hipError_t launch_attention_grad(const AttnArgs& a, int type, uint32_t* peaks, hipStream_t stream) {
+  const int64_t tiles = tiles_of(a.tokens, a.sequences, ROWS);
+  auto on = [&](auto t, auto dp) {
+    using T = decltype(t);
+    constexpr int DP = dp();
+    if (NARROW<T>) hipLaunchKernelGGL(clear_peaks_kernel, dim3(1), dim3(64), 0, stream, peaks);
+    hipLaunchKernelGGL(delta_kernel<T>, dim3((a.tokens + 15) / 16, a.q_heads + (NARROW<T> ? a.k_heads : 0)),
+                       dim3(256), 0, stream, a, peaks);
+    hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.k_heads)), dim3(THREADS), 0,
+                       stream, a, peaks, static_cast<int>(tiles));
+    hipLaunchKernelGGL((dq_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.q_heads)), dim3(THREADS), 0,
+                       stream, a, peaks, static_cast<int>(tiles));
+    return hipGetLastError();
+  };
+  auto shaped = [&](auto t) {
+    return a.dim <= 64 ? on(t, std::integral_constant<int, 64>{}) : on(t, std::integral_constant<int, 128>{});
+  };
+  return type == NS_DT_BF16 ? shaped(__bf16{}) : shaped(_Float16{});
+}
+
+}  // namespace nsmi

@@ -129,6 +129,36 @@ hipError_t launch_preference_grad(const PrefArgs& a, int type, bool labels64,
                                   void* dlogits, int64_t ld_dlogits, int64_t ld_dseq,
                                   hipStream_t stream);
 
+// ------------------------------------------------- token log probabilities
+
+constexpr int LOGPS_MAX_TOP = NS_MAX_TOP;
+constexpr int LOGPS_JOIN = 1024;      // entries of a row's pieces, all together, where they are asked for
+struct LogpsArgs {
+  const void* logits;
+  const void* tokens;
+  int64_t ld;
+  int rows, vocab, top;
+  bool tokens64;
+};
+struct LogpsOut {
+  float* logps;
+  float* lse;
+  float* entropy;
+  float* top_logps;    // (rows, top)
+  void* top_ids;       // (rows, top), of the tokens' type
+};
+// Maximum and sums of a piece of a row.
+struct LogpsPart {
+  double m, s, t;
+};
+PrefSplit logps_split(int64_t rows, int64_t vocab, int top);
+// entries: (rows, pieces, top)
+hipError_t launch_token_logps(const LogpsArgs& a, int type, const PrefSplit& sp, LogpsPart* parts,
+                              uint64_t* entries, const LogpsOut& o, hipStream_t stream);
+hipError_t launch_token_logps_grad(const LogpsArgs& a, int type, const float* lse, const float* entropy,
+                                   const float* dlogps, const float* dentropy, void* dlogits,
+                                   int64_t ld_dlogits, hipStream_t stream);
+
 // -------------------------------------------------------------- AdamW
 
 constexpr int ADAMW_TENSORS = 32;     // tensors of one launch (its table is a kernel argument)

@@ -1,0 +1,453 @@
+// RMS norm of each query's and key's head, with the rotation of its position in
+// the same pass, and the gradient of both.
+//
+//   rstd = 1 / sqrt(mean(x^2) + eps),  u = x rstd w
+//   (y_a, y_b) = (u_a cos t - u_b sin t, u_b cos t + u_a sin t),   t = position inv_freq
+//   gradient: g = dy turned back, n = x rstd:  dw = sum g n,
+//   dx = rstd (g w - n mean(g w n))
+//
+// Bound by memory. A head is the work of a team of lanes, each with two vectors of
+// W elements that hold W whole pairs: W from each half of the rotated part (or 2 W
+// in a row where pairs are neighbours), and two of the rest for the lanes behind.
+// A wave takes one token, several heads at a time, so that its lanes keep the
+// same pairs and the angles are worked out once for all heads of a token.
+#include <algorithm>
+
+#include "heads_internal.h"
+#include "train_device.h"
+#include "train_internal.h"
+
+namespace nsmi {
+namespace {
+
+constexpr int THREADS = 256, WAVES = THREADS / 64;
+constexpr int MAX_PAIRS = QK_MAX_DIM / 2;
+
+// W elements as loaded, from any element's address.
+typedef uint32_t Duo __attribute__((ext_vector_type(2), aligned(2), may_alias));
+typedef uint32_t Uno __attribute__((aligned(2), may_alias));
+template <int BYTES>
+struct Access {
+  typedef Quad type;
+};
+template <>
+struct Access<8> {
+  typedef Duo type;
+};
+template <>
+struct Access<4> {
+  typedef Uno type;
+};
+template <class T, int W>
+struct Part {
+  static constexpr int BYTES = sizeof(T) * W;
+  typedef typename Access<BYTES>::type A;
+  static constexpr int N = BYTES / sizeof(A);
+  A q[N];
+
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = reinterpret_cast<const A*>(p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) reinterpret_cast<A*>(p)[i] = q[i];
+  }
+  __device__ __forceinline__ void widen(float (&v)[W]) const {
+    T r[W];
+    __builtin_memcpy(r, q, sizeof(r));
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[e] = static_cast<float>(r[e]);
+  }
+  __device__ __forceinline__ void narrow(const float (&v)[W]) {
+    T r[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) r[e] = static_cast<T>(v[e]);
+    __builtin_memcpy(q, r, sizeof(r));
+  }
+};
+
+// What a lane is within its team: the columns of its two vectors, and whether
+// they hold pairs that turn.
+template <int W>
+struct Lane {
+  int a, b, pair;      // first columns, first pair
+  bool turns, there;   // else the vectors pass, or there are none
+  __device__ __forceinline__ Lane(const QkArgs& q, int j) {
+    const int turning = q.rotary / (2 * W);
+    turns = j < turning;
+    there = j < q.dim / (2 * W);
+    pair = turns ? W * j : 0;
+    if (turns && !q.interleaved) {
+      a = W * j;
+      b = q.rotary / 2 + W * j;
+    } else {
+      a = there ? 2 * W * j : 0;   // (rotary is 2 W times the lanes that turn)
+      b = a + W;
+    }
+  }
+};
+
+// sin and cos of a token's angles, one pair a lane, into LDS. The angle is
+// taken in turns and in 64 bits before its whole turns are dropped: at position
+// 10^6 an angle in 32 bits would be off by 0.03.
+template <class I>
+__device__ __forceinline__ void angles(const QkArgs& a, int64_t token, int lane, float2* table) {
+  const I* positions = static_cast<const I*>(a.positions);
+  for (int p = lane; p < a.rotary / 2; p += 64) {
+    int axis = 0;
+#pragma unroll
+    for (int k = 1; k < QK_AXES; ++k) axis += p >= a.first[k];
+    const double position = static_cast<double>(positions[axis * a.ld_positions + token]);
+    const double turns = position * static_cast<double>(a.inv_freq[p]) * 0.15915494309189533577;
+    float s, c;
+    sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
+    table[p] = make_float2(c, s);
+  }
+}
+__device__ __forceinline__ void angles_of(const QkArgs& a, int64_t token, int lane, float2* table) {
+  if (a.positions64) angles<int64_t>(a, token, lane, table);
+  else angles<int32_t>(a, token, lane, table);
+}
+
+template <int W>
+__device__ __forceinline__ void read_angles(const Lane<W>& l, const float2* table, float (&c)[W],
+                                            float (&s)[W]) {
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    const float2 t = table[l.pair + e];
+    c[e] = l.turns ? t.x : 1.f;
+    s[e] = l.turns ? t.y : 0.f;
+  }
+}
+
+// Turns the pairs of two vectors by (c, sign s).
+template <int W>
+__device__ __forceinline__ void turn(bool neighbours, float sign, const float (&c)[W],
+                                     const float (&s)[W], float (&a)[W], float (&b)[W]) {
+  if (neighbours) {
+#pragma unroll
+    for (int e = 0; e < W / 2; ++e) {
+      const float x = a[2 * e], y = a[2 * e + 1], u = b[2 * e], v = b[2 * e + 1];
+      const float sx = sign * s[e], su = sign * s[W / 2 + e];
+      a[2 * e] = x * c[e] - y * sx;
+      a[2 * e + 1] = y * c[e] + x * sx;
+      b[2 * e] = u * c[W / 2 + e] - v * su;
+      b[2 * e + 1] = v * c[W / 2 + e] + u * su;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      const float x = a[e], y = b[e], t = sign * s[e];
+      a[e] = x * c[e] - y * t;
+      b[e] = y * c[e] + x * t;
+    }
+  }
+}
+
+// Sum over the lanes of a team (a power of two of them).
+__device__ __forceinline__ float team_sum(float v, int team) {
+  for (int off = 1; off < team; off <<= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+template <class T, int W>
+__device__ __forceinline__ void weight_of(const void* w, bool w32, int at, float (&v)[W]) {
+  if (w32) {
+    Part<float, W> p;
+    p.load(static_cast<const float*>(w) + at);
+    p.widen(v);
+  } else {
+    Part<T, W> p;
+    p.load(static_cast<const T*>(w) + at);
+    p.widen(v);
+  }
+}
+
+// One wave a token and chunk of `rounds` rounds of heads. The loads of U rounds
+// are in flight before the angles are worked out.
+template <class T, int W>
+__global__ __launch_bounds__(THREADS) void qk_norm_kernel(QkArgs a, int team, int rounds, int chunks) {
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;
+  __shared__ float2 tables[WAVES][MAX_PAIRS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * WAVES + wave;
+  const int64_t token = unit / chunks;
+  if (token >= a.tokens) return;   // no barrier below: a wave's table is its own
+  const Lane<W> l(a, lane & (team - 1));
+  const int each = 64 / team, heads = a.part[0].heads + a.part[1].heads;
+  const int slot0 = static_cast<int>(unit - token * chunks) * rounds * each + lane / team;
+  float2* table = tables[wave];
+  float c[W], s[W];
+  for (int r0 = 0; r0 < rounds; r0 += U) {
+    Part<T, W> ra[U], rb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int slot = slot0 + (r0 + u) * each;
+      if (r0 + u < rounds && slot < heads && l.there) {
+        const bool key = slot >= a.part[0].heads;
+        const QkPart& p = a.part[key];
+        const T* x = static_cast<const T*>(p.x) + token * p.x_token +
+                     (slot - (key ? a.part[0].heads : 0)) * p.x_head;
+        ra[u].load(x + l.a);
+        rb[u].load(x + l.b);
+      } else {
+        ra[u] = {};
+        rb[u] = {};
+      }
+    }
+    if (r0 == 0) {
+      angles_of(a, token, lane, table);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      read_angles<W>(l, table, c, s);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int slot = slot0 + (r0 + u) * each;
+      if (r0 + u >= rounds) break;
+      const bool key = slot >= a.part[0].heads;
+      const QkPart& p = a.part[key];
+      float va[W], vb[W];
+      ra[u].widen(va);
+      rb[u].widen(vb);
+      if (a.part[0].weight) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < W; ++e) sum = fmaf(va[e], va[e], fmaf(vb[e], vb[e], sum));
+        const float rstd = rsqrtf(team_sum(sum, team) / static_cast<float>(a.dim) + a.eps);
+        if (l.there) {
+          float wa[W], wb[W];
+          weight_of<T>(p.weight, a.weight32, l.a, wa);
+          weight_of<T>(p.weight, a.weight32, l.b, wb);
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            va[e] *= rstd * wa[e];
+            vb[e] *= rstd * wb[e];
+          }
+        }
+      }
+      turn<W>(a.interleaved, 1.f, c, s, va, vb);
+      if (slot < heads && l.there) {
+        T* y = static_cast<T*>(p.out) + token * p.out_token +
+               (slot - (key ? a.part[0].heads : 0)) * p.out_head;
+        Part<T, W> o;
+        o.narrow(va);
+        o.store(y + l.a);
+        o.narrow(vb);
+        o.store(y + l.b);
+      }
+    }
+  }
+}
+
+// The gradient: waves take tokens in turn and keep their share of the weights'
+// gradients in registers; a workgroup adds its waves' shares at the end.
+template <class T, int W>
+__global__ __launch_bounds__(THREADS) void qk_grad_kernel(QkArgs a, int team, int rounds,
+                                                          float* partial) {
+  constexpr int U = sizeof(T) == 2 ? 2 : 1;
+  __shared__ float2 tables[WAVES][MAX_PAIRS];
+  __shared__ float shares[WAVES][2][QK_MAX_DIM];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool norm = a.part[0].weight != nullptr;
+  const Lane<W> l(a, lane & (team - 1));
+  const int each = 64 / team, heads = a.part[0].heads + a.part[1].heads;
+  float2* table = tables[wave];
+  float dw[2][2][W];   // queries and keys, the two vectors
+#pragma unroll
+  for (int i = 0; i < 4 * W; ++i) dw[i / (2 * W)][i / W % 2][i % W] = 0.f;
+  for (int64_t token = static_cast<int64_t>(blockIdx.x) * WAVES + wave; token < a.tokens;
+       token += static_cast<int64_t>(gridDim.x) * WAVES) {
+    float c[W], s[W];
+    for (int r0 = 0; r0 < rounds; r0 += U) {
+      Part<T, W> ga[U], gb[U], xa[U], xb[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int slot = (r0 + u) * each + lane / team;
+        ga[u] = gb[u] = xa[u] = xb[u] = {};
+        if (slot < heads && l.there) {
+          const bool key = slot >= a.part[0].heads;
+          const QkPart& p = a.part[key];
+          const int head = slot - (key ? a.part[0].heads : 0);
+          const T* dy = static_cast<const T*>(p.dy) + token * p.dy_token + head * p.dy_head;
+          ga[u].load(dy + l.a);
+          gb[u].load(dy + l.b);
+          if (norm) {
+            const T* x = static_cast<const T*>(p.x) + token * p.x_token + head * p.x_head;
+            xa[u].load(x + l.a);
+            xb[u].load(x + l.b);
+          }
+        }
+      }
+      if (r0 == 0) {
+        __builtin_amdgcn_wave_barrier();   // the last token's angles have been read
+        angles_of(a, token, lane, table);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        read_angles<W>(l, table, c, s);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int slot = (r0 + u) * each + lane / team;
+        const bool key = slot >= a.part[0].heads, mine = slot < heads && l.there;
+        const QkPart& p = a.part[key];
+        float va[W], vb[W];
+        ga[u].widen(va);
+        gb[u].widen(vb);
+        turn<W>(a.interleaved, -1.f, c, s, va, vb);
+        if (norm) {
+          float na[W], nb[W], sum = 0.f, dot = 0.f;
+          xa[u].widen(na);
+          xb[u].widen(nb);
+#pragma unroll
+          for (int e = 0; e < W; ++e) sum = fmaf(na[e], na[e], fmaf(nb[e], nb[e], sum));
+          const float rstd = rsqrtf(team_sum(sum, team) / static_cast<float>(a.dim) + a.eps);
+          float wa[W], wb[W];
+          if (mine) {
+            weight_of<T>(p.weight, a.weight32, l.a, wa);
+            weight_of<T>(p.weight, a.weight32, l.b, wb);
+          }
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            na[e] *= rstd;
+            nb[e] *= rstd;
+            const float da = va[e] * na[e], db = vb[e] * nb[e];
+            dw[0][0][e] += mine && !key ? da : 0.f;
+            dw[0][1][e] += mine && !key ? db : 0.f;
+            dw[1][0][e] += mine && key ? da : 0.f;
+            dw[1][1][e] += mine && key ? db : 0.f;
+            va[e] = mine ? va[e] * wa[e] : 0.f;
+            vb[e] = mine ? vb[e] * wb[e] : 0.f;
+            dot = fmaf(va[e], na[e], fmaf(vb[e], nb[e], dot));
+          }
+          const float mean = team_sum(dot, team) / static_cast<float>(a.dim);
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            va[e] = rstd * fmaf(-na[e], mean, va[e]);
+            vb[e] = rstd * fmaf(-nb[e], mean, vb[e]);
+          }
+        }
+        if (mine) {
+          T* dx = static_cast<T*>(p.out) + token * p.out_token +
+                  (slot - (key ? a.part[0].heads : 0)) * p.out_head;
+          Part<T, W> o;
+          o.narrow(va);
+          o.store(dx + l.a);
+          o.narrow(vb);
+          o.store(dx + l.b);
+        }
+      }
+    }
+  }
+  if (!norm) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        float v = dw[k][h][e];
+        for (int off = team; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
+        if (lane < team && l.there) shares[wave][k][(h ? l.b : l.a) + e] = v;
+      }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.dim; i += THREADS) {
+    const int k = i >= a.dim, col = i - k * a.dim;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) v += shares[w][k][col];
+    partial[static_cast<int64_t>(blockIdx.x) * 2 * a.dim + i] = v;
+  }
+}
+
+// dweight[c] = sum over the workgroups' shares, in 64 bits: 16 columns by 64 groups
+// of shares in a workgroup.
+constexpr int DW_COLS = 16, DW_GROUPS = 64;
+template <class TO>
+__global__ __launch_bounds__(DW_COLS * DW_GROUPS) void qk_dweight_kernel(const float* partial,
+                                                                         int blocks, int dim,
+                                                                         TO* dq, TO* dk) {
+  __shared__ double sums[DW_GROUPS][DW_COLS + 1];
+  const int tx = threadIdx.x % DW_COLS, ty = threadIdx.x / DW_COLS;
+  const int col = blockIdx.x * DW_COLS + tx;
+  double s = 0.0;
+  if (col < 2 * dim) {
+#pragma unroll 8
+    for (int b = ty; b < blocks; b += DW_GROUPS) s += partial[static_cast<int64_t>(b) * 2 * dim + col];
+  }
+  sums[ty][tx] = s;
+  __syncthreads();
+  if (ty != 0 || col >= 2 * dim) return;
+  for (int k = 1; k < DW_GROUPS; ++k) s += sums[k][tx];
+  TO* to = col < dim ? dq : dk;
+  if (to) to[col < dim ? col : col - dim] = static_cast<TO>(static_cast<float>(s));
+}
+
+// Calls f with the widest vectors that the sizes allow, as a type.
+template <class F>
+hipError_t by_vector(const QkArgs& a, F f) {
+  if (a.dim % 16 == 0 && a.rotary % 16 == 0) return f(std::integral_constant<int, 8>{});
+  if (a.dim % 8 == 0 && a.rotary % 8 == 0) return f(std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 2>{});
+}
+int team_of(int dim, int w) {
+  int team = 1;
+  while (team * 2 * w < dim) team *= 2;
+  return team;
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope(const QkArgs& a, int type, hipStream_t stream) {
+  return by_type(type, [&](auto t) {
+    using T = decltype(t);
+    return by_vector(a, [&](auto w) {
+      constexpr int W = w();
+      const int team = team_of(a.dim, W), each = 64 / team;
+      const int all = (a.part[0].heads + a.part[1].heads + each - 1) / each;
+      // few tokens: one round a wave; else all heads of a token, whose angles are shared
+      const int rounds = a.tokens < 2048 ? 1 : all;
+      const int chunks = (all + rounds - 1) / rounds;
+      const int64_t units = static_cast<int64_t>(a.tokens) * chunks;
+      hipLaunchKernelGGL((qk_norm_kernel<T, W>), dim3((units + WAVES - 1) / WAVES), dim3(THREADS), 0,
+                         stream, a, team, rounds, chunks);
+      return hipGetLastError();
+    });
+  });
+}
+
+int qk_grad_blocks(int64_t tokens) {
+  return static_cast<int>(std::min<int64_t>((tokens + WAVES - 1) / WAVES, 1024));
+}
+
+hipError_t launch_qk_norm_rope_grad(const QkArgs& a, int type, float* partial, void* dq_weight,
+                                    void* dk_weight, int dweight_type, hipStream_t stream) {
+  const int blocks = a.tokens > 0 ? qk_grad_blocks(a.tokens) : 0;
+  if (blocks > 0) {
+    const hipError_t e = by_type(type, [&](auto t) {
+      using T = decltype(t);
+      return by_vector(a, [&](auto w) {
+        constexpr int W = w();
+        const int team = team_of(a.dim, W), each = 64 / team;
+        const int rounds = (a.part[0].heads + a.part[1].heads + each - 1) / each;
+        hipLaunchKernelGGL((qk_grad_kernel<T, W>), dim3(blocks), dim3(THREADS), 0, stream, a, team,
+                           rounds, partial);
+        return hipGetLastError();
+      });
+    });
+    if (e != hipSuccess) return e;
+  }
+  if (!dq_weight && !dk_weight) return hipSuccess;
+  return by_type(dweight_type, [&](auto t) {
+    using TO = decltype(t);
+    hipLaunchKernelGGL(qk_dweight_kernel<TO>, dim3((2 * a.dim + DW_COLS - 1) / DW_COLS),
+                       dim3(DW_COLS * DW_GROUPS), 0, stream, partial, blocks, a.dim,
+                       static_cast<TO*>(dq_weight), static_cast<TO*>(dk_weight));
+    return hipGetLastError();
+  });
+}
+
+}  // namespace nsmi

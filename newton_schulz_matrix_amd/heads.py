@@ -1,0 +1,230 @@
+"""Operators on heads, tensors of shape (tokens, heads, dim) (see include/ns.h):
+the norm of queries and keys with the rotation of their positions, and causal
+attention over packed sequences, with their gradients.
+
+Argument marshalling in the manner of ``operators``; the package exports every
+name of this module. Queries, keys and values may be views of one projection's
+output, and the outputs that a call is given may be views of one buffer: any
+strides of tokens and heads are taken as long as the last dimension is
+contiguous and, in a tensor that is written, heads do not overlap.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Sequence
+
+from . import _check, _device_tensor, _dtype_code, library
+from .operators import (_code, _dense, _device_of, _f32, _given_or_new, _i64, _ids_type, _int, _mismatch,
+                        _size, _sized, _stream_of, _vp, torch)
+
+NS_MAX_HEADS = 1024
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", _vp), ("ld_token", _i64), ("ld_head", _i64)]
+
+
+class _QkNormRopeArgs(ctypes.Structure):
+    _fields_ = ([("q", _Heads), ("k", _Heads)]
+                + [(n, _vp) for n in ("q_weight", "k_weight", "positions", "inv_freq")]
+                + [(n, _i64) for n in ("tokens", "q_heads", "k_heads", "dim", "rotary", "ld_positions",
+                                       "axes")]
+                + [("sections", _i64 * 4)]
+                + [(n, _int) for n in ("interleaved", "dtype", "weight_dtype", "position_type")]
+                + [("eps", _f32)])
+
+
+class _AttentionArgs(ctypes.Structure):
+    _fields_ = ([(n, _Heads) for n in ("q", "k", "v")] + [("offsets", _vp)]
+                + [(n, _i64) for n in ("tokens", "sequences", "q_heads", "k_heads", "dim")]
+                + [("dtype", _int), ("clear_rest", _int), ("scale", _f32)])
+
+
+SIGNATURES = {
+    "ns_qk_norm_rope": [ctypes.POINTER(_QkNormRopeArgs), _Heads, _Heads, _vp],
+    "ns_qk_norm_rope_grad_workspace_size": [_i64, _i64, ctypes.POINTER(_size)],
+    "ns_qk_norm_rope_grad": [ctypes.POINTER(_QkNormRopeArgs), _Heads, _Heads, _Heads, _Heads, _vp, _vp,
+                             _int, _vp, _size, _vp],
+    "ns_attention": [ctypes.POINTER(_AttentionArgs), _Heads, _vp, _vp],
+    "ns_attention_grad_workspace_size": [_i64, _i64, ctypes.POINTER(_size)],
+    "ns_attention_grad": [ctypes.POINTER(_AttentionArgs), _Heads, _Heads, _vp, _Heads, _Heads, _Heads,
+                          _vp, _size, _vp],
+}
+
+
+def _heads_of(t, name: str, dev: int, shape=None, dtype=None) -> _Heads:
+    """A (tokens, heads, dim) tensor of this shape (and type) on device `dev`."""
+    if t.get_device() != dev or (shape is not None and t.shape != shape) or (
+            dtype is not None and t.dtype != dtype):
+        _mismatch(t, t.shape if shape is None else shape, name, dtype)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be (tokens, heads, dim), not {tuple(t.shape)}")
+    ld_token, ld_head, one = t.stride()
+    if one != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: heads must be contiguous (stride(-1) == 1)")
+    return _Heads(t.data_ptr(), ld_token, ld_head)
+
+
+def _new_or_heads(t, name: str, dev: int, like):
+    """An output of `like`'s shape and type: (tensor, its _Heads)."""
+    if t is None:
+        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return t, _heads_of(t, name, dev, like.shape, like.dtype)
+
+
+# ------------------------------------- norm and rotation of queries and keys
+
+def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, sections, interleaved, dev):
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError(f"q and k must be (tokens, heads, dim) of the same tokens and dim, not "
+                         f"{tuple(q.shape)} and {tuple(k.shape)}")
+    tokens, _, dim = q.shape
+    heads_q, heads_k = _heads_of(q, "q", dev), _heads_of(k, "k", dev, dtype=q.dtype)
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight: give both or neither")
+    weight_ptrs, weight_code = (None, None), 0
+    if q_weight is not None:
+        weight_ptrs = (_dense(q_weight, (dim,), "q_weight", dev),
+                       _dense(k_weight, (dim,), "k_weight", dev, q_weight.dtype))
+        weight_code = _code(q_weight)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be 1-D: one for each pair that turns")
+    pairs = inv_freq.shape[0]
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    parts = (_i64 * 4)()
+    if positions.dim() not in (1, 2) or positions.shape[-1] != tokens or axes > 4:
+        raise ValueError(f"positions must be (tokens,) or (axes, tokens) with up to 4 axes, not "
+                         f"{tuple(positions.shape)} for {tokens} tokens")
+    if axes > 1:
+        if sections is None or len(sections) != axes or sum(sections) != pairs or min(sections) < 0:
+            raise ValueError(f"sections must give the pairs of each of the {axes} axes, {pairs} in all")
+        parts[:axes] = list(sections)
+    elif sections is not None and list(sections) != [pairs]:
+        raise ValueError(f"sections: one axis has all {pairs} pairs")
+    if positions.get_device() != dev:
+        _device_tensor(positions, "positions")
+    if positions.stride(-1) != 1 and tokens > 1:
+        raise ValueError("positions: an axis' positions must be contiguous")
+    return _QkNormRopeArgs(heads_q, heads_k, *weight_ptrs, positions.data_ptr(),
+                           _dense(inv_freq, (pairs,), "inv_freq", dev, torch.float32), tokens, q.shape[1],
+                           k.shape[1], dim, 2 * pairs, positions.stride(0) if axes > 1 else 0, axes,
+                           parts, 1 if interleaved else 0, _code(q), weight_code,
+                           _ids_type(positions, "positions"), eps)
+
+
+def ns_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-6,
+                    sections: Optional[Sequence[int]] = None, interleaved: bool = False, out_q=None,
+                    out_k=None):
+    """RMS norm of each query's and key's head (q (tokens, q_heads, dim), k
+    (tokens, k_heads, dim)) with the rotation of its position in the same pass.
+    The first 2 * len(inv_freq) columns turn, in pairs (i, i + half) or, with
+    interleaved, (2 i, 2 i + 1), by the angle position * inv_freq[i] (taken in 64
+    bits). positions is (tokens,), int32 or int64, or (axes, tokens) with
+    `sections`, the number of pairs of each axis (such as time, height, width).
+    Weights are (dim,), of q's type or fp32; None for both leaves out the norm.
+    Returns (q, k); out_q may be q itself and out_k k, which the gradient then no
+    longer has."""
+    dev = _device_of(q, "q")
+    args = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, sections, interleaved, dev)
+    out_q, to_q = _new_or_heads(out_q, "out_q", dev, q)
+    out_k, to_k = _new_or_heads(out_k, "out_k", dev, k)
+    _check(library().ns_qk_norm_rope(args, to_q, to_k, _stream_of(dev)), "ns_qk_norm_rope")
+    return out_q, out_k
+
+
+def ns_qk_norm_rope_grad_workspace_size(tokens: int, dim: int) -> int:
+    return _sized("ns_qk_norm_rope_grad_workspace_size", tokens, dim)
+
+
+def ns_qk_norm_rope_grad(dout_q, dout_k, q, k, q_weight, k_weight, positions, inv_freq,
+                         eps: float = 1e-6, sections: Optional[Sequence[int]] = None,
+                         interleaved: bool = False, dq=None, dk=None, dweight_dtype=None,
+                         workspace=None):
+    """Gradients of ns_qk_norm_rope for the gradients of its outputs: (dq, dk,
+    dq_weight, dk_weight), the last two None without weights and of weights' type
+    unless dweight_dtype says so. q and k are the call's inputs. dq may be
+    dout_q's buffer and dk dout_k's, or both views of one larger buffer."""
+    dev = _device_of(q, "q")
+    args = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, sections, interleaved, dev)
+    g_q = _heads_of(dout_q, "dout_q", dev, q.shape, q.dtype)
+    g_k = _heads_of(dout_k, "dout_k", dev, k.shape, k.dtype)
+    dq, to_q = _new_or_heads(dq, "dq", dev, q)
+    dk, to_k = _new_or_heads(dk, "dk", dev, k)
+    if q_weight is None:
+        _check(library().ns_qk_norm_rope_grad(args, g_q, g_k, to_q, to_k, None, None, 0, None, 0,
+                                              _stream_of(dev)), "ns_qk_norm_rope_grad")
+        return dq, dk, None, None
+    dim = q.shape[2]
+    dweights = torch.empty((2, dim), dtype=dweight_dtype or q_weight.dtype, device=q.device)
+    dqw, dkw = dweights.unbind(0)
+    workspace = _given_or_new(workspace, ns_qk_norm_rope_grad_workspace_size(q.shape[0], dim), q.device)
+    _check(library().ns_qk_norm_rope_grad(args, g_q, g_k, to_q, to_k, dqw.data_ptr(), dkw.data_ptr(),
+                                          _code(dweights), workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(),
+                                          _stream_of(dev)), "ns_qk_norm_rope_grad")
+    return dq, dk, dqw, dkw
+
+
+# ------------------------------------------------------------------ attention
+
+def _attention_args(q, k, v, offsets, scale, clear_rest, dev):
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or q.shape[::2] != k.shape[::2]:
+        raise ValueError(f"q (tokens, q_heads, dim) and k, v (tokens, k_heads, dim) do not go together: "
+                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be 1-D: where each sequence begins, and the end of the last")
+    tokens, q_heads, dim = q.shape
+    return _AttentionArgs(_heads_of(q, "q", dev), _heads_of(k, "k", dev, dtype=q.dtype),
+                          _heads_of(v, "v", dev, dtype=q.dtype),
+                          _dense(offsets, offsets.shape, "offsets", dev, torch.int32), tokens,
+                          offsets.shape[0] - 1, q_heads, k.shape[1], dim, _code(q),
+                          1 if clear_rest else 0, dim ** -0.5 if scale is None else scale)
+
+
+def ns_attention(q, k, v, offsets, scale: Optional[float] = None, out=None):
+    """Causal attention of packed sequences: q (tokens, q_heads, dim), k and v
+    (tokens, k_heads, dim) in bf16 or fp16, q_heads a multiple of k_heads, dim a
+    multiple of 8 up to 128; offsets (sequences + 1) int32 on the device, where
+    each sequence begins and the last one ends (offsets[0] is 0). scale is
+    dim ** -0.5 by default. Returns (out, lse): out like q, and the log sum of
+    exponentials of each row, (q_heads, tokens) fp32, for the gradient. Rows
+    behind the last sequence are zeros in a new out, and left as they are in one
+    that is given; lse is 0 there in the first case and unset in the second."""
+    dev = _device_of(q, "q")
+    args = _attention_args(q, k, v, offsets, scale, out is None, dev)
+    out, to = _new_or_heads(out, "out", dev, q)
+    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    _check(library().ns_attention(args, to, lse.data_ptr(), _stream_of(dev)), "ns_attention")
+    return out, lse
+
+
+def ns_attention_grad_workspace_size(tokens: int, q_heads: int) -> int:
+    return _sized("ns_attention_grad_workspace_size", tokens, q_heads)
+
+
+def ns_attention_grad(dout, q, k, v, out, lse, offsets, scale: Optional[float] = None, dq=None, dk=None,
+                      dv=None, workspace=None):
+    """Gradients (dq, dk, dv) of ns_attention for the gradient of its out, with
+    out and lse as it returned them. dq, dk and dv may be given, all three, for
+    instance as views of one buffer: rows behind the last sequence are then left
+    as they are, and are zeros in new ones."""
+    dev = _device_of(q, "q")
+    if (dq is None) != (dk is None) or (dq is None) != (dv is None):
+        raise ValueError("dq, dk and dv: give all three or none")
+    args = _attention_args(q, k, v, offsets, scale, dq is None, dev)
+    tokens, q_heads, _ = q.shape
+    dq, to_q = _new_or_heads(dq, "dq", dev, q)
+    dk, to_k = _new_or_heads(dk, "dk", dev, k)
+    dv, to_v = _new_or_heads(dv, "dv", dev, v)
+    workspace = _given_or_new(workspace, ns_attention_grad_workspace_size(tokens, q_heads), q.device)
+    _check(library().ns_attention_grad(
+        args, _heads_of(dout, "dout", dev, q.shape, q.dtype), _heads_of(out, "out", dev, q.shape, q.dtype),
+        _dense(lse, (q_heads, tokens), "lse", dev, torch.float32), to_q, to_k, to_v, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_of(dev)), "ns_attention_grad")
+    return dq, dk, dv
+
+
+__all__ = ["NS_MAX_HEADS", "ns_qk_norm_rope", "ns_qk_norm_rope_grad",
+           "ns_qk_norm_rope_grad_workspace_size", "ns_attention", "ns_attention_grad",
+           "ns_attention_grad_workspace_size"]

@@ -1,8 +1,9 @@
 """Operators around the matrix update of a training step (see include/ns.h).
 
 ``ns_embedding`` and its gradient, ``ns_rms_norm`` / ``ns_rms_norm_fp8`` and
-their gradient, the preference loss on logits and its gradient, and the AdamW
-step of the parameters that the Newton-Schulz update does not take. Argument
+their gradient, the preference loss on logits and its gradient, the log
+probabilities of given tokens and their gradient, and the AdamW step of the
+parameters that the Newton-Schulz update does not take. Argument
 marshalling only, like the rest of the package, which exports every name of
 this module: tensors become pointers, outputs and workspaces come from torch,
 work goes to the current stream of the tensors' device. There is no autograd
@@ -65,6 +66,11 @@ class _PreferenceArgs(ctypes.Structure):
                 ("beta", _f32), ("label_smoothing", _f32), ("ld_sequence", _i64)]
 
 
+class _TokenLogpsArgs(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("tokens", _vp), ("rows", _i64), ("vocab", _i64), ("ld", _i64),
+                ("top", _i64), ("dtype", _int), ("token_type", _int)]
+
+
 class _AdamwTensor(ctypes.Structure):
     _fields_ = ([(n, _vp) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "master")]
                 + [("elems", _i64)]
@@ -85,6 +91,9 @@ SIGNATURES = {
     "ns_preference_loss": [ctypes.POINTER(_PreferenceArgs), _vp, _vp, _vp, _vp, _vp, _vp, _size,
                            _vp],
     "ns_preference_loss_grad": [ctypes.POINTER(_PreferenceArgs), _vp, _vp, _vp, _vp, _i64, _vp],
+    "ns_token_logps_workspace_size": [_i64, _i64, _i64, ctypes.POINTER(_size)],
+    "ns_token_logps": [ctypes.POINTER(_TokenLogpsArgs), _vp, _vp, _vp, _vp, _vp, _vp, _size, _vp],
+    "ns_token_logps_grad": [ctypes.POINTER(_TokenLogpsArgs), _vp, _vp, _vp, _vp, _vp, _i64, _vp],
     "ns_adamw_step": [ctypes.POINTER(_AdamwTensor), _int, _i64, _f64, _f64, _f64, _f64, _vp],
 }
 
@@ -435,6 +444,74 @@ def ns_preference_loss_grad(logits, labels, margins, lse, dlosses, beta: float =
     return out
 
 
+# --------------------------------------------------- token log probabilities
+
+def _token_logps_args(logits, tokens, top, dev):
+    if logits.dim() < 1:
+        raise ValueError("logits must have at least one dimension")
+    rows, vocab, ld = _rows_of(logits, "logits", dev)
+    return _TokenLogpsArgs(logits.data_ptr(), _dense(tokens, logits.shape[:-1], "tokens", dev), rows,
+                           vocab, ld, top, _code(logits), _ids_type(tokens, "tokens"))
+
+
+def ns_token_logps_workspace_size(rows: int, vocab: int, top: int = 0) -> int:
+    return _sized("ns_token_logps_workspace_size", rows, vocab, top)
+
+
+def ns_token_logps(logits, tokens, top: int = 0, workspace=None):
+    """Log probabilities of the tokens (int32 or int64, of any shape) from
+    logits of shape tokens.shape + (vocab,). Returns (logps, lse, entropy,
+    top_logps, top_ids): the first three are fp32 and of the tokens' shape, the
+    log sum of exponentials and entropy of each row are also what the gradient
+    needs; top_logps (fp32) and top_ids (of the tokens' type) are each row's
+    `top` (0 to 64) likeliest entries, of equal ones the lowest index first, of
+    shape tokens.shape + (top,), or None if top is 0. Rows whose token is not in
+    the vocabulary, such as -100, do not count: 0, and -1 in top_ids."""
+    dev = _device_of(logits, "logits")
+    tokens = tokens if tokens.is_contiguous() else tokens.contiguous()
+    args = _token_logps_args(logits, tokens, top, dev)
+    rows, shape, device = args.rows, logits.shape[:-1], logits.device
+    out = torch.empty(rows * 3, dtype=torch.float32, device=device)
+    top_logps = top_ids = logps_ptr = ids_ptr = None
+    if top > 0:
+        top_logps = torch.empty(shape + (top,), dtype=torch.float32, device=device)
+        top_ids = torch.empty(shape + (top,), dtype=tokens.dtype, device=device)
+        logps_ptr, ids_ptr = top_logps.data_ptr(), top_ids.data_ptr()
+    workspace = _given_or_new(workspace, ns_token_logps_workspace_size(rows, args.vocab, top), device)
+    at = out.data_ptr()
+    _check(library().ns_token_logps(args, at, at + 4 * rows, at + 8 * rows, logps_ptr, ids_ptr,
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _stream_of(dev)), "ns_token_logps")
+    logps, lse, entropy = out.view((3,) + shape).unbind(0)
+    return logps, lse, entropy, top_logps, top_ids
+
+
+def ns_token_logps_grad(logits, tokens, lse, entropy, dlogps, dentropy=None, out=None):
+    """Gradient of ns_token_logps's log probabilities and entropies with respect
+    to the logits, for lse and entropy as it returned them and the gradient of
+    each row's (fp32, of the tokens' shape; dlogps or dentropy may be None).
+    `out` may be the logits themselves."""
+    dev = _device_of(logits, "logits")
+    tokens = tokens if tokens.is_contiguous() else tokens.contiguous()
+    args = _token_logps_args(logits, tokens, 0, dev)
+    shape = logits.shape
+    if out is None:
+        out = torch.empty(shape, dtype=logits.dtype, device=logits.device)
+        ld_out = args.vocab
+    else:
+        ld_out = _like_rows(out, shape, "out", dev, logits.dtype)
+
+    def row(t, name):
+        return None if t is None else _dense(t, shape[:-1], name, dev, torch.float32)
+
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs the entropy")
+    _check(library().ns_token_logps_grad(args, row(lse, "lse"), row(entropy, "entropy"),
+                                         row(dlogps, "dlogps"), row(dentropy, "dentropy"),
+                                         out.data_ptr(), ld_out, _stream_of(dev)), "ns_token_logps_grad")
+    return out
+
+
 # ---------------------------------------------------------------------- AdamW
 
 def ns_adamw_step(params: List, grads: List, exp_avgs: List, exp_avg_sqs: List, step: int,
@@ -488,4 +565,5 @@ __all__ = ["NS_DT_E4M3", "NS_IDS_I32", "NS_IDS_I64", "NS_MAX_ROWS", "ns_embeddin
            "ns_embedding_grad", "ns_embedding_grad_workspace_size", "ns_rms_norm",
            "ns_rms_norm_fp8", "ns_rms_norm_grad", "ns_rms_norm_grad_workspace_size",
            "ns_preference_loss", "ns_preference_loss_grad", "ns_preference_loss_workspace_size",
+           "ns_token_logps", "ns_token_logps_grad", "ns_token_logps_workspace_size",
            "ns_adamw_step"]
