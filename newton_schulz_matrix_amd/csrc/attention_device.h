@@ -26,7 +26,6 @@ typedef uint32_t U32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t U32x4 __attribute__((ext_vector_type(4)));
 typedef int I32x4 __attribute__((ext_vector_type(4)));
 typedef short S16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) char LdsChar;
 
 template <class T>
 struct Eight {
@@ -113,19 +112,18 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // every WAVES-th copy instruction.
 template <int DP, int ROWS, int WAVES>
 struct Copier {
-  static constexpr int N = ROWS / Tile<DP>::ROWS_A_COPY / WAVES;   // instructions of a wave
-  uint32_t at[N];      // this lane's byte offset from the tile's first row
+  static constexpr int EACH = Tile<DP>::ROWS_A_COPY * WAVES;   // rows of an instruction of all waves
+  static constexpr int N = ROWS / EACH;                        // instructions of a wave
+  static_assert(EACH % 16 == 0 && N * EACH == ROWS, "the swizzle repeats with 16 rows");
+  uint32_t at;         // this lane's byte offset from the tile's first row, in the first instruction
   uint32_t lds;        // of the wave's first instruction, from the tile
 
-  // `step`: bytes from one row to the next; dim: the head's own columns.
+  // `step`: bytes from one row to the next, at most 2^24; dim: the head's own columns.
   __device__ __forceinline__ Copier(int wave, int lane, uint32_t step, int dim) {
     constexpr int C = Tile<DP>::CHUNKS;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int row = (i * WAVES + wave) * Tile<DP>::ROWS_A_COPY + lane / C;
-      const int chunk = (lane % C) ^ Tile<DP>::swizzle(row);
-      at[i] = 8 * chunk < dim ? row * step + 16 * chunk : 0x80000000u;   // past every descriptor
-    }
+    const int row = wave * Tile<DP>::ROWS_A_COPY + lane / C;
+    const int chunk = (lane % C) ^ Tile<DP>::swizzle(row);
+    at = 8 * chunk < dim ? row * step + 16 * chunk : 0x80000000u;   // past every descriptor
     lds = __builtin_amdgcn_readfirstlane(wave * 1024);
   }
   // `rows`: how many of the tile's rows there are.
@@ -134,25 +132,24 @@ struct Copier {
     const int n = min(rows, ROWS);
     const I32x4 from = descriptor(first, n > 0 ? (n - 1) * step + 2 * dim : 0);
 #pragma unroll
-    for (int i = 0; i < N; ++i) copy16(from, tile + lds + i * WAVES * 1024, at[i]);
+    for (int i = 0; i < N; ++i) copy16(from, tile + lds + i * WAVES * 1024, at + i * EACH * step);
   }
 };
 
-// This lane's offsets for reading rows: A (or B) operand of rows row .. row + 31 at
-// columns 16 k .. + 15 is at row * ROW + at[k].
+// Reads rows: A (or B) operand of rows row .. row + 31 at columns 16 k .. + 15, a
+// chunk for each lane. Tiles begin at multiples of a row, so that chunks are told
+// apart by the address' bits above 4 and one register serves for all of them.
 template <int DP>
 struct RowReader {
-  uint32_t at[DP / 16];
+  uint32_t at;
   __device__ __forceinline__ explicit RowReader(int lane) {
     const int row = lane & 31, half = lane >> 5;
-#pragma unroll
-    for (int k = 0; k < DP / 16; ++k)
-      at[k] = row * Tile<DP>::ROW + (((2 * k + half) ^ Tile<DP>::swizzle(row)) << 4);
+    at = row * Tile<DP>::ROW + ((half ^ Tile<DP>::swizzle(row)) << 4);
   }
   template <class T>
-  __device__ __forceinline__ typename Eight<T>::type read(const LdsChar* tile, int row, int k) const {
-    const U32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) U32x4*>(
-        tile + row * Tile<DP>::ROW + at[k]);
+  __device__ __forceinline__ typename Eight<T>::type read(uint32_t tile, int row, int k) const {
+    const uint32_t p = ((tile + at) ^ (k << 5)) + row * Tile<DP>::ROW;
+    const U32x4 v = *(const __attribute__((address_space(3))) U32x4*)(p);
     return __builtin_bit_cast(typename Eight<T>::type, v);
   }
 };
@@ -163,26 +160,20 @@ struct RowReader {
 // consecutive values M[j][0..3]; lane i receives M[4 q + i / 4][i % 4] in slot q.
 template <int DP>
 struct ColumnReader {
-  uint32_t at[DP / 32][2];
+  uint32_t at;
   __device__ __forceinline__ explicit ColumnReader(int lane) {
     const int j = lane & 15, group = lane >> 4;
-    const int half = group >> 1;
-#pragma unroll
-    for (int t = 0; t < DP / 32; ++t)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int row = 8 * u + 4 * half + (j >> 2);
-        const int column = 32 * t + 16 * (group & 1) + 4 * (j & 3);
-        at[t][u] = row * Tile<DP>::ROW + (((column >> 3) ^ Tile<DP>::swizzle(row)) << 4) + (column & 4) * 2;
-      }
+    const int row = 4 * (group >> 1) + (j >> 2), column = 16 * (group & 1) + 4 * (j & 3);
+    at = row * Tile<DP>::ROW + (((column >> 3) ^ Tile<DP>::swizzle(row)) << 4) + (column & 4) * 2;
   }
   template <class T>
-  __device__ __forceinline__ typename Eight<T>::type read(const LdsChar* tile, int c, int t) const {
-    const LdsChar* p = tile + 16 * c * Tile<DP>::ROW;
+  __device__ __forceinline__ typename Eight<T>::type read(uint32_t tile, int c, int t) const {
+    const uint32_t p = (tile + at) ^ (t << 6);
+    const uint32_t p8 = p ^ (Tile<DP>::swizzle(8) << 4);   // eight rows on: the other half's pattern
     const S16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) S16x4*)(p + at[t][0]));
+        (__attribute__((address_space(3))) S16x4*)(p + 16 * c * Tile<DP>::ROW));
     const S16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) S16x4*)(p + at[t][1]));
+        (__attribute__((address_space(3))) S16x4*)(p8 + (16 * c + 8) * Tile<DP>::ROW));
     const U32x2 a = __builtin_bit_cast(U32x2, x), b = __builtin_bit_cast(U32x2, y);
     const U32x4 v = {a[0], a[1], b[0], b[1]};
     return __builtin_bit_cast(typename Eight<T>::type, v);

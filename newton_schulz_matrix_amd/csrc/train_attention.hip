@@ -93,8 +93,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
     if (n + 1 < steps) fetch_tile(n + 1);
     const int first_key = n * KEYS;
     if (first_key > first_query + 31) continue;
-    const LdsChar* const kt = (const LdsChar*)(smem) + (n & 1) * 2 * TILE;
-    const LdsChar* const vt = kt + TILE;
+    const uint32_t kt = lds + (n & 1) * 2 * TILE, vt = kt + TILE;
     Acc s[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

@@ -92,10 +92,11 @@ __global__ __launch_bounds__(256) void delta_kernel(AttnArgs a, uint32_t* peaks)
 // Rows behind the last sequence: zeros.
 template <class T>
 __device__ __forceinline__ void clear_rows(const HeadsAt& to, int head, int dim, int first, int last) {
+  const int threads = blockDim.x;
   T* p = static_cast<T*>(to.p) + head * to.head;
   const int chunks = dim / 8, n = (last - first) * chunks;
   const U32x4 zero = {0, 0, 0, 0};
-  for (int i = threadIdx.x; i < n; i += THREADS)
+  for (int i = threadIdx.x; i < n; i += threads)
     *reinterpret_cast<U32x4*>(p + (first + i / chunks) * to.token + i % chunks * 8) = zero;
 }
 
@@ -158,8 +159,7 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
     __syncthreads();
     if (n + 1 < steps) fetch_tile(n + 1);
     const int first_key = n * STEP;
-    const LdsChar* const kt = (const LdsChar*)(smem) + (n & 1) * 2 * TILE;
-    const LdsChar* const vt = kt + TILE;
+    const uint32_t kt = lds + (n & 1) * 2 * TILE, vt = kt + TILE;
 #pragma unroll
     for (int i = 0; i < STEP / 32; ++i) {
       const int key0 = first_key + 32 * i;
@@ -191,14 +191,22 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
 
 // ----------------------------------------------------------------- dk and dv
 
+// Eight waves: four times 32 keys, and of every tile of queries each half. The two
+// waves of the same keys add up their sums at the end: the longest workgroup, which
+// keeps the first keys of the longest sequence, is done in half the time so.
+constexpr int KV_WAVES = 8, KV_THREADS = 64 * KV_WAVES;
+constexpr int KV_STEP = 128;          // queries of a tile
+
 template <class T, int DP>
-__global__ __launch_bounds__(THREADS, 2) void dkv_kernel(AttnArgs a, const uint32_t* peaks, int tiles) {
+__global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const uint32_t* peaks, int tiles) {
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32;
-  constexpr int TILE = STEP * Tile<DP>::ROW, STATS = 2 * STEP * 4, STAGE = 2 * TILE + STATS;
+  constexpr int TILE = KV_STEP * Tile<DP>::ROW, STATS = 2 * KV_STEP * 4, STAGE = 2 * TILE + STATS;
+  static_assert(2 * STAGE >= 2 * ROWS * DP * 4, "both sums of half the waves fit in the tiles");
   __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];   // queries, dout, lse, delta, twice
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave / 4;           // of the queries
   const Work w = work_of(blockIdx.x, a.k_heads, a.k_heads, tiles);
   const Place at = place_of<ROWS>(a.offsets, a.sequences, a.tokens, tiles - 1 - w.tile);   // the first are the longest
   if (at.length == 0) return;
@@ -215,23 +223,24 @@ __global__ __launch_bounds__(THREADS, 2) void dkv_kernel(AttnArgs a, const uint3
   const T* g = static_cast<const T*>(a.dout.p) + at.begin * a.dout.token + w.head * group * a.dout.head;
   const int64_t stat0 = static_cast<int64_t>(w.head) * group * a.tokens + at.begin;
   const uint32_t q_step = static_cast<uint32_t>(a.q.token * 2), g_step = static_cast<uint32_t>(a.dout.token * 2);
-  const Copier<DP, STEP, WAVES> q_copy(wave, lane, q_step, a.dim), g_copy(wave, lane, g_step, a.dim);
+  const Copier<DP, KV_STEP, KV_WAVES> q_copy(wave, lane, q_step, a.dim), g_copy(wave, lane, g_step, a.dim);
   const uint32_t lds = lds_address(smem);
-  const int begin = at.row / STEP;
-  const int each = (at.length + STEP - 1) / STEP - begin, steps = each * group;   // each >= 1
+  const int begin = at.row / KV_STEP;
+  const int each = (at.length + KV_STEP - 1) / KV_STEP - begin, steps = each * group;   // each >= 1
   auto fetch_tile = [&](int n) {
     const uint32_t to = lds + (n & 1) * STAGE;
-    const int h = n / each, first = (begin + n - h * each) * STEP, rows = at.length - first;
+    const int h = n / each, first = (begin + n - h * each) * KV_STEP, rows = at.length - first;
     q_copy.copy(q + h * a.q.head + first * a.q.token, rows, q_step, a.dim, to);
     g_copy.copy(g + h * a.dout.head + first * a.dout.token, rows, g_step, a.dim, to + TILE);
-    if (wave < 2) {
-      const float* from = (wave == 0 ? a.lse2 : a.delta) + stat0 + static_cast<int64_t>(h) * a.tokens + first;
-      copy4(descriptor(from, 4 * min(rows, STEP)), to + 2 * TILE + wave * STEP * 4, 4 * lane);
+    if (wave < 4) {   // lse and delta of 64 rows each
+      const int row = 64 * (wave & 1), left = min(rows - row, 64);
+      const float* from = (wave < 2 ? a.lse2 : a.delta) + stat0 + static_cast<int64_t>(h) * a.tokens + first + row;
+      copy4(descriptor(from, left > 0 ? 4 * left : 0), to + 2 * TILE + wave * 64 * 4, 4 * lane);
     }
   };
   fetch_tile(0);
 
-  const int first_key = at.row + 32 * wave, key = first_key + (lane & 31);
+  const int first_key = at.row + 32 * (wave & 3), key = first_key + (lane & 31);
   const bool there = key < at.length;
   const int64_t token = at.begin + key;
   V8 k[KC], v[KC];
@@ -252,46 +261,60 @@ __global__ __launch_bounds__(THREADS, 2) void dkv_kernel(AttnArgs a, const uint3
     copies_done();
     __syncthreads();
     if (n + 1 < steps) fetch_tile(n + 1);
-    const int first_query = (begin + n % each) * STEP;
-    const LdsChar* const qt = (const LdsChar*)(smem) + (n & 1) * STAGE;
-    const LdsChar* const gt = qt + TILE;
-    const __attribute__((address_space(3))) float* const stats =
-        (const __attribute__((address_space(3))) float*)(gt + TILE);
-#pragma unroll
-    for (int i = 0; i < STEP / 32; ++i) {
-      const int query0 = first_query + 32 * i;
+    const int first_query = (begin + n % each) * KV_STEP;
+    const uint32_t qt = lds + (n & 1) * STAGE, gt = qt + TILE;
+#pragma unroll 1
+    for (int i = 0; i < KV_STEP / 64; ++i) {
+      const int row0 = 64 * i + 32 * part, query0 = first_query + row0;
       if (query0 + 31 < first_key) continue;
+      const uint32_t qr = qt + row0 * Tile<DP>::ROW, gr = gt + row0 * Tile<DP>::ROW;
+      const __attribute__((address_space(3))) float* const stats =
+          (const __attribute__((address_space(3))) float*)(gt + TILE) + row0 + 4 * half;
       Acc s = no_sum(), dp = no_sum();
 #pragma unroll
-      for (int j = 0; j < KC; ++j) s = product(rows.template read<T>(qt, 32 * i, j), k[j], s);
+      for (int j = 0; j < KC; ++j) s = product(rows.template read<T>(qr, 0, j), k[j], s);
 #pragma unroll
-      for (int j = 0; j < KC; ++j) dp = product(rows.template read<T>(gt, 32 * i, j), v[j], dp);
-      const bool edge = query0 < first_key + 31;
+      for (int j = 0; j < KC; ++j) dp = product(rows.template read<T>(gr, 0, j), v[j], dp);
+      const int hidden = query0 < first_key + 31 ? key - query0 - 4 * half : -64;   // rows below it are
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int at_row = 32 * i + 8 * (r / 4) + 4 * half + r % 4;
-        const float lse2 = stats[at_row] - (NARROW<T> ? LIFT : 0.f), delta = stats[STEP + at_row];
-        float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2));
-        float d = p * (NARROW<T> ? (dp[r] - delta) * to_ds : dp[r] - delta);
-        const bool hidden = edge && key > first_query + at_row;
-        s[r] = hidden ? 0.f : p;
-        dp[r] = hidden ? 0.f : d;
+        const int row = 8 * (r / 4) + r % 4;
+        const float lse2 = stats[row] - (NARROW<T> ? LIFT : 0.f), delta = stats[KV_STEP + row];
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2));
+        const float d = p * (NARROW<T> ? (dp[r] - delta) * to_ds : dp[r] - delta);
+        s[r] = row < hidden ? 0.f : p;
+        dp[r] = row < hidden ? 0.f : d;
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const V8 p = operand<T>(s, j), ds = operand<T>(dp, j);   // rounded to T, half a step each
 #pragma unroll
         for (int t = 0; t < DT; ++t) {
-          dv[t] = product(columns.template read<T>(gt, 2 * i + j, t), p, dv[t]);
-          dk[t] = product(columns.template read<T>(qt, 2 * i + j, t), ds, dk[t]);
+          dv[t] = product(columns.template read<T>(gr, j, t), p, dv[t]);
+          dk[t] = product(columns.template read<T>(qr, j, t), ds, dk[t]);
         }
       }
     }
   }
-  T* to_k = static_cast<T*>(a.dk.p) + token * a.dk.token + w.head * a.dk.head;
-  T* to_v = static_cast<T*>(a.dv.p) + token * a.dv.token + w.head * a.dv.head;
-  store_columns<T, DP>(there ? to_k : nullptr, a.dim, half, dk, a.scale / scaled);
-  store_columns<T, DP>(there ? to_v : nullptr, a.dim, half, dv, NARROW<T> ? 1.f / 16384.f : 1.f);
+
+  // the first four waves finish dk, the others dv
+  __syncthreads();
+  float* const sums = reinterpret_cast<float*>(smem) + (wave & 3) * 64 * DP / 2 + lane;
+  float* const give = sums + (part ? 0 : 2 * 64 * DP);
+  float* const take = sums + (part ? 2 * 64 * DP : 0);
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) give[64 * (16 * t + r)] = part ? dk[t][r] : dv[t][r];
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) dk[t][r] = (part ? dv[t][r] : dk[t][r]) + take[64 * (16 * t + r)];
+  const HeadsAt& to = part ? a.dv : a.dk;
+  T* row = static_cast<T*>(to.p) + token * to.token + w.head * to.head;
+  const float by = part == 0 ? a.scale / scaled : NARROW<T> ? 1.f / 16384.f : 1.f;
+  store_columns<T, DP>(there ? row : nullptr, a.dim, half, dk, by);
 }
 
 }  // namespace
@@ -304,7 +327,7 @@ hipError_t launch_attention_grad(const AttnArgs& a, int type, uint32_t* peaks, h
     if (NARROW<T>) hipLaunchKernelGGL(clear_peaks_kernel, dim3(1), dim3(64), 0, stream, peaks);
     hipLaunchKernelGGL(delta_kernel<T>, dim3((a.tokens + 15) / 16, a.q_heads + (NARROW<T> ? a.k_heads : 0)),
                        dim3(256), 0, stream, a, peaks);
-    hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.k_heads)), dim3(THREADS), 0,
+    hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.k_heads)), dim3(KV_THREADS), 0,
                        stream, a, peaks, static_cast<int>(tiles));
     hipLaunchKernelGGL((dq_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.q_heads)), dim3(THREADS), 0,
                        stream, a, peaks, static_cast<int>(tiles));
