@@ -41,39 +41,62 @@ __device__ __forceinline__ double wave_sum64(double v) {
   return v;
 }
 
-// Running maximum and sums of a thread.
+// bf16 as one step each: taken from the halves by type, the upper ones are shifted
+// down and up again.
+__device__ __forceinline__ void widen(const Raw<__bf16>& raw, float (&v)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) {
+    const uint32_t word = raw.q[0][i];
+    v[2 * i] = __builtin_bit_cast(float, word << 16);
+    v[2 * i + 1] = __builtin_bit_cast(float, word & 0xffff0000u);
+  }
+}
+
+// Sums of a thread against a reference m, which is at most LAG below its
+// greatest entry: x is at most LAG, and the entropy's two terms do not cancel.
+constexpr float LAG = 1.f;
 struct Sums {
   float m, s, t;
 };
-// Brings the sums to another maximum.
+// Brings the sums to another reference.
 __device__ __forceinline__ void rebase(Sums& r, float m) {
-  const float d = base_of(r.m) - base_of(m);   // <= 0 (r.m = -inf: both sums are 0)
+  const float d = base_of(r.m) - base_of(m);   // (r.m = -inf: both sums are 0)
   const float f = r.m == -INFINITY ? 0.f : exp_of(d);
   r.t = f == 0.f ? 0.f : f * fmaf(r.s, d, r.t);
   r.s *= f;
   r.m = m;
 }
-// Takes in a step; `high` receives the maximum of each vector.
-template <int U>
-__device__ __forceinline__ void take(const float (&v)[U][VEC], Sums& r, float (&high)[U]) {
-  float top = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
-    high[j] = v[j][0];
-#pragma unroll
-    for (int e = 1; e < VEC; ++e) high[j] = fmaxf(high[j], v[j][e]);
-    top = fmaxf(top, high[j]);
-  }
-  if (top > r.m) rebase(r, top);
+// Takes in one vector, whose greatest entry is `high`.
+__device__ __forceinline__ void take(const float (&v)[VEC], float high, Sums& r) {
+  if (__any(high > r.m + LAG)) rebase(r, fmaxf(r.m, high));
   const float base = base_of(r.m);
 #pragma unroll
-  for (int j = 0; j < U; ++j)
+  for (int e = 0; e < VEC; ++e) {
+    const float x = v[e] - base, w = exp_of(x);   // (a NaN stays one in w)
+    r.s += w;
+    r.t = fmaf(w, fmaxf(x, -FAR), r.t);           // 0 for an entry at -inf
+  }
+}
+__device__ __forceinline__ float highest(const float (&v)[VEC]) {
+  float h = v[0];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float x = v[j][e] - base, w = exp_of(x);   // (a NaN stays one in w)
-      r.s += w;
-      r.t = fmaf(w, fmaxf(x, -FAR), r.t);              // 0 for an entry at -inf
-    }
+  for (int e = 1; e < VEC; ++e) h = fmaxf(h, v[e]);
+  return h;
+}
+
+// The vector at `at` of a row that ends at `end`, -inf behind it.
+template <class T>
+__device__ __forceinline__ Raw<T> fetch_upto(const T* z, int at, int end) {
+  if (at + VEC <= end) return fetch(z + at);
+  T e[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    e[i] = static_cast<T>(-INFINITY);
+    if (at + i < end) e[i] = z[at + i];
+  }
+  Raw<T> raw;
+  __builtin_memcpy(&raw, e, sizeof(raw));
+  return raw;
 }
 
 // ------------------------------------------------------- likeliest entries
@@ -89,89 +112,124 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   const uint32_t b = k & 0x80000000u ? k & 0x7fffffffu : ~k;
   return k == 0u ? NAN : __builtin_bit_cast(float, b);
 }
+constexpr uint32_t LOWEST = 0x007fffffu;   // of -inf
+
 // Orders by value, and the lowest index first among equals.
 __device__ __forceinline__ uint64_t entry_of(uint32_t order, int index) {
   return static_cast<uint64_t>(order) << 32 | static_cast<uint32_t>(~index);
 }
 
-// A wave's candidates, in LDS. A vector brings at most 512; `top` and those fit.
-constexpr int CANDIDATES = LOGPS_MAX_TOP + 64 * VEC;
-
-// Orders of the list's first `count` entries: those of rank < top move to their
-// ranks. Every entry is another number, so ranks are distinct.
-__device__ __forceinline__ void compact(uint64_t* list, int& count, int top, uint32_t& above) {
-  constexpr int MINE = (CANDIDATES + 63) / 64;
-  const int lane = threadIdx.x & 63;
-  uint64_t mine[MINE];
-  int rank[MINE];
-#pragma unroll
-  for (int i = 0; i < MINE; ++i) {
-    mine[i] = lane + 64 * i < count ? list[lane + 64 * i] : 0;
-    rank[i] = 0;
-  }
-  for (int k = 0; k < count; ++k) {
-    const uint64_t other = list[k];
-#pragma unroll
-    for (int i = 0; i < MINE; ++i) rank[i] += other > mine[i];
-  }
+// What the lanes of a wave have written to LDS is there for the others.
+__device__ __forceinline__ void wave_settled() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
-#pragma unroll
-  for (int i = 0; i < MINE; ++i)
-    if (lane + 64 * i < count && rank[i] < top) list[rank[i]] = mine[i];
-  __builtin_amdgcn_wave_barrier();
-  if (count >= top) {
-    count = top;
-    above = max(above, static_cast<uint32_t>(list[top - 1] >> 32));
-  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Offers a step's entries: those whose order is more than `above` become
-// candidates. `high` is the maximum of each of the lane's vectors. Indices rise
-// from one vector of a wave to the next, so an entry equal to the last of `top`
-// earlier ones is behind them.
-template <int U, int THREADS>
-__device__ __forceinline__ void offer(const float (&v)[U][VEC], const float (&high)[U], int at, int end,
-                                      int top, uint64_t* list, int& count, uint32_t& above) {
+// A wave's candidates, in LDS. A vector brings at most 512; `top` and those fit.
+constexpr int CANDIDATES = LOGPS_MAX_TOP + 64 * VEC;
+constexpr int AT_ONCE = 8;   // entries of a list that are read together
+constexpr int LAST = 256;    // entries that are left for the final order, hardly ever more than 2 top
+struct Candidates {
+  uint64_t list[CANDIDATES];
+  uint64_t ordered[LOGPS_MAX_TOP];
+  uint32_t best[64];   // greatest order of each lane
+  int count;
+};
+
+// Zeros behind a list's entries, up to where it is read.
+__device__ __forceinline__ void pad(uint64_t* list, int count, int size) {
   const int lane = threadIdx.x & 63;
-  uint32_t most = 0;
-  int hits = 0;
+  if (lane < AT_ONCE && count + lane < size) list[count + lane] = 0;
+  wave_settled();
+}
+// How many entries of a padded list stand before `mine`.
+__device__ __forceinline__ int rank_in(const uint64_t* list, int count, uint64_t mine) {
+  int rank = 0;
+  for (int k = 0; k < count; k += AT_ONCE)
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    const uint32_t order = order_of(high[j]);
-    most = max(most, order);
-    hits += __popcll(__ballot(order > above));
+    for (int i = 0; i < AT_ONCE; ++i) rank += list[k + i] > mine;
+  return rank;
+}
+
+// A number that `top` of N orders a lane reach, near the greatest such: its upper 16
+// bits, one a step.
+template <int N>
+__device__ __forceinline__ uint32_t reached_by(const uint32_t (&order)[N], int top) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int b = 31; b >= 16; --b) {
+    const uint32_t more = t | 1u << b;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __popcll(__ballot(order[i] >= more));
+    t = n >= top ? more : t;
   }
-  if (hits == 0) return;
-  if (hits > top + 32) {
-    // the lane of rank top - 1 by its greatest entry: that many entries reach its order
-    int rank = 0;
-    for (int i = 0; i < 64; ++i) {
-      const uint32_t other = __builtin_amdgcn_readlane(most, i);
-      rank += other > most || (other == most && i < lane);
-    }
-    const int at_rank = __ffsll(static_cast<unsigned long long>(__ballot(rank == top - 1))) - 1;
-    const uint32_t reached = __builtin_amdgcn_readlane(most, at_rank);
-    above = max(above, reached > 0 ? reached - 1 : 0u);
+  return t;
+}
+
+// What a wave knows: entries from order `from` on (value `from_value`) are
+// candidates, `count` so far; best is the lane's greatest entry.
+struct Choice {
+  uint32_t from;
+  float from_value, best;
+  int count;
+
+  __device__ __forceinline__ void raise(uint32_t to) {
+    from = max(from, to);
+    from_value = value_of(from);   // (behind inf: NaN, which nothing reaches)
   }
+};
+
+// Leaves the `top` first candidates, in order. Every entry is another number, so
+// ranks are distinct.
+__device__ __forceinline__ void compact(Candidates& c, Choice& w, int top) {
+  const int lane = threadIdx.x & 63;
+  pad(c.list, w.count, CANDIDATES);
+  for (int first = 0; first < w.count; first += 64) {
+    const int i = first + lane;
+    const uint64_t mine = i < w.count ? c.list[i] : 0;
+    const int rank = rank_in(c.list, w.count, mine);
+    if (i < w.count && rank < top) c.ordered[rank] = mine;
+  }
+  wave_settled();
+  const int left = min(w.count, top);
+  if (lane < left) c.list[lane] = c.ordered[lane];
+  if (lane == 0) c.count = left;
+  wave_settled();
+  // indices rise from one vector of a wave to the next: an entry equal to the last of these is behind it
+  if (w.count >= top) w.raise(static_cast<uint32_t>(c.list[top - 1] >> 32) + 1);
+  w.count = left;
+}
+
+// Offers a step's entries. `high` is the greatest of each of the lane's vectors.
+template <int THREADS, class T>
+__device__ __forceinline__ void offer(const Raw<T> (&raw)[UNROLL], const float (&high)[UNROLL], int at, int end,
+                                      int top, Candidates& c, Choice& w) {
+  float most = high[0];
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    if (!__any(order_of(high[j]) > above)) continue;
-    const int first = at + j * THREADS * VEC;
-    int more = 0;
+  for (int j = 1; j < UNROLL; ++j) most = fmaxf(most, high[j]);
+  if (!__any(most >= w.from_value)) return;
+  w.best = fmaxf(w.best, most);
+  const uint32_t best[1] = {order_of(w.best)};
+  w.raise(reached_by(best, top));
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) more += __popcll(__ballot(order_of(v[j][e]) > above && first + e < end));
-    if (count + more > CANDIDATES) compact(list, count, top, above);
+  for (int j = 0; j < UNROLL; ++j) {
+    const unsigned long long hits = __ballot(high[j] >= w.from_value);
+    if (hits == 0) continue;
+    if (w.count + VEC * __popcll(hits) > CANDIDATES) compact(c, w, top);
+    if (high[j] >= w.from_value) {
+      float v[VEC];
+      widen(raw[j], v);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const uint32_t order = order_of(v[j][e]);
-      const bool in = order > above && first + e < end;
-      const unsigned long long all = __ballot(in);
-      if (in)
-        list[count + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(all >> 32),
-                                               __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), 0))] =
-            entry_of(order, first + e);
-      count += __popcll(all);
+      for (int e = 0; e < VEC; ++e) {
+        const int index = at + j * THREADS * VEC + e;
+        if (v[e] >= w.from_value && index < end)
+          c.list[atomicAdd(&c.count, 1)] = entry_of(order_of(v[e]), index);
+      }
     }
+    wave_settled();
+    w.count = __builtin_amdgcn_readfirstlane(*const_cast<volatile int*>(&c.count));
   }
 }
 
@@ -209,8 +267,9 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
   constexpr int STEP = step_of(THREADS), WAVES = THREADS / 64;
   __shared__ float red_m[WAVES];
   __shared__ double red_s[WAVES], red_t[WAVES];
-  __shared__ uint64_t lists[TOP ? WAVES : 1][TOP ? CANDIDATES : 1];
-  __shared__ int counts[WAVES];
+  __shared__ Candidates found[TOP ? WAVES : 1];
+  __shared__ uint64_t last[TOP ? LAST + AT_ONCE : 1];
+  __shared__ int lasts;
   const int64_t row = blockIdx.x;
   const int64_t token = token_at(a, row);
   if (!counted(a, token)) {
@@ -222,62 +281,68 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int col0 = threadIdx.x * VEC;
   const float token_logit = static_cast<float>(z[token]);
+  Candidates& mine = found[TOP ? wave : 0];
+  if constexpr (TOP) {
+    if (lane == 0) mine.count = 0;
+    if (threadIdx.x == 0) lasts = 0;
+    wave_settled();
+  }
   Sums r = {-INFINITY, 0.f, 0.f};
-  int count = 0;
-  uint32_t above = 0;
-  int base = begin;
-  for (; base + STEP <= end; base += STEP) {
-    float v[UNROLL][VEC];
-    Raw<T> raw[UNROLL];
-#pragma unroll
-    for (int j = 0; j < UNROLL; ++j) raw[j] = fetch(z + base + j * THREADS * VEC + col0);
-#pragma unroll
-    for (int j = 0; j < UNROLL; ++j) widen(raw[j], v[j]);
+  Choice w = {LOWEST, -INFINITY, -INFINITY, 0};
+  for (int base = begin; base < end; base += STEP) {
     float high[UNROLL];
-    take(v, r, high);
-    if constexpr (TOP) offer<UNROLL, THREADS>(v, high, base + col0, end, a.top, lists[wave], count, above);
-  }
-  if (base < end) {   // the vectors left, all in flight, then one after the other
     Raw<T> raw[UNROLL];
+    int there = UNROLL;
+    if (base + STEP <= end) {
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
-      const int at = base + j * THREADS * VEC;
-      if (at < end && end >= VEC) raw[j] = fetch_at(z, end, at + col0);
+      for (int j = 0; j < UNROLL; ++j) raw[j] = fetch(z + base + j * THREADS * VEC + col0);
+    } else {
+      there = (end - base + THREADS * VEC - 1) / (THREADS * VEC);
+#pragma unroll
+      for (int j = 0; j < UNROLL; ++j) raw[j] = fetch_upto(z, base + j * THREADS * VEC + col0, end);
     }
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j) {
-      const int at = base + j * THREADS * VEC;
-      if (at >= end) break;
-      float v[1][VEC];
-      widen_at(raw[j], z, end, at + col0, v[0]);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[0][e] = at + col0 + e < end ? v[0][e] : -INFINITY;
-      float high[1];
-      take(v, r, high);
-      if constexpr (TOP) offer<1, THREADS>(v, high, at + col0, end, a.top, lists[wave], count, above);
+      float v[VEC];
+      widen(raw[j], v);
+      high[j] = highest(v);
+      if (j < there) take(v, high[j], r);
     }
+    if constexpr (TOP) offer<THREADS>(raw, high, base + col0, end, a.top, mine, w);
   }
+  if constexpr (TOP) mine.best[lane] = order_of(w.best);
   const float wave_top = wave_max(r.m);
-  if (lane == 0) {
-    red_m[wave] = wave_top;
-    counts[wave] = count;
-  }
+  if (lane == 0) red_m[wave] = wave_top;
   __syncthreads();
   float m = red_m[0];
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) m = fmaxf(m, red_m[w]);
+  for (int u = 1; u < WAVES; ++u) m = fmaxf(m, red_m[u]);
   rebase(r, m);
   const double ws = wave_sum64(static_cast<double>(r.s)), wt = wave_sum64(static_cast<double>(r.t));
   if (lane == 0) {
     red_s[wave] = ws;
     red_t[wave] = wt;
   }
+  if constexpr (TOP) {   // those of all waves that reach what `top` lanes have reached
+    uint32_t best[WAVES];
+#pragma unroll
+    for (int u = 0; u < WAVES; ++u) best[u] = found[u].best[lane];
+    const uint32_t from = reached_by(best, a.top);
+    for (int i = lane; i < w.count; i += 64) {
+      const uint64_t e = mine.list[i];
+      if (static_cast<uint32_t>(e >> 32) >= from) {
+        const int at = atomicAdd(&lasts, 1);
+        if (at < LAST) last[at] = e;
+      }
+    }
+    pad(mine.list, w.count, CANDIDATES);
+  }
   __syncthreads();
   double s = 0.0, t = 0.0;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) {
-    s += red_s[w];
-    t += red_t[w];
+  for (int u = 0; u < WAVES; ++u) {
+    s += red_s[u];
+    t += red_t[u];
   }
   const bool whole = sp.pieces == 1;
   const int64_t part = row * sp.pieces + blockIdx.y;
@@ -286,25 +351,25 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
     else parts[part] = {m, s, t};
   }
   if constexpr (TOP) {
-    // ranks among all waves' candidates
+    const int left = lasts;
     const double log_s = whole ? log(s) : 0.0;
-    int all = 0;
-    for (int w = 0; w < WAVES; ++w) {
-      all += counts[w];
-      for (int i = threadIdx.x; i < counts[w]; i += THREADS) {
-        const uint64_t mine = lists[w][i];
+    auto put = [&](int rank, uint64_t e) {
+      if (rank >= a.top) return;
+      if (whole) write_entry(a, o, row, rank, e, m, log_s);
+      else entries[part * a.top + rank] = e;
+    };
+    if (left <= LAST) {
+      if (wave == 0) pad(last, left, LAST + AT_ONCE);
+      __syncthreads();
+      for (int i = threadIdx.x; i < left; i += THREADS) put(rank_in(last, left, last[i]), last[i]);
+    } else {   // many equal entries: ranks among all candidates
+      for (int i = lane; i < w.count; i += 64) {
         int rank = 0;
-        for (int u = 0; u < WAVES; ++u)
-          for (int k = 0; k < counts[u]; ++k) rank += lists[u][k] > mine;
-        if (rank >= a.top) continue;
-        if (whole) write_entry(a, o, row, rank, mine, m, log_s);
-        else entries[part * a.top + rank] = mine;
+        for (int u = 0; u < WAVES; ++u) rank += rank_in(found[u].list, found[u].count, mine.list[i]);
+        put(rank, mine.list[i]);
       }
     }
-    for (int rank = all + threadIdx.x; rank < a.top; rank += THREADS) {   // short, or NaN
-      if (whole) write_entry(a, o, row, rank, 0, m, log_s);
-      else entries[part * a.top + rank] = 0;
-    }
+    for (int rank = left + threadIdx.x; rank < a.top; rank += THREADS) put(rank, 0);   // short, or NaN
   }
 }
 
@@ -314,13 +379,13 @@ template <class T>
 __global__ __launch_bounds__(JOIN_THREADS) void join_kernel(LogpsArgs a, int pieces,
                                                             const LogpsPart* parts,
                                                             const uint64_t* entries, LogpsOut o) {
-  __shared__ uint64_t list[LOGPS_JOIN];
+  __shared__ uint64_t list[LOGPS_JOIN + AT_ONCE];
   const int64_t row = blockIdx.x;
   const int64_t token = token_at(a, row);
   if (!counted(a, token)) return;   // written by the row's first piece
   const LogpsPart* p = parts + row * pieces;
   const int all = pieces * a.top;
-  for (int i = threadIdx.x; i < all; i += JOIN_THREADS) list[i] = entries[row * all + i];
+  for (int i = threadIdx.x; i < all + AT_ONCE; i += JOIN_THREADS) list[i] = i < all ? entries[row * all + i] : 0;
   double m = -INFINITY, s = 0.0, t = 0.0;
   for (int k = 0; k < pieces; ++k) m = fmax(m, p[k].m);
   const double base = base_of(static_cast<float>(m));
@@ -340,9 +405,9 @@ __global__ __launch_bounds__(JOIN_THREADS) void join_kernel(LogpsArgs a, int pie
   const double log_s = log(s);
   for (int i = threadIdx.x; i < all; i += JOIN_THREADS) {
     const uint64_t mine = list[i];
-    int rank = 0;
-    // empty places are equal; they are told apart by where they stand
-    for (int k = 0; k < all; ++k) rank += list[k] > mine || (list[k] == mine && k < i);
+    int rank = rank_in(list, all, mine);
+    if (mine == 0)   // empty places are equal: they are told apart by where they stand
+      for (int k = 0; k < i; ++k) rank += list[k] == 0;
     if (rank < a.top) write_entry(a, o, row, rank, mine, m, log_s);
   }
 }
