@@ -12,6 +12,7 @@
 // A wave takes one token, several heads at a time, so that its lanes keep the
 // same pairs and the angles are worked out once for all heads of a token.
 #include <algorithm>
+#include <type_traits>
 
 #include "heads_internal.h"
 #include "train_device.h"
@@ -54,6 +55,16 @@ struct Part {
     for (int i = 0; i < N; ++i) reinterpret_cast<A*>(p)[i] = q[i];
   }
   __device__ __forceinline__ void widen(float (&v)[W]) const {
+    if constexpr (std::is_same_v<T, __bf16>) {   // one step each, from the words
+      uint32_t words[W / 2];
+      __builtin_memcpy(words, q, sizeof(words));
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        v[2 * i] = __builtin_bit_cast(float, words[i] << 16);
+        v[2 * i + 1] = __builtin_bit_cast(float, words[i] & 0xffff0000u);
+      }
+      return;
+    }
     T r[W];
     __builtin_memcpy(r, q, sizeof(r));
 #pragma unroll
@@ -110,6 +121,13 @@ __device__ __forceinline__ void angles_of(const QkArgs& a, int64_t token, int la
   else angles<int32_t>(a, token, lane, table);
 }
 
+// What the lanes of a wave have written to LDS is there for the others.
+__device__ __forceinline__ void wave_settled() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 template <int W>
 __device__ __forceinline__ void read_angles(const Lane<W>& l, const float2* table, float (&c)[W],
                                             float (&s)[W]) {
@@ -145,24 +163,55 @@ __device__ __forceinline__ void turn(bool neighbours, float sign, const float (&
   }
 }
 
-// Sum over the lanes of a team (a power of two of them).
+// Sum over the lanes of a team (a power of two of them), each step one instruction
+// on the lanes of a row: neighbours, pairs, then mirrored halves, whose lanes all
+// hold the same by then.
+template <int CONTROL>
+__device__ __forceinline__ float moved(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CONTROL, 0xf, 0xf,
+                                                               false));
+}
 __device__ __forceinline__ float team_sum(float v, int team) {
-  for (int off = 1; off < team; off <<= 1) v += __shfl_xor(v, off, 64);
+  constexpr int XOR1 = 0xb1, XOR2 = 0x4e, HALF_MIRROR = 0x141, MIRROR = 0x140;
+  if (team > 1) v += moved<XOR1>(v);
+  if (team > 2) v += moved<XOR2>(v);
+  if (team > 4) v += moved<HALF_MIRROR>(v);
+  if (team > 8) v += moved<MIRROR>(v);
+  if (team > 16) v += __shfl_xor(v, 16, 64);
+  if (team > 32) v += __shfl_xor(v, 32, 64);
   return v;
 }
 
-template <class T, int W>
-__device__ __forceinline__ void weight_of(const void* w, bool w32, int at, float (&v)[W]) {
-  if (w32) {
-    Part<float, W> p;
-    p.load(static_cast<const float*>(w) + at);
-    p.widen(v);
-  } else {
-    Part<T, W> p;
-    p.load(static_cast<const T*>(w) + at);
-    p.widen(v);
+// The weights of queries and keys into LDS, as fp32.
+template <class T>
+__device__ __forceinline__ void share_weights(const QkArgs& a, float (*to)[QK_MAX_DIM]) {
+  for (int i = threadIdx.x; i < 2 * a.dim; i += THREADS) {
+    const int k = i >= a.dim, col = i - k * a.dim;
+    const void* w = a.part[k].weight;
+    to[k][col] = a.weight32 ? static_cast<const float*>(w)[col] : static_cast<float>(static_cast<const T*>(w)[col]);
   }
 }
+template <int W>
+__device__ __forceinline__ void read_weights(const float* w, int at, float (&v)[W]) {
+#pragma unroll
+  for (int e = 0; e < W; ++e) v[e] = w[at + e];
+}
+
+// The head that a team takes in round r of a wave's: queries first, then keys.
+struct Slot {
+  bool key, mine;
+  int head;
+  __device__ __forceinline__ Slot(const QkArgs& a, int slot, bool there) {
+    key = slot >= a.part[0].heads;
+    head = slot - (key ? a.part[0].heads : 0);
+    mine = there && slot < a.part[0].heads + a.part[1].heads;
+  }
+  template <class T>
+  __device__ __forceinline__ T* in(const QkArgs& a, T* queries, T* keys, int64_t token, int64_t q_token,
+                                   int64_t q_head, int64_t k_token, int64_t k_head) const {
+    return (key ? keys : queries) + token * (key ? k_token : q_token) + head * (key ? k_head : q_head);
+  }
+};
 
 // One wave a token and chunk of `rounds` rounds of heads. The loads of U rounds
 // are in flight before the angles are worked out.
@@ -170,68 +219,61 @@ template <class T, int W>
 __global__ __launch_bounds__(THREADS) void qk_norm_kernel(QkArgs a, int team, int rounds, int chunks) {
   constexpr int U = sizeof(T) == 2 ? 4 : 2;
   __shared__ float2 tables[WAVES][MAX_PAIRS];
+  __shared__ float weights[2][QK_MAX_DIM];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool norm = a.part[0].weight != nullptr;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * WAVES + wave;
   const int64_t token = unit / chunks;
-  if (token >= a.tokens) return;   // no barrier below: a wave's table is its own
   const Lane<W> l(a, lane & (team - 1));
-  const int each = 64 / team, heads = a.part[0].heads + a.part[1].heads;
+  const int each = 64 / team;
   const int slot0 = static_cast<int>(unit - token * chunks) * rounds * each + lane / team;
+  const bool here = token < a.tokens;
   float2* table = tables[wave];
   float c[W], s[W];
   for (int r0 = 0; r0 < rounds; r0 += U) {
     Part<T, W> ra[U], rb[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int slot = slot0 + (r0 + u) * each;
-      if (r0 + u < rounds && slot < heads && l.there) {
-        const bool key = slot >= a.part[0].heads;
-        const QkPart& p = a.part[key];
-        const T* x = static_cast<const T*>(p.x) + token * p.x_token +
-                     (slot - (key ? a.part[0].heads : 0)) * p.x_head;
+      const Slot at(a, slot0 + (r0 + u) * each, l.there && here && r0 + u < rounds);
+      ra[u] = {};
+      rb[u] = {};
+      if (at.mine) {
+        const T* x = at.in(a, static_cast<const T*>(a.part[0].x), static_cast<const T*>(a.part[1].x), token,
+                           a.part[0].x_token, a.part[0].x_head, a.part[1].x_token, a.part[1].x_head);
         ra[u].load(x + l.a);
         rb[u].load(x + l.b);
-      } else {
-        ra[u] = {};
-        rb[u] = {};
       }
     }
     if (r0 == 0) {
-      angles_of(a, token, lane, table);
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      if (here) angles_of(a, token, lane, table);
+      if (norm) share_weights<T>(a, weights);
+      __syncthreads();
       read_angles<W>(l, table, c, s);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int slot = slot0 + (r0 + u) * each;
       if (r0 + u >= rounds) break;
-      const bool key = slot >= a.part[0].heads;
-      const QkPart& p = a.part[key];
+      const Slot at(a, slot0 + (r0 + u) * each, l.there && here);
       float va[W], vb[W];
       ra[u].widen(va);
       rb[u].widen(vb);
-      if (a.part[0].weight) {
-        float sum = 0.f;
+      if (norm) {
+        float sum = 0.f, wa[W], wb[W];
 #pragma unroll
         for (int e = 0; e < W; ++e) sum = fmaf(va[e], va[e], fmaf(vb[e], vb[e], sum));
         const float rstd = rsqrtf(team_sum(sum, team) / static_cast<float>(a.dim) + a.eps);
-        if (l.there) {
-          float wa[W], wb[W];
-          weight_of<T>(p.weight, a.weight32, l.a, wa);
-          weight_of<T>(p.weight, a.weight32, l.b, wb);
+        read_weights<W>(weights[at.key], l.a, wa);
+        read_weights<W>(weights[at.key], l.b, wb);
 #pragma unroll
-          for (int e = 0; e < W; ++e) {
-            va[e] *= rstd * wa[e];
-            vb[e] *= rstd * wb[e];
-          }
+        for (int e = 0; e < W; ++e) {
+          va[e] *= rstd * wa[e];
+          vb[e] *= rstd * wb[e];
         }
       }
       turn<W>(a.interleaved, 1.f, c, s, va, vb);
-      if (slot < heads && l.there) {
-        T* y = static_cast<T*>(p.out) + token * p.out_token +
-               (slot - (key ? a.part[0].heads : 0)) * p.out_head;
+      if (at.mine) {
+        T* y = at.in(a, static_cast<T*>(a.part[0].out), static_cast<T*>(a.part[1].out), token, a.part[0].out_token,
+                     a.part[0].out_head, a.part[1].out_token, a.part[1].out_head);
         Part<T, W> o;
         o.narrow(va);
         o.store(y + l.a);
@@ -249,12 +291,15 @@ __global__ __launch_bounds__(THREADS) void qk_grad_kernel(QkArgs a, int team, in
                                                           float* partial) {
   constexpr int U = sizeof(T) == 2 ? 2 : 1;
   __shared__ float2 tables[WAVES][MAX_PAIRS];
+  __shared__ float weights[2][QK_MAX_DIM];
   __shared__ float shares[WAVES][2][QK_MAX_DIM];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool norm = a.part[0].weight != nullptr;
   const Lane<W> l(a, lane & (team - 1));
-  const int each = 64 / team, heads = a.part[0].heads + a.part[1].heads;
+  const int each = 64 / team, q_heads = a.part[0].heads;
   float2* table = tables[wave];
+  if (norm) share_weights<T>(a, weights);
+  __syncthreads();
   float dw[2][2][W];   // queries and keys, the two vectors
 #pragma unroll
   for (int i = 0; i < 4 * W; ++i) dw[i / (2 * W)][i / W % 2][i % W] = 0.f;
@@ -265,62 +310,77 @@ __global__ __launch_bounds__(THREADS) void qk_grad_kernel(QkArgs a, int team, in
       Part<T, W> ga[U], gb[U], xa[U], xb[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int slot = (r0 + u) * each + lane / team;
+        const Slot at(a, (r0 + u) * each + lane / team, l.there);
         ga[u] = gb[u] = xa[u] = xb[u] = {};
-        if (slot < heads && l.there) {
-          const bool key = slot >= a.part[0].heads;
-          const QkPart& p = a.part[key];
-          const int head = slot - (key ? a.part[0].heads : 0);
-          const T* dy = static_cast<const T*>(p.dy) + token * p.dy_token + head * p.dy_head;
+        if (at.mine) {
+          const T* dy = at.in(a, static_cast<const T*>(a.part[0].dy), static_cast<const T*>(a.part[1].dy), token,
+                              a.part[0].dy_token, a.part[0].dy_head, a.part[1].dy_token, a.part[1].dy_head);
           ga[u].load(dy + l.a);
           gb[u].load(dy + l.b);
           if (norm) {
-            const T* x = static_cast<const T*>(p.x) + token * p.x_token + head * p.x_head;
+            const T* x = at.in(a, static_cast<const T*>(a.part[0].x), static_cast<const T*>(a.part[1].x), token,
+                               a.part[0].x_token, a.part[0].x_head, a.part[1].x_token, a.part[1].x_head);
             xa[u].load(x + l.a);
             xb[u].load(x + l.b);
           }
         }
       }
       if (r0 == 0) {
-        __builtin_amdgcn_wave_barrier();   // the last token's angles have been read
+        wave_settled();   // the last token's angles have been read
         angles_of(a, token, lane, table);
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        wave_settled();
         read_angles<W>(l, table, c, s);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int slot = (r0 + u) * each + lane / team;
-        const bool key = slot >= a.part[0].heads, mine = slot < heads && l.there;
-        const QkPart& p = a.part[key];
+        if (r0 + u >= rounds) break;
+        const int first = (r0 + u) * each;
+        const Slot at(a, first + lane / team, l.there);
         float va[W], vb[W];
         ga[u].widen(va);
         gb[u].widen(vb);
         turn<W>(a.interleaved, -1.f, c, s, va, vb);
         if (norm) {
-          float na[W], nb[W], sum = 0.f, dot = 0.f;
+          float na[W], nb[W], wa[W], wb[W], sum = 0.f, dot = 0.f;
           xa[u].widen(na);
           xb[u].widen(nb);
+          read_weights<W>(weights[at.key], l.a, wa);
+          read_weights<W>(weights[at.key], l.b, wb);
 #pragma unroll
           for (int e = 0; e < W; ++e) sum = fmaf(na[e], na[e], fmaf(nb[e], nb[e], sum));
-          const float rstd = rsqrtf(team_sum(sum, team) / static_cast<float>(a.dim) + a.eps);
-          float wa[W], wb[W];
-          if (mine) {
-            weight_of<T>(p.weight, a.weight32, l.a, wa);
-            weight_of<T>(p.weight, a.weight32, l.b, wb);
-          }
+          sum = team_sum(sum, team) / static_cast<float>(a.dim) + a.eps;
+          const float rstd = at.mine ? rsqrtf(sum) : 0.f;   // (idle lanes hold zeros, also where eps is 0)
 #pragma unroll
           for (int e = 0; e < W; ++e) {
             na[e] *= rstd;
             nb[e] *= rstd;
-            const float da = va[e] * na[e], db = vb[e] * nb[e];
-            dw[0][0][e] += mine && !key ? da : 0.f;
-            dw[0][1][e] += mine && !key ? db : 0.f;
-            dw[1][0][e] += mine && key ? da : 0.f;
-            dw[1][1][e] += mine && key ? db : 0.f;
-            va[e] = mine ? va[e] * wa[e] : 0.f;
-            vb[e] = mine ? vb[e] * wb[e] : 0.f;
+          }
+          if (first + each <= q_heads) {   // all of them queries, or keys
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              dw[0][0][e] = fmaf(va[e], na[e], dw[0][0][e]);
+              dw[0][1][e] = fmaf(vb[e], nb[e], dw[0][1][e]);
+            }
+          } else if (first >= q_heads) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              dw[1][0][e] = fmaf(va[e], na[e], dw[1][0][e]);
+              dw[1][1][e] = fmaf(vb[e], nb[e], dw[1][1][e]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              const float da = va[e] * na[e], db = vb[e] * nb[e];
+              dw[0][0][e] += at.key ? 0.f : da;
+              dw[0][1][e] += at.key ? 0.f : db;
+              dw[1][0][e] += at.key ? da : 0.f;
+              dw[1][1][e] += at.key ? db : 0.f;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            va[e] *= wa[e];
+            vb[e] *= wb[e];
             dot = fmaf(va[e], na[e], fmaf(vb[e], nb[e], dot));
           }
           const float mean = team_sum(dot, team) / static_cast<float>(a.dim);
@@ -330,9 +390,9 @@ __global__ __launch_bounds__(THREADS) void qk_grad_kernel(QkArgs a, int team, in
             vb[e] = rstd * fmaf(-nb[e], mean, vb[e]);
           }
         }
-        if (mine) {
-          T* dx = static_cast<T*>(p.out) + token * p.out_token +
-                  (slot - (key ? a.part[0].heads : 0)) * p.out_head;
+        if (at.mine) {
+          T* dx = at.in(a, static_cast<T*>(a.part[0].out), static_cast<T*>(a.part[1].out), token,
+                        a.part[0].out_token, a.part[0].out_head, a.part[1].out_token, a.part[1].out_head);
           Part<T, W> o;
           o.narrow(va);
           o.store(dx + l.a);
