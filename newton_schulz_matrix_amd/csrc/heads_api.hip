@@ -167,7 +167,7 @@ NS_API ns_status ns_qk_norm_rope(const ns_qk_norm_rope_args* p, ns_heads q_out, 
 
 NS_API ns_status ns_qk_norm_rope_grad_workspace_size(int64_t tokens, int64_t dim, size_t* bytes) {
   if (!bytes || !qk_sizes_ok(tokens, dim)) return NS_ERR_INVALID_ARG;
-  *bytes = std::max(ALIGN, align_up(sizeof(float) * 2 * dim * qk_grad_blocks(tokens)));
+  *bytes = std::max(ALIGN, align_up(sizeof(float) * 2 * dim * qk_grad_blocks(tokens, dim)));
   return NS_OK;
 }
 

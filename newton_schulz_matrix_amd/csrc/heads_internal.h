@@ -38,7 +38,7 @@ struct QkArgs {
 };
 hipError_t launch_qk_norm_rope(const QkArgs& a, int type, hipStream_t stream);
 // partial: (blocks, 2, dim), each workgroup's share of the weights' gradients
-int qk_grad_blocks(int64_t tokens);
+int qk_grad_blocks(int64_t tokens, int64_t dim);
 hipError_t launch_qk_norm_rope_grad(const QkArgs& a, int type, float* partial, void* dq_weight,
                                     void* dk_weight, int dweight_type, hipStream_t stream);
 

@@ -287,12 +287,12 @@ __global__ __launch_bounds__(THREADS) void qk_norm_kernel(QkArgs a, int team, in
 // The gradient: waves take tokens in turn and keep their share of the weights'
 // gradients in registers; a workgroup adds its waves' shares at the end.
 template <class T, int W>
-__global__ __launch_bounds__(THREADS) void qk_grad_kernel(QkArgs a, int team, int rounds,
+__global__ __launch_bounds__(THREADS, W == 8 ? 3 : 4) void qk_grad_kernel(QkArgs a, int team, int rounds,
                                                           float* partial) {
   constexpr int U = sizeof(T) == 2 ? 2 : 1;
   __shared__ float2 tables[WAVES][MAX_PAIRS];
   __shared__ float weights[2][QK_MAX_DIM];
-  __shared__ float shares[WAVES][2][QK_MAX_DIM];
+  __shared__ float shares[WAVES][4 * W][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool norm = a.part[0].weight != nullptr;
   const Lane<W> l(a, lane & (team - 1));
@@ -404,21 +404,21 @@ __global__ __launch_bounds__(THREADS) void qk_grad_kernel(QkArgs a, int team, in
   }
   if (!norm) return;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < W; ++e) {
-        float v = dw[k][h][e];
-        for (int off = team; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
-        if (lane < team && l.there) shares[wave][k][(h ? l.b : l.a) + e] = v;
-      }
+  for (int i = 0; i < 4 * W; ++i) shares[wave][i][lane] = dw[i / (2 * W)][i / W % 2][i % W];
   __syncthreads();
+  // a thread a column: the lane of a team and the value that hold it, of all teams and waves
   for (int i = threadIdx.x; i < 2 * a.dim; i += THREADS) {
     const int k = i >= a.dim, col = i - k * a.dim;
+    int j = col / (2 * W), value = col % (2 * W);
+    if (!a.interleaved && col < a.rotary) {
+      const int second = col >= a.rotary / 2, at = col - second * (a.rotary / 2);
+      j = at / W;
+      value = at % W + second * W;
+    }
     float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) v += shares[w][k][col];
+    for (int w = 0; w < WAVES; ++w)
+#pragma unroll 4
+      for (int t = j; t < 64; t += team) v += shares[w][2 * W * k + value][t];
     partial[static_cast<int64_t>(blockIdx.x) * 2 * a.dim + i] = v;
   }
 }
@@ -479,13 +479,16 @@ hipError_t launch_qk_norm_rope(const QkArgs& a, int type, hipStream_t stream) {
   });
 }
 
-int qk_grad_blocks(int64_t tokens) {
-  return static_cast<int>(std::min<int64_t>((tokens + WAVES - 1) / WAVES, 1024));
+// As many workgroups as the chip holds at a time: three a CU where vectors are of 8,
+// whose registers allow no more (16384 tokens of 40 heads of 128: 115 us; 129 with 1024
+// workgroups, a third of which come in a second round), else four.
+int qk_grad_blocks(int64_t tokens, int64_t dim) {
+  return static_cast<int>(std::min<int64_t>((tokens + WAVES - 1) / WAVES, dim % 16 == 0 ? 768 : 1024));
 }
 
 hipError_t launch_qk_norm_rope_grad(const QkArgs& a, int type, float* partial, void* dq_weight,
                                     void* dk_weight, int dweight_type, hipStream_t stream) {
-  const int blocks = a.tokens > 0 ? qk_grad_blocks(a.tokens) : 0;
+  const int blocks = a.tokens > 0 ? qk_grad_blocks(a.tokens, a.dim) : 0;
   if (blocks > 0) {
     const hipError_t e = by_type(type, [&](auto t) {
       using T = decltype(t);
