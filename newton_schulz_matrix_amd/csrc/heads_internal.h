@@ -56,7 +56,7 @@ struct AttnArgs {
   HeadsAt dout, dq, dk, dv;    // gradient only
   float* lse;                  // (q_heads, tokens)
   float* lse2;                 // lse log2(e), gradient only
-  float* delta;                // (q_heads, tokens), gradient only
+  float* delta;                // -delta, (q_heads, tokens), gradient only
   const int* offsets;          // (sequences + 1)
   int tokens, sequences, q_heads, k_heads, dim;
   bool clear_rest;

@@ -49,8 +49,8 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
   __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];   // keys, values, twice
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Work w = work_of(blockIdx.x, a.q_heads, a.k_heads, tiles);
-  const Place at = place_of<QUERIES>(a.offsets, a.sequences, a.tokens, w.tile);
+  const Work w = work_of(blockIdx.x, a.q_heads, a.k_heads);
+  const Place at = place_of<QUERIES, false>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
   if (at.rest) {
     if (a.clear_rest) clear_rows<T>(a, w.head, at.begin + at.row, min(at.begin + at.row + QUERIES, at.begin + at.length));
@@ -93,13 +93,14 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
     if (n + 1 < steps) fetch_tile(n + 1);
     const int first_key = n * KEYS;
     if (first_key > first_query + 31) continue;
-    const uint32_t kt = lds + (n & 1) * 2 * TILE, vt = kt + TILE;
+    const auto kt = rows.in(lds + (n & 1) * 2 * TILE);
+    const auto vt = columns.in(lds + (n & 1) * 2 * TILE + TILE);
     Acc s[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       s[i] = no_sum();
 #pragma unroll
-      for (int j = 0; j < KC; ++j) s[i] = product(rows.template read<T>(kt, 32 * i, j), q[j], s[i]);
+      for (int j = 0; j < KC; ++j) s[i] = product(kt.template read<T>(j, 32 * i * Tile<DP>::ROW), q[j], s[i]);
     }
     if (first_key + KEYS - 1 > first_query) {   // some keys lie behind some queries
 #pragma unroll
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
     for (int j = 0; j < KEYS / 16; ++j) {
       const V8 p = operand<T>(s[j / 2], j % 2);   // weights of at most 2^15, rounded to T: half a step each
 #pragma unroll
-      for (int t = 0; t < DT; ++t) o[t] = product(columns.template read<T>(vt, j, t), p, o[t]);
+      for (int t = 0; t < DT; ++t) o[t] = product(vt.template read<T>(t, 16 * j * Tile<DP>::ROW), p, o[t]);
     }
   }
 

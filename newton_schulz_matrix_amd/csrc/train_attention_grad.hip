@@ -47,7 +47,7 @@ __global__ void clear_peaks_kernel(uint32_t* peaks) {
   if (threadIdx.x < 2) peaks[threadIdx.x] = 0;
 }
 
-// Rows of heads: delta, and lse times log2(e) for the kernels below, 16 lanes a row,
+// Rows of heads: -delta, and lse times log2(e) for the kernels below, 16 lanes a row,
 // 16 rows one behind the other a workgroup. For fp16 also the greatest norms of dout's
 // rows and v's; a maximum does not depend on the order in which it is taken.
 template <class T>
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256) void delta_kernel(AttnArgs a, uint32_t* peaks)
     for (int off = 8; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 64);
     if (there && lane == 0) {
       const int64_t at = static_cast<int64_t>(head) * a.tokens + token;
-      a.delta[at] = dot;
+      a.delta[at] = -dot;
       a.lse2[at] = a.lse[at] * LOG2E;
     }
   } else if (there) {
@@ -110,8 +110,8 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
   __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];   // keys, values, twice
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Work w = work_of(blockIdx.x, a.q_heads, a.k_heads, tiles);
-  const Place at = place_of<ROWS>(a.offsets, a.sequences, a.tokens, w.tile);
+  const Work w = work_of(blockIdx.x, a.q_heads, a.k_heads);
+  const Place at = place_of<ROWS, false>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
   if (at.rest) {
     if (a.clear_rest)
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
   const float scaled = NARROW<T> ? ds_scale(peaks) : 1.f;
   const float to_ds = NARROW<T> ? scaled * (1.f / 16384.f) : 1.f;
   const float lse2 = (there ? a.lse2[stat] : 0.f) - (NARROW<T> ? LIFT : 0.f);
-  const float delta = (there ? a.delta[stat] : 0.f) * to_ds;
+  const float delta = (there ? -a.delta[stat] : 0.f) * to_ds;
   const RowReader<DP> rows(lane);
   const ColumnReader<DP> columns(lane);
   const float c = a.scale * LOG2E;
@@ -159,29 +159,32 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
     __syncthreads();
     if (n + 1 < steps) fetch_tile(n + 1);
     const int first_key = n * STEP;
-    const uint32_t kt = lds + (n & 1) * 2 * TILE, vt = kt + TILE;
+    const auto kt = rows.in(lds + (n & 1) * 2 * TILE);
+    const auto kc = columns.in(lds + (n & 1) * 2 * TILE);
 #pragma unroll
     for (int i = 0; i < STEP / 32; ++i) {
-      const int key0 = first_key + 32 * i;
+      const int key0 = first_key + 32 * i, at_row = 32 * i * Tile<DP>::ROW;
       if (key0 > first_query + 31) break;
       Acc s = no_sum(), dp = no_sum();
 #pragma unroll
-      for (int j = 0; j < KC; ++j) s = product(rows.template read<T>(kt, 32 * i, j), q[j], s);
+      for (int j = 0; j < KC; ++j) s = product(kt.template read<T>(j, at_row), q[j], s);
 #pragma unroll
-      for (int j = 0; j < KC; ++j) dp = product(rows.template read<T>(vt, 32 * i, j), g[j], dp);
-      const bool edge = key0 + 31 > first_query;
+      for (int j = 0; j < KC; ++j) dp = product(kt.template read<T>(j, at_row + TILE), g[j], dp);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2));
-        const float d = p * (NARROW<T> ? fmaf(dp[r], to_ds, -delta) : dp[r] - delta);
-        const int key = key0 + 8 * (r / 4) + 4 * half + r % 4;
-        s[r] = edge && key > query ? 0.f : d;
+      for (int r = 0; r < 16; ++r)
+        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2)) *
+               (NARROW<T> ? fmaf(dp[r], to_ds, -delta) : dp[r] - delta);
+      if (key0 + 31 > first_query) {   // some keys lie behind some queries
+        const int hidden = query - key0 - 4 * half;   // rows above it are
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = 8 * (r / 4) + r % 4 > hidden ? 0.f : s[r];
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const V8 ds = operand<T>(s, j);   // rounded to T, half a step each
 #pragma unroll
-        for (int t = 0; t < DT; ++t) dq[t] = product(columns.template read<T>(kt, 2 * i + j, t), ds, dq[t]);
+        for (int t = 0; t < DT; ++t)
+          dq[t] = product(kc.template read<T>(t, at_row + 16 * j * Tile<DP>::ROW), ds, dq[t]);
       }
     }
   }
@@ -207,8 +210,8 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = wave / 4;           // of the queries
-  const Work w = work_of(blockIdx.x, a.k_heads, a.k_heads, tiles);
-  const Place at = place_of<ROWS>(a.offsets, a.sequences, a.tokens, tiles - 1 - w.tile);   // the first are the longest
+  const Work w = work_of(blockIdx.x, a.k_heads, a.k_heads);
+  const Place at = place_of<ROWS, true>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
   if (at.rest) {
     if (a.clear_rest) {
@@ -262,36 +265,43 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
     __syncthreads();
     if (n + 1 < steps) fetch_tile(n + 1);
     const int first_query = (begin + n % each) * KV_STEP;
-    const uint32_t qt = lds + (n & 1) * STAGE, gt = qt + TILE;
+    const uint32_t qt = lds + (n & 1) * STAGE;
 #pragma unroll 1
     for (int i = 0; i < KV_STEP / 64; ++i) {
       const int row0 = 64 * i + 32 * part, query0 = first_query + row0;
       if (query0 + 31 < first_key) continue;
-      const uint32_t qr = qt + row0 * Tile<DP>::ROW, gr = gt + row0 * Tile<DP>::ROW;
+      const auto qr = rows.in(qt + row0 * Tile<DP>::ROW);   // dout's tile lies TILE behind
+      const auto qc = columns.in(qt + row0 * Tile<DP>::ROW);
       const __attribute__((address_space(3))) float* const stats =
-          (const __attribute__((address_space(3))) float*)(gt + TILE) + row0 + 4 * half;
-      Acc s = no_sum(), dp = no_sum();
+          (const __attribute__((address_space(3))) float*)(qt + 2 * TILE) + row0 + 4 * half;
+      Acc s = no_sum(), dp;
 #pragma unroll
-      for (int j = 0; j < KC; ++j) s = product(rows.template read<T>(qr, 0, j), k[j], s);
+      for (int r = 0; r < 16; ++r) dp[r] = stats[KV_STEP + 8 * (r / 4) + r % 4];   // -delta
 #pragma unroll
-      for (int j = 0; j < KC; ++j) dp = product(rows.template read<T>(gr, 0, j), v[j], dp);
-      const int hidden = query0 < first_key + 31 ? key - query0 - 4 * half : -64;   // rows below it are
+      for (int j = 0; j < KC; ++j) s = product(qr.template read<T>(j, 0), k[j], s);
+#pragma unroll
+      for (int j = 0; j < KC; ++j) dp = product(qr.template read<T>(j, TILE), v[j], dp);
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int row = 8 * (r / 4) + r % 4;
-        const float lse2 = stats[row] - (NARROW<T> ? LIFT : 0.f), delta = stats[KV_STEP + row];
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2));
-        const float d = p * (NARROW<T> ? (dp[r] - delta) * to_ds : dp[r] - delta);
-        s[r] = row < hidden ? 0.f : p;
-        dp[r] = row < hidden ? 0.f : d;
+        const float lse2 = stats[8 * (r / 4) + r % 4];
+        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, (NARROW<T> ? LIFT : 0.f) - lse2));
+        dp[r] = NARROW<T> ? s[r] * (dp[r] * to_ds) : s[r] * dp[r];
+      }
+      if (query0 < first_key + 31) {   // some keys lie behind some queries
+        const int hidden = key - query0 - 4 * half;   // rows below it are
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[r] = 8 * (r / 4) + r % 4 < hidden ? 0.f : s[r];
+          dp[r] = 8 * (r / 4) + r % 4 < hidden ? 0.f : dp[r];
+        }
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const V8 p = operand<T>(s, j), ds = operand<T>(dp, j);   // rounded to T, half a step each
 #pragma unroll
         for (int t = 0; t < DT; ++t) {
-          dv[t] = product(columns.template read<T>(gr, j, t), p, dv[t]);
-          dk[t] = product(columns.template read<T>(qr, j, t), ds, dk[t]);
+          dv[t] = product(qc.template read<T>(t, TILE + 16 * j * Tile<DP>::ROW), p, dv[t]);
+          dk[t] = product(qc.template read<T>(t, 16 * j * Tile<DP>::ROW), ds, dk[t]);
         }
       }
     }
