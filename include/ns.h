@@ -584,7 +584,8 @@ typedef struct {
   float scale;
 } ns_attention_args;
 ns_status ns_attention(const ns_attention_args* args, ns_heads out, float* lse, void* stream);
-ns_status ns_attention_grad_workspace_size(int64_t tokens, int64_t q_heads, size_t* bytes);
+ns_status ns_attention_grad_workspace_size(int64_t tokens, int64_t sequences, int64_t q_heads,
+                                           int64_t k_heads, int64_t dim, size_t* bytes);
 ns_status ns_attention_grad(const ns_attention_args* args, ns_heads dout, ns_heads out,
                             const float* lse, ns_heads dq, ns_heads dk, ns_heads dv, void* ws,
                             size_t ws_bytes, void* stream);

@@ -243,17 +243,16 @@ HeadsAt place(const ns_heads& h, const View& v) {
   // one token: its stride is not used, whatever it is
   return {h.data, v.tokens <= 1 ? v.dim : v.ld_token, v.heads <= 1 ? 0 : v.ld_head};
 }
-bool attention_sizes_ok(int64_t tokens, int64_t q_heads) {
-  return rows_ok(tokens) && q_heads >= 1 && q_heads <= NS_MAX_HEADS;
+bool attention_sizes_ok(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t k_heads, int64_t dim) {
+  return rows_ok(tokens) && rows_ok(sequences) && q_heads >= 1 && q_heads <= NS_MAX_HEADS && k_heads >= 1 &&
+         k_heads <= q_heads && q_heads % k_heads == 0 && dim >= 8 && dim <= ATTN_MAX_DIM && dim % 8 == 0;
 }
 struct AttnViews {
   View q, k, v;
 };
 ns_status check_attention(const ns_attention_args* p, AttnArgs* a, AttnViews* in) {
   if (!p || (p->dtype != NS_DT_BF16 && p->dtype != NS_DT_F16)) return NS_ERR_INVALID_ARG;
-  if (!attention_sizes_ok(p->tokens, p->q_heads) || !rows_ok(p->sequences)) return NS_ERR_INVALID_ARG;
-  if (p->k_heads < 1 || p->k_heads > p->q_heads || p->q_heads % p->k_heads != 0) return NS_ERR_INVALID_ARG;
-  if (p->dim < 8 || p->dim > ATTN_MAX_DIM || p->dim % 8 != 0) return NS_ERR_INVALID_ARG;
+  if (!attention_sizes_ok(p->tokens, p->sequences, p->q_heads, p->k_heads, p->dim)) return NS_ERR_INVALID_ARG;
   if (!std::isfinite(p->scale) || p->scale <= 0.f) return NS_ERR_INVALID_ARG;
   if (p->tokens == 0) return NS_OK;
   in->q = view(p->q, p->tokens, p->q_heads, p->dim, 2);
@@ -277,14 +276,18 @@ ns_status check_attention(const ns_attention_args* p, AttnArgs* a, AttnViews* in
   return NS_OK;
 }
 struct AttnGradPlan {
-  size_t delta, peaks, total;   // byte offsets, bytes
+  int parts;
+  size_t delta, peaks, sums, total;   // byte offsets, bytes
 };
-AttnGradPlan attention_grad_plan(int64_t tokens, int64_t q_heads) {
+AttnGradPlan attention_grad_plan(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t k_heads, int64_t dim) {
   AttnGradPlan p;
   const size_t rows = align_up(sizeof(float) * static_cast<size_t>(tokens) * q_heads);
+  p.parts = attention_grad_parts(tokens, sequences, k_heads);
   p.delta = rows;
   p.peaks = 2 * rows;
-  p.total = 2 * rows + ALIGN;
+  p.sums = p.peaks + align_up(sizeof(uint32_t) * 2 * PEAKS);
+  p.total = p.sums;
+  if (p.parts > 1) p.total += align_up(sizeof(float) * 2 * p.parts * static_cast<size_t>(tokens) * k_heads * dim);
   return p;
 }
 
@@ -310,9 +313,10 @@ NS_API ns_status ns_attention(const ns_attention_args* p, ns_heads out, float* l
   return from_hip(launch_attention(a, p->dtype, static_cast<hipStream_t>(stream)));
 }
 
-NS_API ns_status ns_attention_grad_workspace_size(int64_t tokens, int64_t q_heads, size_t* bytes) {
-  if (!bytes || !attention_sizes_ok(tokens, q_heads)) return NS_ERR_INVALID_ARG;
-  *bytes = attention_grad_plan(tokens, q_heads).total;
+NS_API ns_status ns_attention_grad_workspace_size(int64_t tokens, int64_t sequences, int64_t q_heads,
+                                                  int64_t k_heads, int64_t dim, size_t* bytes) {
+  if (!bytes || !attention_sizes_ok(tokens, sequences, q_heads, k_heads, dim)) return NS_ERR_INVALID_ARG;
+  *bytes = attention_grad_plan(tokens, sequences, q_heads, k_heads, dim).total;
   return NS_OK;
 }
 
@@ -329,7 +333,7 @@ NS_API ns_status ns_attention_grad(const ns_attention_args* p, ns_heads dout, ns
                           view(dk, p->tokens, p->k_heads, p->dim, 2),
                           view(dv, p->tokens, p->k_heads, p->dim, 2)};
   if (!vectors_ok(g) || !vectors_ok(o) || !lse || !aligned(lse, 4)) return NS_ERR_INVALID_ARG;
-  const AttnGradPlan plan = attention_grad_plan(p->tokens, p->q_heads);
+  const AttnGradPlan plan = attention_grad_plan(p->tokens, p->sequences, p->q_heads, p->k_heads, p->dim);
   const Span l = dense(lse, p->tokens * p->q_heads, 4), ends = dense(p->offsets, p->sequences + 1, 4);
   const Span work = dense(ws, plan.total, 1);
   for (int i = 0; i < 3; ++i) {
@@ -356,6 +360,7 @@ NS_API ns_status ns_attention_grad(const ns_attention_args* p, ns_heads dout, ns
   a.lse = const_cast<float*>(lse);
   a.lse2 = reinterpret_cast<float*>(w);
   a.delta = reinterpret_cast<float*>(w + plan.delta);
-  return from_hip(launch_attention_grad(a, p->dtype, reinterpret_cast<uint32_t*>(w + plan.peaks),
+  return from_hip(launch_attention_grad(a, p->dtype, plan.parts, reinterpret_cast<uint32_t*>(w + plan.peaks),
+                                        reinterpret_cast<float*>(w + plan.sums),
                                         static_cast<hipStream_t>(stream)));
 }

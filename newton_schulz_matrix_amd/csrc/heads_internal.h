@@ -63,7 +63,13 @@ struct AttnArgs {
   float scale;
 };
 hipError_t launch_attention(const AttnArgs& a, int type, hipStream_t stream);
-// peaks: two words, fp16 only
-hipError_t launch_attention_grad(const AttnArgs& a, int type, uint32_t* peaks, hipStream_t stream);
+// Greatest norms of a head's rows in dout and v, in so many places each, so that
+// waves do not queue for one (fp16 only).
+constexpr int PEAKS = 64;
+// Into how many parts a workgroup's queries are cut for dk and dv; from two on their
+// sums go through `sums`: (parts, 2, k_heads, tokens, dim) fp32.
+int attention_grad_parts(int64_t tokens, int64_t sequences, int64_t k_heads);
+hipError_t launch_attention_grad(const AttnArgs& a, int type, int parts, uint32_t* peaks, float* sums,
+                                 hipStream_t stream);
 
 }  // namespace nsmi

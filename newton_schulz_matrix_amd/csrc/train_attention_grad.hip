@@ -16,6 +16,9 @@
 // times 2^14, and dS times a power of two that keeps the largest one possible
 // (2 max |dout| max |v|, norms of a head's rows) below 2^15; both are taken back from
 // the sums in fp32.
+#include <algorithm>
+#include <type_traits>
+
 #include "attention_device.h"
 #include "train_device.h"
 #include "train_internal.h"
@@ -36,7 +39,10 @@ constexpr float LIFT = 14.f;
 
 // What dS is multiplied by, for fp16.
 __device__ __forceinline__ float ds_scale(const uint32_t* peaks) {
-  const float most = 2.f * __builtin_bit_cast(float, peaks[0]) * __builtin_bit_cast(float, peaks[1]);
+  const int lane = threadIdx.x & 63;
+  static_assert(PEAKS == 64, "one for each lane");
+  const float most = 2.f * wave_max(__builtin_bit_cast(float, peaks[lane])) *
+                     wave_max(__builtin_bit_cast(float, peaks[PEAKS + lane]));
   if (!(most > 0.f && most < INFINITY)) return 1.f;
   int e;
   frexpf(most, &e);
@@ -44,7 +50,7 @@ __device__ __forceinline__ float ds_scale(const uint32_t* peaks) {
 }
 
 __global__ void clear_peaks_kernel(uint32_t* peaks) {
-  if (threadIdx.x < 2) peaks[threadIdx.x] = 0;
+  peaks[threadIdx.x] = 0;
 }
 
 // Rows of heads: -delta, and lse times log2(e) for the kernels below, 16 lanes a row,
@@ -85,7 +91,9 @@ __global__ __launch_bounds__(256) void delta_kernel(AttnArgs a, uint32_t* peaks)
 #pragma unroll
     for (int off = 8; off >= 1; off >>= 1) norm += __shfl_xor(norm, off, 64);
     norm = wave_max(sqrtf(norm));   // (a NaN is passed over: its rows are NaN anyway)
-    if ((threadIdx.x & 63) == 0) atomicMax(peaks + (head < a.q_heads ? 0 : 1), __builtin_bit_cast(uint32_t, norm));
+    if ((threadIdx.x & 63) == 0)
+      atomicMax(peaks + (head < a.q_heads ? 0 : PEAKS) + (4 * blockIdx.x + threadIdx.x / 64 + 7 * head) % PEAKS,
+                __builtin_bit_cast(uint32_t, norm));
   }
 }
 
@@ -200,8 +208,13 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
 constexpr int KV_WAVES = 8, KV_THREADS = 64 * KV_WAVES;
 constexpr int KV_STEP = 128;          // queries of a tile
 
+//
+// Where the keys alone would not fill the chip, `parts` workgroups share the
+// queries of the same keys, and leave their sums in fp32 for a kernel that adds
+// them up in order.
 template <class T, int DP>
-__global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const uint32_t* peaks, int tiles) {
+__global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const uint32_t* peaks, int tiles,
+                                                            int parts, float* sums) {
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32;
   constexpr int TILE = KV_STEP * Tile<DP>::ROW, STATS = 2 * KV_STEP * 4, STAGE = 2 * TILE + STATS;
@@ -209,12 +222,14 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
   __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];   // queries, dout, lse, delta, twice
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int part = wave / 4;           // of the queries
-  const Work w = work_of(blockIdx.x, a.k_heads, a.k_heads);
+  const int side = wave / 4;           // of a tile's queries
+  const unsigned blocks = gridDim.x / parts;
+  const int part = blockIdx.x / blocks;
+  const Work w = work_of(blockIdx.x - part * blocks, a.k_heads, a.k_heads);
   const Place at = place_of<ROWS, true>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
   if (at.rest) {
-    if (a.clear_rest) {
+    if (a.clear_rest && part == 0) {
       const int first = at.begin + at.row, last = min(first + ROWS, at.begin + at.length);
       clear_rows<T>(a.dk, w.head, a.dim, first, last);
       clear_rows<T>(a.dv, w.head, a.dim, first, last);
@@ -229,7 +244,9 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
   const Copier<DP, KV_STEP, KV_WAVES> q_copy(wave, lane, q_step, a.dim), g_copy(wave, lane, g_step, a.dim);
   const uint32_t lds = lds_address(smem);
   const int begin = at.row / KV_STEP;
-  const int each = (at.length + KV_STEP - 1) / KV_STEP - begin, steps = each * group;   // each >= 1
+  const int each = (at.length + KV_STEP - 1) / KV_STEP - begin;   // >= 1
+  const int64_t all = static_cast<int64_t>(each) * group;
+  const int first_step = static_cast<int>(all * part / parts), steps = static_cast<int>(all * (part + 1) / parts);
   auto fetch_tile = [&](int n) {
     const uint32_t to = lds + (n & 1) * STAGE;
     const int h = n / each, first = (begin + n - h * each) * KV_STEP, rows = at.length - first;
@@ -241,7 +258,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
       copy4(descriptor(from, left > 0 ? 4 * left : 0), to + 2 * TILE + wave * 64 * 4, 4 * lane);
     }
   };
-  fetch_tile(0);
+  if (first_step < steps) fetch_tile(first_step);
 
   const int first_key = at.row + 32 * (wave & 3), key = first_key + (lane & 31);
   const bool there = key < at.length;
@@ -260,7 +277,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
 #pragma unroll
   for (int t = 0; t < DT; ++t) dk[t] = dv[t] = no_sum();
 
-  for (int n = 0; n < steps; ++n) {
+  for (int n = first_step; n < steps; ++n) {
     copies_done();
     __syncthreads();
     if (n + 1 < steps) fetch_tile(n + 1);
@@ -268,7 +285,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
     const uint32_t qt = lds + (n & 1) * STAGE;
 #pragma unroll 1
     for (int i = 0; i < KV_STEP / 64; ++i) {
-      const int row0 = 64 * i + 32 * part, query0 = first_query + row0;
+      const int row0 = 64 * i + 32 * side, query0 = first_query + row0;
       if (query0 + 31 < first_key) continue;
       const auto qr = rows.in(qt + row0 * Tile<DP>::ROW);   // dout's tile lies TILE behind
       const auto qc = columns.in(qt + row0 * Tile<DP>::ROW);
@@ -309,36 +326,81 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
 
   // the first four waves finish dk, the others dv
   __syncthreads();
-  float* const sums = reinterpret_cast<float*>(smem) + (wave & 3) * 64 * DP / 2 + lane;
-  float* const give = sums + (part ? 0 : 2 * 64 * DP);
-  float* const take = sums + (part ? 2 * 64 * DP : 0);
+  float* const shared = reinterpret_cast<float*>(smem) + (wave & 3) * 64 * DP / 2 + lane;
+  float* const give = shared + (side ? 0 : 2 * 64 * DP);
+  float* const take = shared + (side ? 2 * 64 * DP : 0);
 #pragma unroll
   for (int t = 0; t < DT; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) give[64 * (16 * t + r)] = part ? dk[t][r] : dv[t][r];
+    for (int r = 0; r < 16; ++r) give[64 * (16 * t + r)] = side ? dk[t][r] : dv[t][r];
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < DT; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) dk[t][r] = (part ? dv[t][r] : dk[t][r]) + take[64 * (16 * t + r)];
-  const HeadsAt& to = part ? a.dv : a.dk;
-  T* row = static_cast<T*>(to.p) + token * to.token + w.head * to.head;
-  const float by = part == 0 ? a.scale / scaled : NARROW<T> ? 1.f / 16384.f : 1.f;
-  store_columns<T, DP>(there ? row : nullptr, a.dim, half, dk, by);
+    for (int r = 0; r < 16; ++r) dk[t][r] = (side ? dv[t][r] : dk[t][r]) + take[64 * (16 * t + r)];
+  const float by = side == 0 ? a.scale / scaled : NARROW<T> ? 1.f / 16384.f : 1.f;
+  if (parts == 1) {
+    const HeadsAt& to = side ? a.dv : a.dk;
+    T* row = static_cast<T*>(to.p) + token * to.token + w.head * to.head;
+    store_columns<T, DP>(there ? row : nullptr, a.dim, half, dk, by);
+  } else if (there) {
+    float* row = sums + (((static_cast<int64_t>(part) * 2 + side) * a.k_heads + w.head) * a.tokens + token) * a.dim;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int column = 32 * t + 8 * g + 4 * half;
+        if (column < a.dim)
+          *reinterpret_cast<float4*>(row + column) = make_float4(dk[t][4 * g] * by, dk[t][4 * g + 1] * by,
+                                                                 dk[t][4 * g + 2] * by, dk[t][4 * g + 3] * by);
+      }
+  }
+}
+
+// Adds up the parts' sums, eight columns a lane.
+template <class T>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int parts, const float* sums) {
+  const int chunks = a.dim / 8, side = blockIdx.y / a.k_heads, head = blockIdx.y % a.k_heads;
+  const int i = blockIdx.x * 256 + threadIdx.x, token = i / chunks, column = i % chunks * 8;
+  if (token < offset_at(a.offsets, 0, a.tokens) || token >= offset_at(a.offsets, a.sequences, a.tokens)) return;
+  const int64_t one = static_cast<int64_t>(a.k_heads) * a.tokens * a.dim;
+  const float* from = sums + (static_cast<int64_t>(side) * a.k_heads + head) * a.tokens * a.dim +
+                      static_cast<int64_t>(token) * a.dim + column;
+  float v[VEC];
+  load8(from, v);
+  for (int k = 1; k < parts; ++k) {
+    float x[VEC];
+    load8(from + 2 * k * one, x);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] += x[e];
+  }
+  const HeadsAt& to = side ? a.dv : a.dk;
+  store8(static_cast<T*>(to.p) + token * to.token + head * to.head + column, v);
 }
 
 }  // namespace
 
-hipError_t launch_attention_grad(const AttnArgs& a, int type, uint32_t* peaks, hipStream_t stream) {
+// Parts as many as fill the 256 CUs with the one workgroup that each holds, and at
+// most eight: 2064 tokens of 6 heads that read 2 take PARTS_US us so, ONE_US in one part.
+int attention_grad_parts(int64_t tokens, int64_t sequences, int64_t k_heads) {
+  const int64_t blocks = tiles_of(tokens, sequences, ROWS) * k_heads;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, 256 / blocks)));
+}
+
+hipError_t launch_attention_grad(const AttnArgs& a, int type, int parts, uint32_t* peaks, float* sums,
+                                 hipStream_t stream) {
   const int64_t tiles = tiles_of(a.tokens, a.sequences, ROWS);
   auto on = [&](auto t, auto dp) {
     using T = decltype(t);
     constexpr int DP = dp();
-    if (NARROW<T>) hipLaunchKernelGGL(clear_peaks_kernel, dim3(1), dim3(64), 0, stream, peaks);
+    if (NARROW<T>) hipLaunchKernelGGL(clear_peaks_kernel, dim3(1), dim3(2 * PEAKS), 0, stream, peaks);
     hipLaunchKernelGGL(delta_kernel<T>, dim3((a.tokens + 15) / 16, a.q_heads + (NARROW<T> ? a.k_heads : 0)),
                        dim3(256), 0, stream, a, peaks);
-    hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.k_heads)), dim3(KV_THREADS), 0,
-                       stream, a, peaks, static_cast<int>(tiles));
+    hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.k_heads * parts)),
+                       dim3(KV_THREADS), 0, stream, a, peaks, static_cast<int>(tiles), parts, sums);
+    if (parts > 1)
+      hipLaunchKernelGGL(join_kernel<T>, dim3((a.tokens * (a.dim / 8) + 255) / 256, 2 * a.k_heads), dim3(256), 0,
+                         stream, a, parts, sums);
     hipLaunchKernelGGL((dq_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.q_heads)), dim3(THREADS), 0,
                        stream, a, peaks, static_cast<int>(tiles));
     return hipGetLastError();

@@ -47,7 +47,7 @@ SIGNATURES = {
     "ns_qk_norm_rope_grad": [ctypes.POINTER(_QkNormRopeArgs), _Heads, _Heads, _Heads, _Heads, _vp, _vp,
                              _int, _vp, _size, _vp],
     "ns_attention": [ctypes.POINTER(_AttentionArgs), _Heads, _vp, _vp],
-    "ns_attention_grad_workspace_size": [_i64, _i64, ctypes.POINTER(_size)],
+    "ns_attention_grad_workspace_size": [_i64] * 5 + [ctypes.POINTER(_size)],
     "ns_attention_grad": [ctypes.POINTER(_AttentionArgs), _Heads, _Heads, _vp, _Heads, _Heads, _Heads,
                           _vp, _size, _vp],
 }
@@ -199,8 +199,8 @@ def ns_attention(q, k, v, offsets, scale: Optional[float] = None, out=None):
     return out, lse
 
 
-def ns_attention_grad_workspace_size(tokens: int, q_heads: int) -> int:
-    return _sized("ns_attention_grad_workspace_size", tokens, q_heads)
+def ns_attention_grad_workspace_size(tokens: int, sequences: int, q_heads: int, k_heads: int, dim: int) -> int:
+    return _sized("ns_attention_grad_workspace_size", tokens, sequences, q_heads, k_heads, dim)
 
 
 def ns_attention_grad(dout, q, k, v, out, lse, offsets, scale: Optional[float] = None, dq=None, dk=None,
@@ -217,7 +217,8 @@ def ns_attention_grad(dout, q, k, v, out, lse, offsets, scale: Optional[float] =
     dq, to_q = _new_or_heads(dq, "dq", dev, q)
     dk, to_k = _new_or_heads(dk, "dk", dev, k)
     dv, to_v = _new_or_heads(dv, "dv", dev, v)
-    workspace = _given_or_new(workspace, ns_attention_grad_workspace_size(tokens, q_heads), q.device)
+    workspace = _given_or_new(workspace, ns_attention_grad_workspace_size(
+        tokens, args.sequences, q_heads, args.k_heads, args.dim), q.device)
     _check(library().ns_attention_grad(
         args, _heads_of(dout, "dout", dev, q.shape, q.dtype), _heads_of(out, "out", dev, q.shape, q.dtype),
         _dense(lse, (q_heads, tokens), "lse", dev, torch.float32), to_q, to_k, to_v, workspace.data_ptr(),
