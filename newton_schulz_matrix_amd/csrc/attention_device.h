@@ -21,6 +21,8 @@
 
 namespace nsmi {
 
+constexpr int CUS = 256;
+
 typedef float Acc __attribute__((ext_vector_type(16)));
 typedef uint32_t U32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t U32x4 __attribute__((ext_vector_type(4)));
@@ -331,6 +333,11 @@ __device__ __forceinline__ Place place_of(const int* offsets, int sequences, int
 inline int64_t tiles_of(int64_t tokens, int64_t sequences, int rows) {
   return tokens / rows + sequences + 1;
 }
+
+// Whether workgroups of eight waves share the keys of 128 queries: where there is no
+// more than one for a CU (2064 fp16 tokens of 6 heads: dq 33 us with four waves, 26 with
+// eight; one tile of keys, 23 tokens of 32 heads, has nothing to share: 5.5 and 6.4).
+inline bool two_sides(const AttnArgs& a, int64_t tiles) { return tiles * a.q_heads <= CUS; }
 
 // Which head and tile a workgroup takes. Workgroups go to the eight XCDs in turn,
 // each with an L2 of its own: heads that read the same keys and values go to one

@@ -10,6 +10,8 @@
 // query, a row's maximum and sum are its own registers and one exchange, and the
 // weights are the next product's operand as they stand. Keys and values come
 // into LDS directly, the next tile while this one is worked on.
+#include <type_traits>
+
 #include "attention_device.h"
 #include "train_device.h"
 #include "train_internal.h"
@@ -34,21 +36,27 @@ constexpr float LIFT<_Float16> = 7.f;
 template <class T>
 __device__ __forceinline__ void clear_rows(const AttnArgs& a, int head, int first, int last) {
   T* out = static_cast<T*>(a.out.p) + head * a.out.head;
+  const int threads = blockDim.x;
   const int chunks = a.dim / 8, n = (last - first) * chunks;
   const U32x4 zero = {0, 0, 0, 0};
-  for (int i = threadIdx.x; i < n; i += THREADS)
+  for (int i = threadIdx.x; i < n; i += threads)
     *reinterpret_cast<U32x4*>(out + (first + i / chunks) * a.out.token + i % chunks * 8) = zero;
-  for (int r = first + threadIdx.x; r < last; r += THREADS) a.lse[static_cast<int64_t>(head) * a.tokens + r] = 0.f;
+  for (int r = first + threadIdx.x; r < last; r += threads) a.lse[static_cast<int64_t>(head) * a.tokens + r] = 0.f;
 }
 
-template <class T, int DP>
-__global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int tiles) {
+// With two SIDES eight waves share 128 queries, each half of every tile's keys, and
+// bring their sums together at the end: for launches that leave most of a CU empty.
+template <class T, int DP, int SIDES>
+__global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs a, int tiles) {
   typedef typename Eight<T>::type V8;
-  constexpr int KC = DP / 16, DT = DP / 32;
+  constexpr int KC = DP / 16, DT = DP / 32, SUB = KEYS / 32 / SIDES;   // 32 keys a time, SUB of them a tile
   constexpr int TILE = KEYS * Tile<DP>::ROW;
   __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];   // keys, values, twice
+  __shared__ float2 known[SIDES == 2 ? WAVES * 64 : 1];            // reference and sum of the second side
+  static_assert(4 * TILE >= QUERIES * DP * 4, "the sums of one side fit in the tiles");
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int side = wave / WAVES;
   const Work w = work_of(blockIdx.x, a.q_heads, a.k_heads);
   const Place at = place_of<QUERIES, false>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
@@ -60,7 +68,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
   const T* k = static_cast<const T*>(a.k.p) + at.begin * a.k.token + kv_head * a.k.head;
   const T* v = static_cast<const T*>(a.v.p) + at.begin * a.v.token + kv_head * a.v.head;
   const uint32_t k_step = static_cast<uint32_t>(a.k.token * 2), v_step = static_cast<uint32_t>(a.v.token * 2);
-  const Copier<DP, KEYS, WAVES> k_copy(wave, lane, k_step, a.dim), v_copy(wave, lane, v_step, a.dim);
+  const Copier<DP, KEYS, WAVES * SIDES> k_copy(wave, lane, k_step, a.dim), v_copy(wave, lane, v_step, a.dim);
   const uint32_t lds = lds_address(smem);
   const int keys = min(at.length, at.row + QUERIES);   // that any query here sees
   const int steps = (keys + KEYS - 1) / KEYS;
@@ -73,7 +81,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
   };
   fetch_tile(0);
 
-  const int first_query = at.row + 32 * wave, query = first_query + (lane & 31);
+  const int first_query = at.row + 32 * (wave % WAVES), query = first_query + (lane & 31);
   const bool there = query < at.length;
   V8 q[KC];
   load_operands<T, DP>(there ? static_cast<const T*>(a.q.p) + (at.begin + query) * a.q.token + w.head * a.q.head
@@ -91,20 +99,21 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
     copies_done();
     __syncthreads();   // tile n is there, and nobody reads the place of tile n + 1
     if (n + 1 < steps) fetch_tile(n + 1);
-    const int first_key = n * KEYS;
+    const int first_key = n * KEYS + 32 * side;
     if (first_key > first_query + 31) continue;
-    const auto kt = rows.in(lds + (n & 1) * 2 * TILE);
-    const auto vt = columns.in(lds + (n & 1) * 2 * TILE + TILE);
-    Acc s[2];
+    const uint32_t tile = lds + (n & 1) * 2 * TILE + 32 * side * Tile<DP>::ROW;
+    const auto kt = rows.in(tile);
+    const auto vt = columns.in(tile + TILE);
+    Acc s[SUB];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SUB; ++i) {
       s[i] = no_sum();
 #pragma unroll
       for (int j = 0; j < KC; ++j) s[i] = product(kt.template read<T>(j, 32 * i * Tile<DP>::ROW), q[j], s[i]);
     }
-    if (first_key + KEYS - 1 > first_query) {   // some keys lie behind some queries
+    if (first_key + 32 * SUB - 1 > first_query) {   // some keys lie behind some queries
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < SUB; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int key = first_key + 32 * i + 8 * (r / 4) + 4 * half + r % 4;
@@ -113,7 +122,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
     }
     float top = s[0][0];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < SUB; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[i][r]);
     float lower, upper;
@@ -121,7 +130,8 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
     top = fmaxf(lower, upper) * c;
     if (__any(top > ref + LAG + LIFT<T>)) {
       const float to = fmaxf(ref, top - LIFT<T>);
-      const float by = __builtin_amdgcn_exp2f(ref - to);
+      // (a row of the second side may not have met a key yet: its sums stay 0)
+      const float by = SIDES == 2 && to == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref - to);
       ref = to;
       sum *= by;
 #pragma unroll
@@ -129,15 +139,16 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[t][r] *= by;
     }
+    const float base = SIDES == 2 && ref == -INFINITY ? 0.f : ref;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < SUB; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        s[i][r] = __builtin_amdgcn_exp2f(fmaf(s[i][r], c, -ref));
+        s[i][r] = __builtin_amdgcn_exp2f(fmaf(s[i][r], c, -base));
         sum += s[i][r];
       }
 #pragma unroll
-    for (int j = 0; j < KEYS / 16; ++j) {
+    for (int j = 0; j < 2 * SUB; ++j) {
       const V8 p = operand<T>(s[j / 2], j % 2);   // weights of at most 2^15, rounded to T: half a step each
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] = product(vt.template read<T>(t, 16 * j * Tile<DP>::ROW), p, o[t]);
@@ -147,6 +158,28 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
   float lower, upper;
   both_halves(sum, lower, upper);
   sum = lower + upper;
+  if constexpr (SIDES == 2) {
+    __syncthreads();
+    float* const shared = reinterpret_cast<float*>(smem) + wave % WAVES * 64 * DP / 2 + lane;
+    if (side == 1) {
+      known[wave % WAVES * 64 + lane] = make_float2(ref, sum);
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) shared[64 * (16 * t + r)] = o[t][r];
+    }
+    __syncthreads();
+    if (side == 1) return;
+    const float2 other = known[wave * 64 + lane];
+    const float to = fmaxf(ref, other.x);   // (this side has met the first key)
+    const float mine = __builtin_amdgcn_exp2f(ref - to), theirs = __builtin_amdgcn_exp2f(other.x - to);
+    ref = to;
+    sum = sum * mine + other.y * theirs;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[t][r] = o[t][r] * mine + shared[64 * (16 * t + r)] * theirs;
+  }
   T* out = static_cast<T*>(a.out.p) + (at.begin + query) * a.out.token + w.head * a.out.head;
   store_columns<T, DP>(there ? out : nullptr, a.dim, half, o, 1.f / sum);
   if (there && half == 0)
@@ -158,15 +191,19 @@ __global__ __launch_bounds__(THREADS, 2) void attention_kernel(AttnArgs a, int t
 
 hipError_t launch_attention(const AttnArgs& a, int type, hipStream_t stream) {
   const int64_t tiles = tiles_of(a.tokens, a.sequences, QUERIES);
-  auto on = [&](auto t, auto dp) {
+  auto on = [&](auto t, auto dp, auto sides) {
     using T = decltype(t);
-    constexpr int DP = dp();
-    hipLaunchKernelGGL((attention_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.q_heads)), dim3(THREADS),
-                       0, stream, a, static_cast<int>(tiles));
+    constexpr int DP = dp(), SIDES = sides();
+    hipLaunchKernelGGL((attention_kernel<T, DP, SIDES>), dim3(static_cast<unsigned>(tiles * a.q_heads)),
+                       dim3(THREADS * SIDES), 0, stream, a, static_cast<int>(tiles));
     return hipGetLastError();
   };
+  auto sided = [&](auto t, auto dp) {
+    return two_sides(a, tiles) ? on(t, dp, std::integral_constant<int, 2>{})
+                               : on(t, dp, std::integral_constant<int, 1>{});
+  };
   auto shaped = [&](auto t) {
-    return a.dim <= 64 ? on(t, std::integral_constant<int, 64>{}) : on(t, std::integral_constant<int, 128>{});
+    return a.dim <= 64 ? sided(t, std::integral_constant<int, 64>{}) : sided(t, std::integral_constant<int, 128>{});
   };
   return type == NS_DT_BF16 ? shaped(__bf16{}) : shaped(_Float16{});
 }

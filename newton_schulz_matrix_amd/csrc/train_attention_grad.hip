@@ -3,10 +3,10 @@
 //   P = exp(S - lse), S = scale q k^T;   delta = sum of dout out over a head's columns
 //   dv = P^T dout,  dS = P (dout v^T - delta),  dq = scale dS k,  dk = scale dS^T q
 //
-// Bound by the matrix units. Three launches: delta of each row; dk and dv, where a
-// workgroup keeps 128 keys of one key head and goes over the queries of its group's
-// heads behind them; dq, where it keeps 128 queries and goes over the keys before
-// them. S and dout v^T are worked out in both (seven products instead of five): the
+// Bound by the matrix units. Two launches: dq, where a workgroup keeps 128 queries and
+// goes over the keys before them, and which leaves delta of its rows; dk and dv,
+// where it keeps 128 keys of one key head and goes over the queries of its group's
+// heads behind them. S and dout v^T are worked out in both (seven products instead of five): the
 // alternative, adding to dq from every workgroup of keys, would need atomics, whose
 // order changes the sums, or a place for every pair of tiles. Everything is laid out
 // as in the forward pass: the weights of a lane are one row or column, and go on as
@@ -53,48 +53,33 @@ __global__ void clear_peaks_kernel(uint32_t* peaks) {
   peaks[threadIdx.x] = 0;
 }
 
-// Rows of heads: -delta, and lse times log2(e) for the kernels below, 16 lanes a row,
-// 16 rows one behind the other a workgroup. For fp16 also the greatest norms of dout's
-// rows and v's; a maximum does not depend on the order in which it is taken.
+// fp16: the greatest norms of dout's rows of a head and v's, 16 lanes a row, 16 rows
+// one behind the other a workgroup. A maximum does not depend on the order in which
+// it is taken.
 template <class T>
-__global__ __launch_bounds__(256) void delta_kernel(AttnArgs a, uint32_t* peaks) {
+__global__ __launch_bounds__(256) void norms_kernel(AttnArgs a, uint32_t* peaks) {
+  __shared__ float tops[4];
   const int lane = threadIdx.x & 15;
   const int token = blockIdx.x * 16 + threadIdx.x / 16, head = blockIdx.y;
   const int first = offset_at(a.offsets, 0, a.tokens), last = offset_at(a.offsets, a.sequences, a.tokens);
-  const bool there = token >= first && token < last && 8 * lane < a.dim;
-  float dot = 0.f, norm = 0.f;
-  if (head < a.q_heads) {
-    if (there) {
-      float g[VEC], o[VEC];
-      load8(static_cast<const T*>(a.dout.p) + token * a.dout.token + head * a.dout.head + 8 * lane, g);
-      load8(static_cast<const T*>(a.out.p) + token * a.out.token + head * a.out.head + 8 * lane, o);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        dot = fmaf(g[e], o[e], dot);
-        norm = fmaf(g[e], g[e], norm);
-      }
-    }
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 64);
-    if (there && lane == 0) {
-      const int64_t at = static_cast<int64_t>(head) * a.tokens + token;
-      a.delta[at] = -dot;
-      a.lse2[at] = a.lse[at] * LOG2E;
-    }
-  } else if (there) {
+  const bool of_v = head >= a.q_heads;
+  float norm = 0.f;
+  if (token >= first && token < last && 8 * lane < a.dim) {
+    const HeadsAt& from = of_v ? a.v : a.dout;
     float x[VEC];
-    load8(static_cast<const T*>(a.v.p) + token * a.v.token + (head - a.q_heads) * a.v.head + 8 * lane, x);
+    load8(static_cast<const T*>(from.p) + token * from.token + (head - (of_v ? a.q_heads : 0)) * from.head + 8 * lane,
+          x);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) norm = fmaf(x[e], x[e], norm);
   }
-  if constexpr (NARROW<T>) {
 #pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) norm += __shfl_xor(norm, off, 64);
-    norm = wave_max(sqrtf(norm));   // (a NaN is passed over: its rows are NaN anyway)
-    if ((threadIdx.x & 63) == 0)
-      atomicMax(peaks + (head < a.q_heads ? 0 : PEAKS) + (4 * blockIdx.x + threadIdx.x / 64 + 7 * head) % PEAKS,
-                __builtin_bit_cast(uint32_t, norm));
-  }
+  for (int off = 8; off >= 1; off >>= 1) norm += __shfl_xor(norm, off, 64);
+  norm = wave_max(norm);   // (a NaN is passed over: its rows are NaN anyway)
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = norm;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  norm = sqrtf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+  atomicMax(peaks + (of_v ? PEAKS : 0) + (blockIdx.x + 7 * head) % PEAKS, __builtin_bit_cast(uint32_t, norm));
 }
 
 // Rows behind the last sequence: zeros.
@@ -110,14 +95,19 @@ __device__ __forceinline__ void clear_rows(const HeadsAt& to, int head, int dim,
 
 // ------------------------------------------------------------------------ dq
 
-template <class T, int DP>
-__global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32_t* peaks, int tiles) {
+// 32 queries a wave. With two SIDES eight waves share 128 queries, each half of every
+// tile's keys, and add up at the end: for launches that leave most of a CU empty. The
+// rows' delta and lse log2(e) are left for the kernel below.
+template <class T, int DP, int SIDES>
+__global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, const uint32_t* peaks, int tiles) {
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32;
   constexpr int TILE = STEP * Tile<DP>::ROW;
   __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];   // keys, values, twice
+  static_assert(4 * TILE >= ROWS * DP * 4, "the sums of one side fit in the tiles");
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int side = wave / WAVES;
   const Work w = work_of(blockIdx.x, a.q_heads, a.k_heads);
   const Place at = place_of<ROWS, false>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
@@ -130,7 +120,7 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
   const T* k = static_cast<const T*>(a.k.p) + at.begin * a.k.token + kv_head * a.k.head;
   const T* v = static_cast<const T*>(a.v.p) + at.begin * a.v.token + kv_head * a.v.head;
   const uint32_t k_step = static_cast<uint32_t>(a.k.token * 2), v_step = static_cast<uint32_t>(a.v.token * 2);
-  const Copier<DP, STEP, WAVES> k_copy(wave, lane, k_step, a.dim), v_copy(wave, lane, v_step, a.dim);
+  const Copier<DP, STEP, WAVES * SIDES> k_copy(wave, lane, k_step, a.dim), v_copy(wave, lane, v_step, a.dim);
   const uint32_t lds = lds_address(smem);
   const int keys = min(at.length, at.row + ROWS);
   const int steps = (keys + STEP - 1) / STEP;
@@ -142,7 +132,7 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
   };
   fetch_tile(0);
 
-  const int first_query = at.row + 32 * wave, query = first_query + (lane & 31);
+  const int first_query = at.row + 32 * (wave % WAVES), query = first_query + (lane & 31);
   const bool there = query < at.length;
   const int64_t token = at.begin + query;
   V8 q[KC], g[KC];
@@ -150,11 +140,29 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
                        a.dim, half, q);
   load_operands<T, DP>(there ? static_cast<const T*>(a.dout.p) + token * a.dout.token + w.head * a.dout.head : nullptr,
                        a.dim, half, g);
+  float dot = 0.f;
+  {
+    V8 o[KC];
+    load_operands<T, DP>(there ? static_cast<const T*>(a.out.p) + token * a.out.token + w.head * a.out.head : nullptr,
+                         a.dim, half, o);
+#pragma unroll
+    for (int j = 0; j < KC; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dot = fmaf(static_cast<float>(g[j][e]), static_cast<float>(o[j][e]), dot);
+  }
+  float lower, upper;
+  both_halves(dot, lower, upper);
+  dot = lower + upper;
   const int64_t stat = static_cast<int64_t>(w.head) * a.tokens + token;
+  float lse2 = there ? a.lse[stat] * LOG2E : 0.f;
+  if (there && half == 0 && side == 0) {
+    a.delta[stat] = -dot;
+    a.lse2[stat] = lse2;
+  }
   const float scaled = NARROW<T> ? ds_scale(peaks) : 1.f;
   const float to_ds = NARROW<T> ? scaled * (1.f / 16384.f) : 1.f;
-  const float lse2 = (there ? a.lse2[stat] : 0.f) - (NARROW<T> ? LIFT : 0.f);
-  const float delta = (there ? -a.delta[stat] : 0.f) * to_ds;
+  const float delta = dot * to_ds;
+  if (NARROW<T>) lse2 -= LIFT;
   const RowReader<DP> rows(lane);
   const ColumnReader<DP> columns(lane);
   const float c = a.scale * LOG2E;
@@ -166,12 +174,14 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
     copies_done();
     __syncthreads();
     if (n + 1 < steps) fetch_tile(n + 1);
-    const int first_key = n * STEP;
-    const auto kt = rows.in(lds + (n & 1) * 2 * TILE);
-    const auto kc = columns.in(lds + (n & 1) * 2 * TILE);
+    // (one side: both halves of the tile, one after the other)
+    const int key1 = n * STEP + 32 * side;
+    const uint32_t tile = lds + (n & 1) * 2 * TILE + 32 * side * Tile<DP>::ROW;
+    const auto kt = rows.in(tile);
+    const auto kc = columns.in(tile);
 #pragma unroll
-    for (int i = 0; i < STEP / 32; ++i) {
-      const int key0 = first_key + 32 * i, at_row = 32 * i * Tile<DP>::ROW;
+    for (int i = 0; i < STEP / 32 / SIDES; ++i) {
+      const int key0 = key1 + 32 * i, at_row = 32 * i * Tile<DP>::ROW;
       if (key0 > first_query + 31) break;
       Acc s = no_sum(), dp = no_sum();
 #pragma unroll
@@ -195,6 +205,22 @@ __global__ __launch_bounds__(THREADS, 2) void dq_kernel(AttnArgs a, const uint32
           dq[t] = product(kc.template read<T>(t, at_row + 16 * j * Tile<DP>::ROW), ds, dq[t]);
       }
     }
+  }
+  if constexpr (SIDES == 2) {
+    __syncthreads();
+    float* const shared = reinterpret_cast<float*>(smem) + wave % WAVES * 64 * DP / 2 + lane;
+    if (side == 1) {
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) shared[64 * (16 * t + r)] = dq[t][r];
+    }
+    __syncthreads();
+    if (side == 1) return;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) dq[t][r] += shared[64 * (16 * t + r)];
   }
   T* to = static_cast<T*>(a.dq.p) + token * a.dq.token + w.head * a.dq.head;
   store_columns<T, DP>(there ? to : nullptr, a.dim, half, dq, a.scale / scaled);
@@ -384,7 +410,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int parts, const 
 // most eight: 2064 tokens of 6 heads that read 2 take PARTS_US us so, ONE_US in one part.
 int attention_grad_parts(int64_t tokens, int64_t sequences, int64_t k_heads) {
   const int64_t blocks = tiles_of(tokens, sequences, ROWS) * k_heads;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, 256 / blocks)));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, CUS / blocks)));
 }
 
 hipError_t launch_attention_grad(const AttnArgs& a, int type, int parts, uint32_t* peaks, float* sums,
@@ -393,16 +419,23 @@ hipError_t launch_attention_grad(const AttnArgs& a, int type, int parts, uint32_
   auto on = [&](auto t, auto dp) {
     using T = decltype(t);
     constexpr int DP = dp();
-    if (NARROW<T>) hipLaunchKernelGGL(clear_peaks_kernel, dim3(1), dim3(2 * PEAKS), 0, stream, peaks);
-    hipLaunchKernelGGL(delta_kernel<T>, dim3((a.tokens + 15) / 16, a.q_heads + (NARROW<T> ? a.k_heads : 0)),
-                       dim3(256), 0, stream, a, peaks);
+    if constexpr (NARROW<T>) {
+      hipLaunchKernelGGL(clear_peaks_kernel, dim3(1), dim3(2 * PEAKS), 0, stream, peaks);
+      hipLaunchKernelGGL(norms_kernel<T>, dim3((a.tokens + 15) / 16, a.q_heads + a.k_heads), dim3(256), 0, stream,
+                         a, peaks);
+    }
+    auto queries = [&](auto sides) {
+      constexpr int SIDES = sides();
+      hipLaunchKernelGGL((dq_kernel<T, DP, SIDES>), dim3(static_cast<unsigned>(tiles * a.q_heads)),
+                         dim3(THREADS * SIDES), 0, stream, a, peaks, static_cast<int>(tiles));
+    };
+    if (two_sides(a, tiles)) queries(std::integral_constant<int, 2>{});
+    else queries(std::integral_constant<int, 1>{});
     hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.k_heads * parts)),
                        dim3(KV_THREADS), 0, stream, a, peaks, static_cast<int>(tiles), parts, sums);
     if (parts > 1)
       hipLaunchKernelGGL(join_kernel<T>, dim3((a.tokens * (a.dim / 8) + 255) / 256, 2 * a.k_heads), dim3(256), 0,
                          stream, a, parts, sums);
-    hipLaunchKernelGGL((dq_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.q_heads)), dim3(THREADS), 0,
-                       stream, a, peaks, static_cast<int>(tiles));
     return hipGetLastError();
   };
   auto shaped = [&](auto t) {

@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 from typing import Optional, Sequence
 
-from . import _check, _device_tensor, _dtype_code, library
+from . import _check, _device_tensor, library
 from .operators import (_code, _dense, _device_of, _f32, _given_or_new, _i64, _ids_type, _int, _mismatch,
                         _size, _sized, _stream_of, _vp, torch)
 
@@ -53,24 +53,34 @@ SIGNATURES = {
 }
 
 
-def _heads_of(t, name: str, dev: int, shape=None, dtype=None) -> _Heads:
-    """A (tokens, heads, dim) tensor of this shape (and type) on device `dev`."""
-    if t.get_device() != dev or (shape is not None and t.shape != shape) or (
-            dtype is not None and t.dtype != dtype):
-        _mismatch(t, t.shape if shape is None else shape, name, dtype)
+# (data, ld_token, ld_head): a structure within another takes them as they are.
+
+def _heads_of(t, name: str, dev: int):
+    """Address and strides of a (tokens, heads, dim) tensor on device `dev`."""
+    if t.get_device() != dev:
+        _device_tensor(t, name)
     if t.dim() != 3:
         raise ValueError(f"{name} must be (tokens, heads, dim), not {tuple(t.shape)}")
     ld_token, ld_head, one = t.stride()
     if one != 1 and t.shape[2] > 1:
         raise ValueError(f"{name}: heads must be contiguous (stride(-1) == 1)")
-    return _Heads(t.data_ptr(), ld_token, ld_head)
+    return t.data_ptr(), ld_token, ld_head
+
+
+def _heads_like(t, name: str, dev: int, like) -> _Heads:
+    """The same of a tensor that must have like's shape and type."""
+    if t.shape != like.shape or t.dtype is not like.dtype:
+        _mismatch(t, like.shape, name, like.dtype)
+    return _Heads(*_heads_of(t, name, dev))
 
 
 def _new_or_heads(t, name: str, dev: int, like):
     """An output of `like`'s shape and type: (tensor, its _Heads)."""
-    if t is None:
-        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    return t, _heads_of(t, name, dev, like.shape, like.dtype)
+    if t is not None:
+        return t, _heads_like(t, name, dev, like)
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    _, heads, dim = t.shape
+    return t, _Heads(t.data_ptr(), heads * dim, dim)
 
 
 # ------------------------------------- norm and rotation of queries and keys
@@ -80,7 +90,9 @@ def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, sections, inter
         raise ValueError(f"q and k must be (tokens, heads, dim) of the same tokens and dim, not "
                          f"{tuple(q.shape)} and {tuple(k.shape)}")
     tokens, _, dim = q.shape
-    heads_q, heads_k = _heads_of(q, "q", dev), _heads_of(k, "k", dev, dtype=q.dtype)
+    if k.dtype is not q.dtype:
+        _mismatch(k, k.shape, "k", q.dtype)
+    heads_q, heads_k = _heads_of(q, "q", dev), _heads_of(k, "k", dev)
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight: give both or neither")
     weight_ptrs, weight_code = (None, None), 0
@@ -147,8 +159,7 @@ def ns_qk_norm_rope_grad(dout_q, dout_k, q, k, q_weight, k_weight, positions, in
     dout_q's buffer and dk dout_k's, or both views of one larger buffer."""
     dev = _device_of(q, "q")
     args = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, sections, interleaved, dev)
-    g_q = _heads_of(dout_q, "dout_q", dev, q.shape, q.dtype)
-    g_k = _heads_of(dout_k, "dout_k", dev, k.shape, k.dtype)
+    g_q, g_k = _heads_like(dout_q, "dout_q", dev, q), _heads_like(dout_k, "dout_k", dev, k)
     dq, to_q = _new_or_heads(dq, "dq", dev, q)
     dk, to_k = _new_or_heads(dk, "dk", dev, k)
     if q_weight is None:
@@ -169,16 +180,18 @@ def ns_qk_norm_rope_grad(dout_q, dout_k, q, k, q_weight, k_weight, positions, in
 # ------------------------------------------------------------------ attention
 
 def _attention_args(q, k, v, offsets, scale, clear_rest, dev):
-    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or q.shape[::2] != k.shape[::2]:
+    shape, k_shape = q.shape, k.shape
+    if len(shape) != 3 or len(k_shape) != 3 or k_shape != v.shape or shape[::2] != k_shape[::2]:
         raise ValueError(f"q (tokens, q_heads, dim) and k, v (tokens, k_heads, dim) do not go together: "
-                         f"{tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+                         f"{tuple(shape)}, {tuple(k_shape)}, {tuple(v.shape)}")
+    if k.dtype is not q.dtype or v.dtype is not q.dtype:
+        _mismatch(k, k_shape, "k", q.dtype) if k.dtype is not q.dtype else _mismatch(v, k_shape, "v", q.dtype)
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be 1-D: where each sequence begins, and the end of the last")
-    tokens, q_heads, dim = q.shape
-    return _AttentionArgs(_heads_of(q, "q", dev), _heads_of(k, "k", dev, dtype=q.dtype),
-                          _heads_of(v, "v", dev, dtype=q.dtype),
+    tokens, q_heads, dim = shape
+    return _AttentionArgs(_heads_of(q, "q", dev), _heads_of(k, "k", dev), _heads_of(v, "v", dev),
                           _dense(offsets, offsets.shape, "offsets", dev, torch.int32), tokens,
-                          offsets.shape[0] - 1, q_heads, k.shape[1], dim, _code(q),
+                          offsets.shape[0] - 1, q_heads, k_shape[1], dim, _code(q),
                           1 if clear_rest else 0, dim ** -0.5 if scale is None else scale)
 
 
@@ -220,7 +233,7 @@ def ns_attention_grad(dout, q, k, v, out, lse, offsets, scale: Optional[float] =
     workspace = _given_or_new(workspace, ns_attention_grad_workspace_size(
         tokens, args.sequences, q_heads, args.k_heads, args.dim), q.device)
     _check(library().ns_attention_grad(
-        args, _heads_of(dout, "dout", dev, q.shape, q.dtype), _heads_of(out, "out", dev, q.shape, q.dtype),
+        args, _heads_like(dout, "dout", dev, q), _heads_like(out, "out", dev, q),
         _dense(lse, (q_heads, tokens), "lse", dev, torch.float32), to_q, to_k, to_v, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_of(dev)), "ns_attention_grad")
     return dq, dk, dv
