@@ -279,11 +279,15 @@ __device__ __forceinline__ Place place_in_order(const int* offsets, int sequence
   return p;
 }
 
-// Sum over a wave, for all of it.
+// Sum over a wave, in a scalar register: within rows of 16 lanes by shifts (lanes
+// shifted in from outside are 0), then the rows' last lanes.
 __device__ __forceinline__ int wave_total(int v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return __builtin_amdgcn_readfirstlane(v);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  return __builtin_amdgcn_readlane(v, 15) + __builtin_amdgcn_readlane(v, 31) + __builtin_amdgcn_readlane(v, 47) +
+         __builtin_amdgcn_readlane(v, 63);
 }
 
 // The same tiles in the order of their work, the longest first: a tile's work is its
