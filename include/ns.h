@@ -573,8 +573,11 @@ ns_status ns_qk_norm_rope_grad(const ns_qk_norm_rope_args* args, ns_heads dq_out
  * 0 <= tokens <= NS_MAX_ROWS (0 is a no-op), 0 <= sequences <= NS_MAX_ROWS, 1 <= k_heads,
  * q_heads a multiple of it up to NS_MAX_HEADS, dim a multiple of 8 up to 128; scale finite
  * and > 0. All tensors 16-byte aligned with strides that are multiples of 8; a
- * tensor's ld_token >= dim (also of one that is only read) and at most 2^23. Workspace
- * of the gradient call: ns_attention_grad_workspace_size bytes, 256-byte aligned. */
+ * tensor's ld_token >= dim (also of one that is only read) and at most 2^23. Workspaces:
+ * ns_attention_workspace_size and ns_attention_grad_workspace_size bytes, 256-byte
+ * aligned (NULL where the size is 0). They hold the sums of up to 8 parts where few
+ * tiles of 128 rows are cut into them: how a row's sum is ordered depends on the
+ * sizes of the call. */
 typedef struct {
   ns_heads q, k, v;
   const int32_t* offsets;
@@ -583,7 +586,10 @@ typedef struct {
   int clear_rest;
   float scale;
 } ns_attention_args;
-ns_status ns_attention(const ns_attention_args* args, ns_heads out, float* lse, void* stream);
+ns_status ns_attention_workspace_size(int64_t tokens, int64_t sequences, int64_t q_heads,
+                                      int64_t k_heads, int64_t dim, size_t* bytes);
+ns_status ns_attention(const ns_attention_args* args, ns_heads out, float* lse, void* ws,
+                       size_t ws_bytes, void* stream);
 ns_status ns_attention_grad_workspace_size(int64_t tokens, int64_t sequences, int64_t q_heads,
                                            int64_t k_heads, int64_t dim, size_t* bytes);
 ns_status ns_attention_grad(const ns_attention_args* args, ns_heads dout, ns_heads out,

@@ -338,10 +338,33 @@ inline int64_t tiles_of(int64_t tokens, int64_t sequences, int rows) {
   return tokens / rows + sequences + 1;
 }
 
+// The work of one of `parts` workgroups of a tile.
+struct Range {
+  int first, last;
+};
+__device__ __forceinline__ Range range_of(int64_t steps, int part, int parts) {
+  return {static_cast<int>(steps * part / parts), static_cast<int>(steps * (part + 1) / parts)};
+}
+
+// A part's result in memory as fp32: rows of a head by columns of the lane, as for
+// store_columns.
+template <int DP>
+__device__ __forceinline__ void store_sums(float* row, int dim, int half, const Acc (&a)[DP / 32], float by) {
+#pragma unroll
+  for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int column = 32 * t + 8 * g + 4 * half;
+      if (row && column < dim)
+        *reinterpret_cast<float4*>(row + column) = make_float4(a[t][4 * g] * by, a[t][4 * g + 1] * by,
+                                                               a[t][4 * g + 2] * by, a[t][4 * g + 3] * by);
+    }
+}
+
 // Whether workgroups of eight waves share the keys of 128 queries: where there is no
 // more than one for a CU (2064 fp16 tokens of 6 heads: dq 33 us with four waves, 26 with
 // eight; one tile of keys, 23 tokens of 32 heads, has nothing to share: 5.5 and 6.4).
-inline bool two_sides(const AttnArgs& a, int64_t tiles) { return tiles * a.q_heads <= CUS; }
+inline bool two_sides(int64_t workgroups) { return workgroups <= CUS; }
 
 // Which head and tile a workgroup takes. Workgroups go to the eight XCDs in turn,
 // each with an L2 of its own: heads that read the same keys and values go to one

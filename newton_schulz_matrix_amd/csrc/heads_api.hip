@@ -272,29 +272,50 @@ ns_status check_attention(const ns_attention_args* p, AttnArgs* a, AttnViews* in
   a->clear_rest = p->clear_rest != 0;
   a->scale = p->scale;
   // a launch's workgroups, of which each has 128 rows of a head at most
-  if ((p->tokens / 128 + p->sequences + 1) * p->q_heads > (int64_t{1} << 31) / 256) return NS_ERR_INVALID_ARG;
+  if ((p->tokens / 128 + p->sequences + 1) * p->q_heads > (int64_t{1} << 31) / 512) return NS_ERR_INVALID_ARG;
   return NS_OK;
 }
-struct AttnGradPlan {
+struct AttnPlan {
   int parts;
+  size_t known, total;   // byte offset, bytes
+};
+AttnPlan attention_plan(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t dim) {
+  AttnPlan p;
+  p.parts = attention_parts(tokens, sequences, q_heads, tokens, true);
+  const size_t rows = p.parts > 1 ? static_cast<size_t>(p.parts) * tokens * q_heads : 0;
+  p.known = align_up(sizeof(float) * rows * dim);
+  p.total = p.known + align_up(sizeof(float2) * rows);
+  return p;
+}
+struct AttnGradPlan {
+  int q_parts, k_parts;
   size_t delta, peaks, sums, total;   // byte offsets, bytes
 };
 AttnGradPlan attention_grad_plan(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t k_heads, int64_t dim) {
   AttnGradPlan p;
   const size_t rows = align_up(sizeof(float) * static_cast<size_t>(tokens) * q_heads);
-  p.parts = attention_grad_parts(tokens, sequences, k_heads);
+  p.q_parts = attention_parts(tokens, sequences, q_heads, tokens, true);
+  p.k_parts = attention_parts(tokens, sequences, k_heads, tokens * (q_heads / k_heads), false);
   p.delta = rows;
   p.peaks = 2 * rows;
   p.sums = p.peaks + align_up(sizeof(uint32_t) * 2 * PEAKS);
-  p.total = p.sums;
-  if (p.parts > 1) p.total += align_up(sizeof(float) * 2 * p.parts * static_cast<size_t>(tokens) * k_heads * dim);
+  const int64_t most = std::max(p.q_parts > 1 ? p.q_parts * q_heads : 0, p.k_parts > 1 ? 2 * p.k_parts * k_heads : 0);
+  p.total = p.sums + align_up(sizeof(float) * static_cast<size_t>(most) * tokens * dim);
   return p;
 }
 
 }  // namespace
 }  // namespace nsmi
 
-NS_API ns_status ns_attention(const ns_attention_args* p, ns_heads out, float* lse, void* stream) {
+NS_API ns_status ns_attention_workspace_size(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t k_heads,
+                                             int64_t dim, size_t* bytes) {
+  if (!bytes || !attention_sizes_ok(tokens, sequences, q_heads, k_heads, dim)) return NS_ERR_INVALID_ARG;
+  *bytes = attention_plan(tokens, sequences, q_heads, dim).total;
+  return NS_OK;
+}
+
+NS_API ns_status ns_attention(const ns_attention_args* p, ns_heads out, float* lse, void* ws, size_t ws_bytes,
+                              void* stream) {
   AttnArgs a{};
   AttnViews in;
   ns_status s = check_attention(p, &a, &in);
@@ -302,15 +323,21 @@ NS_API ns_status ns_attention(const ns_attention_args* p, ns_heads out, float* l
   if (p->tokens == 0) return NS_OK;
   const View o = view(out, p->tokens, p->q_heads, p->dim, 2);
   if (!vectors_ok(o) || !writable(o) || !lse || !aligned(lse, 4)) return NS_ERR_INVALID_ARG;
+  const AttnPlan plan = attention_plan(p->tokens, p->sequences, p->q_heads, p->dim);
   const Span l = dense(lse, p->tokens * p->q_heads, 4), ends = dense(p->offsets, p->sequences + 1, 4);
-  if (meet(o, l) || meet(o, ends) || overlap(l, ends)) return NS_ERR_INVALID_ARG;
+  const Span work = dense(ws, plan.total, 1);
+  if (meet(o, l) || meet(o, ends) || overlap(l, ends) || meet(o, work) || overlap(l, work) || overlap(ends, work))
+    return NS_ERR_INVALID_ARG;
   for (const View* v : {&in.q, &in.k, &in.v})
-    if (meet(o, *v) || meet(*v, l)) return NS_ERR_INVALID_ARG;
+    if (meet(o, *v) || meet(*v, l) || meet(*v, work)) return NS_ERR_INVALID_ARG;
+  if (plan.total > 0 && !workspace_ok(ws, ws_bytes, plan.total)) return NS_ERR_WORKSPACE;
   s = device_status();
   if (s != NS_OK) return s;
+  unsigned char* w = static_cast<unsigned char*>(ws);
   a.out = place(out, o);
   a.lse = lse;
-  return from_hip(launch_attention(a, p->dtype, static_cast<hipStream_t>(stream)));
+  return from_hip(launch_attention(a, p->dtype, plan.parts, reinterpret_cast<float*>(w),
+                                   reinterpret_cast<float2*>(w + plan.known), static_cast<hipStream_t>(stream)));
 }
 
 NS_API ns_status ns_attention_grad_workspace_size(int64_t tokens, int64_t sequences, int64_t q_heads,
@@ -360,7 +387,8 @@ NS_API ns_status ns_attention_grad(const ns_attention_args* p, ns_heads dout, ns
   a.lse = const_cast<float*>(lse);
   a.lse2 = reinterpret_cast<float*>(w);
   a.delta = reinterpret_cast<float*>(w + plan.delta);
-  return from_hip(launch_attention_grad(a, p->dtype, plan.parts, reinterpret_cast<uint32_t*>(w + plan.peaks),
+  return from_hip(launch_attention_grad(a, p->dtype, plan.q_parts, plan.k_parts,
+                                        reinterpret_cast<uint32_t*>(w + plan.peaks),
                                         reinterpret_cast<float*>(w + plan.sums),
                                         static_cast<hipStream_t>(stream)));
 }

@@ -62,14 +62,21 @@ struct AttnArgs {
   bool clear_rest;
   float scale;
 };
-hipError_t launch_attention(const AttnArgs& a, int type, hipStream_t stream);
+// Into how many parts the keys of a tile of queries (or the queries of a tile of keys)
+// are cut, each a workgroup's: where the tiles alone would leave CUs without work, or
+// with one long sequence's ends. From two parts on their sums go through memory:
+//   forward  sums (parts, q_heads, tokens, dim) fp32 and known (parts, q_heads, tokens),
+//            each row's reference and sum of weights;
+//   dq       sums (parts, q_heads, tokens, dim);
+//   dk, dv   sums (parts, 2, k_heads, tokens, dim).
+// rows: those of all heads that one workgroup goes over at most; keys: whether they are keys.
+int attention_parts(int64_t tokens, int64_t sequences, int64_t heads, int64_t rows, bool keys);
+hipError_t launch_attention(const AttnArgs& a, int type, int parts, float* sums, float2* known, hipStream_t stream);
+
 // Greatest norms of a head's rows in dout and v, in so many places each, so that
 // waves do not queue for one (fp16 only).
 constexpr int PEAKS = 64;
-// Into how many parts a workgroup's queries are cut for dk and dv; from two on their
-// sums go through `sums`: (parts, 2, k_heads, tokens, dim) fp32.
-int attention_grad_parts(int64_t tokens, int64_t sequences, int64_t k_heads);
-hipError_t launch_attention_grad(const AttnArgs& a, int type, int parts, uint32_t* peaks, float* sums,
+hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k_parts, uint32_t* peaks, float* sums,
                                  hipStream_t stream);
 
 }  // namespace nsmi

@@ -10,6 +10,7 @@
 // query, a row's maximum and sum are its own registers and one exchange, and the
 // weights are the next product's operand as they stand. Keys and values come
 // into LDS directly, the next tile while this one is worked on.
+#include <algorithm>
 #include <type_traits>
 
 #include "attention_device.h"
@@ -47,7 +48,8 @@ __device__ __forceinline__ void clear_rows(const AttnArgs& a, int head, int firs
 // With two SIDES eight waves share 128 queries, each half of every tile's keys, and
 // bring their sums together at the end: for launches that leave most of a CU empty.
 template <class T, int DP, int SIDES>
-__global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs a, int tiles) {
+__global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs a, int tiles, int parts, float* sums,
+                                                                       float2* known_to) {
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32, SUB = KEYS / 32 / SIDES;   // 32 keys a time, SUB of them a tile
   constexpr int TILE = KEYS * Tile<DP>::ROW;
@@ -57,11 +59,14 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int side = wave / WAVES;
-  const Work w = work_of(blockIdx.x, a.q_heads, a.k_heads);
+  const unsigned blocks = gridDim.x / parts;
+  const int part = blockIdx.x / blocks;
+  const Work w = work_of(blockIdx.x - part * blocks, a.q_heads, a.k_heads);
   const Place at = place_of<QUERIES, false>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
   if (at.rest) {
-    if (a.clear_rest) clear_rows<T>(a, w.head, at.begin + at.row, min(at.begin + at.row + QUERIES, at.begin + at.length));
+    if (a.clear_rest && part == 0)
+      clear_rows<T>(a, w.head, at.begin + at.row, min(at.begin + at.row + QUERIES, at.begin + at.length));
     return;
   }
   const int kv_head = w.head / (a.q_heads / a.k_heads);
@@ -71,7 +76,8 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
   const Copier<DP, KEYS, WAVES * SIDES> k_copy(wave, lane, k_step, a.dim), v_copy(wave, lane, v_step, a.dim);
   const uint32_t lds = lds_address(smem);
   const int keys = min(at.length, at.row + QUERIES);   // that any query here sees
-  const int steps = (keys + KEYS - 1) / KEYS;
+  const Range range = range_of((keys + KEYS - 1) / KEYS, part, parts);
+  const int steps = range.last;
 
   auto fetch_tile = [&](int n) {
     const uint32_t to = lds + (n & 1) * 2 * TILE;
@@ -79,7 +85,7 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
     k_copy.copy(k + first * a.k.token, at.length - first, k_step, a.dim, to);
     v_copy.copy(v + first * a.v.token, at.length - first, v_step, a.dim, to + TILE);
   };
-  fetch_tile(0);
+  if (range.first < steps) fetch_tile(range.first);
 
   const int first_query = at.row + 32 * (wave % WAVES), query = first_query + (lane & 31);
   const bool there = query < at.length;
@@ -95,7 +101,7 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
   for (int t = 0; t < DT; ++t) o[t] = no_sum();
   float ref = -INFINITY, sum = 0.f;
 
-  for (int n = 0; n < steps; ++n) {
+  for (int n = range.first; n < steps; ++n) {
     copies_done();
     __syncthreads();   // tile n is there, and nobody reads the place of tile n + 1
     if (n + 1 < steps) fetch_tile(n + 1);
@@ -130,8 +136,8 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
     top = fmaxf(lower, upper) * c;
     if (__any(top > ref + LAG + LIFT<T>)) {
       const float to = fmaxf(ref, top - LIFT<T>);
-      // (a row of the second side may not have met a key yet: its sums stay 0)
-      const float by = SIDES == 2 && to == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref - to);
+      // (a row of another side or part may not have met a key yet: its sums stay 0)
+      const float by = to == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref - to);
       ref = to;
       sum *= by;
 #pragma unroll
@@ -139,7 +145,7 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[t][r] *= by;
     }
-    const float base = SIDES == 2 && ref == -INFINITY ? 0.f : ref;
+    const float base = ref == -INFINITY ? 0.f : ref;
 #pragma unroll
     for (int i = 0; i < SUB; ++i)
 #pragma unroll
@@ -171,14 +177,20 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
     __syncthreads();
     if (side == 1) return;
     const float2 other = known[wave * 64 + lane];
-    const float to = fmaxf(ref, other.x);   // (this side has met the first key)
-    const float mine = __builtin_amdgcn_exp2f(ref - to), theirs = __builtin_amdgcn_exp2f(other.x - to);
+    const float to = fmaxf(ref, other.x), base = to == -INFINITY ? 0.f : to;
+    const float mine = __builtin_amdgcn_exp2f(ref - base), theirs = __builtin_amdgcn_exp2f(other.x - base);
     ref = to;
     sum = sum * mine + other.y * theirs;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[t][r] = o[t][r] * mine + shared[64 * (16 * t + r)] * theirs;
+  }
+  if (parts > 1) {
+    const int64_t row = (static_cast<int64_t>(part) * a.q_heads + w.head) * a.tokens + at.begin + query;
+    store_sums<DP>(there ? sums + row * a.dim : nullptr, a.dim, half, o, 1.f);
+    if (there && half == 0) known_to[row] = make_float2(ref, sum);
+    return;
   }
   T* out = static_cast<T*>(a.out.p) + (at.begin + query) * a.out.token + w.head * a.out.head;
   store_columns<T, DP>(there ? out : nullptr, a.dim, half, o, 1.f / sum);
@@ -187,20 +199,64 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
         0.693147182f * (ref + __builtin_amdgcn_logf(sum));
 }
 
+// Brings the parts' sums of a row together, eight columns a lane.
+template <class T>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int parts, const float* sums,
+                                                             const float2* known) {
+  const int chunks = a.dim / 8, head = blockIdx.y;
+  const int i = blockIdx.x * 256 + threadIdx.x, token = i / chunks, column = i % chunks * 8;
+  if (token < offset_at(a.offsets, 0, a.tokens) || token >= offset_at(a.offsets, a.sequences, a.tokens)) return;
+  const int64_t row = static_cast<int64_t>(head) * a.tokens + token, one = static_cast<int64_t>(a.q_heads) * a.tokens;
+  float to = -INFINITY;
+  for (int k = 0; k < parts; ++k) to = fmaxf(to, known[row + k * one].x);
+  const float base = to == -INFINITY ? 0.f : to;
+  float v[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+  for (int k = 0; k < parts; ++k) {
+    const float2 of = known[row + k * one];
+    const float by = __builtin_amdgcn_exp2f(of.x - base);
+    float x[VEC];
+    load8(sums + (row + k * one) * a.dim + column, x);
+    sum = fmaf(of.y, by, sum);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = fmaf(x[e], by, v[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) v[e] /= sum;
+  store8(static_cast<T*>(a.out.p) + token * a.out.token + head * a.out.head + column, v);
+  if (column == 0) a.lse[row] = 0.693147182f * (to + __builtin_amdgcn_logf(sum));
+}
+
 }  // namespace
 
-hipError_t launch_attention(const AttnArgs& a, int type, hipStream_t stream) {
+// Up to eight parts, of 512 rows or more, where there are few workgroups: as many as
+// make three of them for a CU. Two of the keys where there are less than three for a CU
+// and the sequences are long: all are on the chip at once then, and those of the ends take twice the
+// average. Forward (and whole gradient) of bf16 heads of 128, us in one part and so: 16384
+// tokens of 1 head 313 and 130 (733, 367); 4096 of 4 heads 71 and 48 (194, 144); 1500 of 8
+// heads that read 2 24 and 22 (134, 52); 8192 of 8 that read 2 203 and 161; of 12 that read 4,
+// where it is one part, two take 241 instead of 228.
+int attention_parts(int64_t tokens, int64_t sequences, int64_t heads, int64_t rows, bool keys) {
+  const int64_t blocks = tiles_of(tokens, sequences, QUERIES) * heads;
+  const int64_t few = std::min<int64_t>({8, 3 * CUS / blocks, rows / 512});
+  if (few >= 2) return static_cast<int>(few);
+  return keys && blocks < 3 * CUS && tokens / std::max<int64_t>(1, sequences) >= 4096 ? 2 : 1;
+}
+
+hipError_t launch_attention(const AttnArgs& a, int type, int parts, float* sums, float2* known, hipStream_t stream) {
   const int64_t tiles = tiles_of(a.tokens, a.sequences, QUERIES);
   auto on = [&](auto t, auto dp, auto sides) {
     using T = decltype(t);
     constexpr int DP = dp(), SIDES = sides();
-    hipLaunchKernelGGL((attention_kernel<T, DP, SIDES>), dim3(static_cast<unsigned>(tiles * a.q_heads)),
-                       dim3(THREADS * SIDES), 0, stream, a, static_cast<int>(tiles));
+    hipLaunchKernelGGL((attention_kernel<T, DP, SIDES>), dim3(static_cast<unsigned>(tiles * a.q_heads * parts)),
+                       dim3(THREADS * SIDES), 0, stream, a, static_cast<int>(tiles), parts, sums, known);
+    if (parts > 1)
+      hipLaunchKernelGGL(attention_join_kernel<T>, dim3((a.tokens * (a.dim / 8) + 255) / 256, a.q_heads), dim3(256),
+                         0, stream, a, parts, sums, known);
     return hipGetLastError();
   };
   auto sided = [&](auto t, auto dp) {
-    return two_sides(a, tiles) ? on(t, dp, std::integral_constant<int, 2>{})
-                               : on(t, dp, std::integral_constant<int, 1>{});
+    return two_sides(tiles * a.q_heads * parts) ? on(t, dp, std::integral_constant<int, 2>{})
+                                                : on(t, dp, std::integral_constant<int, 1>{});
   };
   auto shaped = [&](auto t) {
     return a.dim <= 64 ? sided(t, std::integral_constant<int, 64>{}) : sided(t, std::integral_constant<int, 128>{});

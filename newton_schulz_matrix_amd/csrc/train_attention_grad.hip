@@ -99,7 +99,8 @@ __device__ __forceinline__ void clear_rows(const HeadsAt& to, int head, int dim,
 // tile's keys, and add up at the end: for launches that leave most of a CU empty. The
 // rows' delta and lse log2(e) are left for the kernel below.
 template <class T, int DP, int SIDES>
-__global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, const uint32_t* peaks, int tiles) {
+__global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, const uint32_t* peaks, int tiles,
+                                                               int parts, float* sums) {
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32;
   constexpr int TILE = STEP * Tile<DP>::ROW;
@@ -108,11 +109,13 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int side = wave / WAVES;
-  const Work w = work_of(blockIdx.x, a.q_heads, a.k_heads);
+  const unsigned blocks = gridDim.x / parts;
+  const int part = blockIdx.x / blocks;
+  const Work w = work_of(blockIdx.x - part * blocks, a.q_heads, a.k_heads);
   const Place at = place_of<ROWS, false>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
   if (at.rest) {
-    if (a.clear_rest)
+    if (a.clear_rest && part == 0)
       clear_rows<T>(a.dq, w.head, a.dim, at.begin + at.row, min(at.begin + at.row + ROWS, at.begin + at.length));
     return;
   }
@@ -123,14 +126,15 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
   const Copier<DP, STEP, WAVES * SIDES> k_copy(wave, lane, k_step, a.dim), v_copy(wave, lane, v_step, a.dim);
   const uint32_t lds = lds_address(smem);
   const int keys = min(at.length, at.row + ROWS);
-  const int steps = (keys + STEP - 1) / STEP;
+  const Range range = range_of((keys + STEP - 1) / STEP, part, parts);
+  const int steps = range.last;
   auto fetch_tile = [&](int n) {
     const uint32_t to = lds + (n & 1) * 2 * TILE;
     const int first = n * STEP;
     k_copy.copy(k + first * a.k.token, at.length - first, k_step, a.dim, to);
     v_copy.copy(v + first * a.v.token, at.length - first, v_step, a.dim, to + TILE);
   };
-  fetch_tile(0);
+  if (range.first < steps) fetch_tile(range.first);
 
   const int first_query = at.row + 32 * (wave % WAVES), query = first_query + (lane & 31);
   const bool there = query < at.length;
@@ -155,7 +159,7 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
   dot = lower + upper;
   const int64_t stat = static_cast<int64_t>(w.head) * a.tokens + token;
   float lse2 = there ? a.lse[stat] * LOG2E : 0.f;
-  if (there && half == 0 && side == 0) {
+  if (there && half == 0 && side == 0 && part == 0) {
     a.delta[stat] = -dot;
     a.lse2[stat] = lse2;
   }
@@ -170,7 +174,7 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
 #pragma unroll
   for (int t = 0; t < DT; ++t) dq[t] = no_sum();
 
-  for (int n = 0; n < steps; ++n) {
+  for (int n = range.first; n < steps; ++n) {
     copies_done();
     __syncthreads();
     if (n + 1 < steps) fetch_tile(n + 1);
@@ -222,6 +226,11 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
 #pragma unroll
       for (int r = 0; r < 16; ++r) dq[t][r] += shared[64 * (16 * t + r)];
   }
+  if (parts > 1) {
+    const int64_t row = (static_cast<int64_t>(part) * a.q_heads + w.head) * a.tokens + token;
+    store_sums<DP>(there ? sums + row * a.dim : nullptr, a.dim, half, dq, a.scale / scaled);
+    return;
+  }
   T* to = static_cast<T*>(a.dq.p) + token * a.dq.token + w.head * a.dq.head;
   store_columns<T, DP>(there ? to : nullptr, a.dim, half, dq, a.scale / scaled);
 }
@@ -271,8 +280,8 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
   const uint32_t lds = lds_address(smem);
   const int begin = at.row / KV_STEP;
   const int each = (at.length + KV_STEP - 1) / KV_STEP - begin;   // >= 1
-  const int64_t all = static_cast<int64_t>(each) * group;
-  const int first_step = static_cast<int>(all * part / parts), steps = static_cast<int>(all * (part + 1) / parts);
+  const Range range = range_of(static_cast<int64_t>(each) * group, part, parts);
+  const int steps = range.last;
   auto fetch_tile = [&](int n) {
     const uint32_t to = lds + (n & 1) * STAGE;
     const int h = n / each, first = (begin + n - h * each) * KV_STEP, rows = at.length - first;
@@ -284,7 +293,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
       copy4(descriptor(from, left > 0 ? 4 * left : 0), to + 2 * TILE + wave * 64 * 4, 4 * lane);
     }
   };
-  if (first_step < steps) fetch_tile(first_step);
+  if (range.first < steps) fetch_tile(range.first);
 
   const int first_key = at.row + 32 * (wave & 3), key = first_key + (lane & 31);
   const bool there = key < at.length;
@@ -303,7 +312,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
 #pragma unroll
   for (int t = 0; t < DT; ++t) dk[t] = dv[t] = no_sum();
 
-  for (int n = first_step; n < steps; ++n) {
+  for (int n = range.first; n < steps; ++n) {
     copies_done();
     __syncthreads();
     if (n + 1 < steps) fetch_tile(n + 1);
@@ -369,51 +378,36 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
     const HeadsAt& to = side ? a.dv : a.dk;
     T* row = static_cast<T*>(to.p) + token * to.token + w.head * to.head;
     store_columns<T, DP>(there ? row : nullptr, a.dim, half, dk, by);
-  } else if (there) {
-    float* row = sums + (((static_cast<int64_t>(part) * 2 + side) * a.k_heads + w.head) * a.tokens + token) * a.dim;
-#pragma unroll
-    for (int t = 0; t < DT; ++t)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int column = 32 * t + 8 * g + 4 * half;
-        if (column < a.dim)
-          *reinterpret_cast<float4*>(row + column) = make_float4(dk[t][4 * g] * by, dk[t][4 * g + 1] * by,
-                                                                 dk[t][4 * g + 2] * by, dk[t][4 * g + 3] * by);
-      }
+  } else {
+    const int64_t row = ((static_cast<int64_t>(part) * 2 + side) * a.k_heads + w.head) * a.tokens + token;
+    store_sums<DP>(there ? sums + row * a.dim : nullptr, a.dim, half, dk, by);
   }
 }
 
-// Adds up the parts' sums, eight columns a lane.
+// Adds up the parts' sums, of one tensor or of two one behind the other, eight columns a lane.
 template <class T>
-__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int parts, const float* sums) {
-  const int chunks = a.dim / 8, side = blockIdx.y / a.k_heads, head = blockIdx.y % a.k_heads;
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, HeadsAt first, HeadsAt second, int heads, int parts,
+                                                   const float* sums) {
+  const int chunks = a.dim / 8, head = blockIdx.y % heads;
   const int i = blockIdx.x * 256 + threadIdx.x, token = i / chunks, column = i % chunks * 8;
   if (token < offset_at(a.offsets, 0, a.tokens) || token >= offset_at(a.offsets, a.sequences, a.tokens)) return;
-  const int64_t one = static_cast<int64_t>(a.k_heads) * a.tokens * a.dim;
-  const float* from = sums + (static_cast<int64_t>(side) * a.k_heads + head) * a.tokens * a.dim +
-                      static_cast<int64_t>(token) * a.dim + column;
+  const int64_t one = static_cast<int64_t>(gridDim.y) * a.tokens * a.dim;
+  const float* from = sums + (static_cast<int64_t>(blockIdx.y) * a.tokens + token) * a.dim + column;
   float v[VEC];
   load8(from, v);
   for (int k = 1; k < parts; ++k) {
     float x[VEC];
-    load8(from + 2 * k * one, x);
+    load8(from + k * one, x);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] += x[e];
   }
-  const HeadsAt& to = side ? a.dv : a.dk;
+  const HeadsAt& to = static_cast<int>(blockIdx.y) < heads ? first : second;
   store8(static_cast<T*>(to.p) + token * to.token + head * to.head + column, v);
 }
 
 }  // namespace
 
-// Parts as many as fill the 256 CUs with the one workgroup that each holds, and at
-// most eight: 2064 tokens of 6 heads that read 2 take PARTS_US us so, ONE_US in one part.
-int attention_grad_parts(int64_t tokens, int64_t sequences, int64_t k_heads) {
-  const int64_t blocks = tiles_of(tokens, sequences, ROWS) * k_heads;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, CUS / blocks)));
-}
-
-hipError_t launch_attention_grad(const AttnArgs& a, int type, int parts, uint32_t* peaks, float* sums,
+hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k_parts, uint32_t* peaks, float* sums,
                                  hipStream_t stream) {
   const int64_t tiles = tiles_of(a.tokens, a.sequences, ROWS);
   auto on = [&](auto t, auto dp) {
@@ -424,18 +418,22 @@ hipError_t launch_attention_grad(const AttnArgs& a, int type, int parts, uint32_
       hipLaunchKernelGGL(norms_kernel<T>, dim3((a.tokens + 15) / 16, a.q_heads + a.k_heads), dim3(256), 0, stream,
                          a, peaks);
     }
+    auto join = [&](int tensors, const HeadsAt& first, const HeadsAt& second, int heads, int parts) {
+      if (parts > 1)
+        hipLaunchKernelGGL(join_kernel<T>, dim3((a.tokens * (a.dim / 8) + 255) / 256, tensors * heads), dim3(256), 0,
+                           stream, a, first, second, heads, parts, sums);
+    };
     auto queries = [&](auto sides) {
       constexpr int SIDES = sides();
-      hipLaunchKernelGGL((dq_kernel<T, DP, SIDES>), dim3(static_cast<unsigned>(tiles * a.q_heads)),
-                         dim3(THREADS * SIDES), 0, stream, a, peaks, static_cast<int>(tiles));
+      hipLaunchKernelGGL((dq_kernel<T, DP, SIDES>), dim3(static_cast<unsigned>(tiles * a.q_heads * q_parts)),
+                         dim3(THREADS * SIDES), 0, stream, a, peaks, static_cast<int>(tiles), q_parts, sums);
     };
-    if (two_sides(a, tiles)) queries(std::integral_constant<int, 2>{});
+    if (two_sides(tiles * a.q_heads * q_parts)) queries(std::integral_constant<int, 2>{});
     else queries(std::integral_constant<int, 1>{});
-    hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.k_heads * parts)),
-                       dim3(KV_THREADS), 0, stream, a, peaks, static_cast<int>(tiles), parts, sums);
-    if (parts > 1)
-      hipLaunchKernelGGL(join_kernel<T>, dim3((a.tokens * (a.dim / 8) + 255) / 256, 2 * a.k_heads), dim3(256), 0,
-                         stream, a, parts, sums);
+    join(1, a.dq, a.dq, a.q_heads, q_parts);
+    hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.k_heads * k_parts)),
+                       dim3(KV_THREADS), 0, stream, a, peaks, static_cast<int>(tiles), k_parts, sums);
+    join(2, a.dk, a.dv, a.k_heads, k_parts);
     return hipGetLastError();
   };
   auto shaped = [&](auto t) {

@@ -46,7 +46,8 @@ SIGNATURES = {
     "ns_qk_norm_rope_grad_workspace_size": [_i64, _i64, ctypes.POINTER(_size)],
     "ns_qk_norm_rope_grad": [ctypes.POINTER(_QkNormRopeArgs), _Heads, _Heads, _Heads, _Heads, _vp, _vp,
                              _int, _vp, _size, _vp],
-    "ns_attention": [ctypes.POINTER(_AttentionArgs), _Heads, _vp, _vp],
+    "ns_attention_workspace_size": [_i64] * 5 + [ctypes.POINTER(_size)],
+    "ns_attention": [ctypes.POINTER(_AttentionArgs), _Heads, _vp, _vp, _size, _vp],
     "ns_attention_grad_workspace_size": [_i64] * 5 + [ctypes.POINTER(_size)],
     "ns_attention_grad": [ctypes.POINTER(_AttentionArgs), _Heads, _Heads, _vp, _Heads, _Heads, _Heads,
                           _vp, _size, _vp],
@@ -195,7 +196,11 @@ def _attention_args(q, k, v, offsets, scale, clear_rest, dev):
                           1 if clear_rest else 0, dim ** -0.5 if scale is None else scale)
 
 
-def ns_attention(q, k, v, offsets, scale: Optional[float] = None, out=None):
+def ns_attention_workspace_size(tokens: int, sequences: int, q_heads: int, k_heads: int, dim: int) -> int:
+    return _sized("ns_attention_workspace_size", tokens, sequences, q_heads, k_heads, dim)
+
+
+def ns_attention(q, k, v, offsets, scale: Optional[float] = None, out=None, workspace=None):
     """Causal attention of packed sequences: q (tokens, q_heads, dim), k and v
     (tokens, k_heads, dim) in bf16 or fp16, q_heads a multiple of k_heads, dim a
     multiple of 8 up to 128; offsets (sequences + 1) int32 on the device, where
@@ -208,7 +213,13 @@ def ns_attention(q, k, v, offsets, scale: Optional[float] = None, out=None):
     args = _attention_args(q, k, v, offsets, scale, out is None, dev)
     out, to = _new_or_heads(out, "out", dev, q)
     lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    _check(library().ns_attention(args, to, lse.data_ptr(), _stream_of(dev)), "ns_attention")
+    nbytes = ns_attention_workspace_size(args.tokens, args.sequences, args.q_heads, args.k_heads, args.dim)
+    ws_ptr = None
+    if nbytes:
+        workspace = _given_or_new(workspace, nbytes, q.device)
+        ws_ptr = workspace.data_ptr()
+    _check(library().ns_attention(args, to, lse.data_ptr(), ws_ptr, workspace.numel() * workspace.element_size()
+                                  if nbytes else 0, _stream_of(dev)), "ns_attention")
     return out, lse
 
 
@@ -240,5 +251,5 @@ def ns_attention_grad(dout, q, k, v, out, lse, offsets, scale: Optional[float] =
 
 
 __all__ = ["NS_MAX_HEADS", "ns_qk_norm_rope", "ns_qk_norm_rope_grad",
-           "ns_qk_norm_rope_grad_workspace_size", "ns_attention", "ns_attention_grad",
-           "ns_attention_grad_workspace_size"]
+           "ns_qk_norm_rope_grad_workspace_size", "ns_attention", "ns_attention_workspace_size",
+           "ns_attention_grad", "ns_attention_grad_workspace_size"]

@@ -185,10 +185,13 @@ def check_grad(c, scale=None, seed=50, size=0.1, **given):
     for name, g, w, sl in zip(("dq", "dk", "dv"), got, want, slack):
         assert g.dtype == dtype
         tiny = 0.0
-        if dtype == HF and w.size:   # dS among the subnormals of the scaled range: 2^-25 where the largest possible is 2^13 or more
+        if w.size:
+            # fp16: dS among the subnormals of the scaled range, 2^-25 where the largest possible is 2^13 or more;
+            # a weight or a dS below fp32's normal range, 2^-126, is 0, each of them at most once
             norm = lambda x: np.sqrt((x[:n] ** 2).sum(-1).max(initial=0.0))   # noqa: E731
             other = {"dq": args[2], "dk": args[1], "dv": args[0]}[name]
-            tiny = longest * group * np.abs(other).max() * 2.0 ** -38 * max(2 * s * norm(args[0]) * norm(args[3]), 1.0)
+            least = 2.0 ** -38 if dtype == HF else 2.0 ** -125
+            tiny = longest * group * np.abs(other).max() * least * max(2 * s * norm(args[0]) * norm(args[3]), 1.0)
         assert_within(g[:n], w[:n], half_step(w, dtype)[:n] + sl[:n] + tiny, name)
     return dout, out, lse, got
 
@@ -243,6 +246,27 @@ def test_gradient_of_other_layouts_and_alone():
         alone = nsmi.ns_attention_grad(*(x[a:b].contiguous() for x in (dout, c["q"], c["k"], c["v"], out)),
                                        lse[:, a:b].contiguous(), ends_of([b - a]))
         assert all(torch.equal(x, y[a:b]) for x, y in zip(alone, want))
+
+
+@pytest.mark.parametrize("case", [([1100, 37, 200], 4, 2, 128), ([1300], 2, 1, 64), ([3, 0, 1500, 90], 6, 2, 80),
+                                  ([700] * 3, 3, 3, 120)], ids=lambda c: str(c)[:40])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_few_long_sequences(case, dtype):
+    """Where few workgroups are cut into parts, whose sums are brought together."""
+    require_gpu()
+    lengths, *shape = case
+    c = make(sum(lengths), lengths, *shape, dtype, rest=5)
+    assert nsmi.ns_attention_workspace_size(len(c["q"]), len(lengths), *shape) > 0
+    check(c)
+    check_grad(c)
+    peaked = make(1, lengths, *shape, dtype, peak=25.0)
+    check(peaked)
+    check_grad(peaked)
+    ws = torch.full((nsmi.ns_attention_workspace_size(len(c["q"]), len(lengths), *shape),), 255, dtype=torch.uint8,
+                    device="cuda")
+    out, lse = nsmi.ns_attention(c["q"], c["k"], c["v"], c["offsets"], workspace=ws)
+    again, lse2 = nsmi.ns_attention(c["q"], c["k"], c["v"], c["offsets"])
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
 def test_offsets_that_do_not_rise():
