@@ -2,9 +2,10 @@
 
 A small model (embedding, norm, two matrices, norm with the residual, head)
 learns to prefer one of two continuations. Its two matrices take the Muon
-step; the embedding table, the head and the norm gains take AdamW. The
-products of the layers are torch's; the backward pass is written out, call by
-call. Run it on an MI355X:
+step; the embedding table, the head and the norm gains take AdamW. A second
+model has an attention layer in front, over the batch as one packed row of
+sequences. The products of the layers are torch's; the backward pass is written
+out, call by call. Run it on an MI355X:
 
     python examples/preference_training.py
 """
@@ -77,6 +78,75 @@ class Model:
                            masters=[self.masters[k] for k in rest])
 
 
+class AttentionModel(Model):
+    """The model with a causal attention layer between its embedding and the rest:
+    heads of queries and keys are normed and turned by their positions."""
+
+    heads, kv_heads, head_dim = 4, 2, 64
+
+    def __init__(self, vocab=1000, dim=256, hidden=768, seed=0):
+        super().__init__(vocab, dim, hidden, seed)
+        g = torch.Generator().manual_seed(seed + 1)
+        rows, wide = (self.heads + 2 * self.kv_heads) * self.head_dim, self.heads * self.head_dim
+        for name, (r, c) in {"qkv": (rows, dim), "out": (dim, wide)}.items():
+            self.mats[name] = (torch.randn(r, c, generator=g) / c ** 0.5).to(BF).cuda()
+            self.momenta[name] = torch.zeros_like(self.mats[name])
+        for name, n in (("gain0", dim), ("q_gain", self.head_dim), ("k_gain", self.head_dim)):
+            self.masters[name] = torch.ones(n, device="cuda")
+            self.w[name] = self.masters[name].to(BF)
+            self.moments[name] = (torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda"))
+        half = torch.arange(self.head_dim // 2, dtype=torch.float64)
+        self.inv_freq = (10000.0 ** (-2 * half / self.head_dim)).float().cuda()
+
+    def parts(self, qkv):
+        """Queries, keys and values of one buffer (tokens, heads of all, head_dim)."""
+        return qkv.split((self.heads, self.kv_heads, self.kv_heads), 1)
+
+    def forward(self, ids):
+        w, m, s = self.w, self.mats, {"ids": ids}
+        n, length = ids.shape
+        s["ends"] = torch.arange(0, n * length + 1, length, dtype=torch.int32, device="cuda")
+        s["at"] = torch.arange(length, device="cuda").repeat(n)
+        x = nsmi.ns_embedding(w["table"], ids.reshape(-1), scale=self.scale)
+        s["y0"], s["h0"], s["r0"] = nsmi.ns_rms_norm(x, w["gain0"])
+        s["qkv"] = (s["y0"] @ m["qkv"].t()).view(n * length, -1, self.head_dim)
+        q, k, v = self.parts(s["qkv"])
+        s["q"], s["k"] = nsmi.ns_qk_norm_rope(q, k, w["q_gain"], w["k_gain"], s["at"], self.inv_freq)
+        s["o"], s["lse"] = nsmi.ns_attention(s["q"], s["k"], v, s["ends"])
+        s["y1"], s["h1"], s["r1"] = nsmi.ns_rms_norm(s["o"].flatten(1) @ m["out"].t(), w["gain1"],
+                                                     residual=s["h0"])
+        s["a"] = s["y1"] @ m["up"].t()
+        s["b"] = s["a"].relu()
+        s["y2"], s["h2"], s["r2"] = nsmi.ns_rms_norm(s["b"] @ m["down"].t(), w["gain2"], residual=s["h1"])
+        return (s["y2"] @ w["head"].t()).view(n, length, -1), s
+
+    def backward(self, s, dlogits):
+        w, m, g = self.w, self.mats, {}
+        dlogits = dlogits.flatten(0, 1)
+        g["head"] = dlogits.t() @ s["y2"]
+        dc, g["gain2"] = nsmi.ns_rms_norm_grad(dlogits @ w["head"], s["h2"], w["gain2"], s["r2"],
+                                               dweight_dtype=F32)
+        g["down"] = dc.t() @ s["b"]
+        da = (dc @ m["down"]) * (s["a"] > 0)
+        g["up"] = da.t() @ s["y1"]
+        dx, g["gain1"] = nsmi.ns_rms_norm_grad(da @ m["up"], s["h1"], w["gain1"], s["r1"], dh=dc,
+                                               dweight_dtype=F32)
+        g["out"] = dx.t() @ s["o"].flatten(1)
+        q, k, v = self.parts(s["qkv"])
+        dqkv = torch.empty_like(s["qkv"])
+        dq, dk, dv = self.parts(dqkv)
+        nsmi.ns_attention_grad((dx @ m["out"]).view_as(s["o"]), s["q"], s["k"], v, s["o"], s["lse"], s["ends"],
+                               dq=dq, dk=dk, dv=dv)
+        _, _, g["q_gain"], g["k_gain"] = nsmi.ns_qk_norm_rope_grad(
+            dq, dk, q, k, w["q_gain"], w["k_gain"], s["at"], self.inv_freq, dq=dq, dk=dk, dweight_dtype=F32)
+        dqkv = dqkv.flatten(1)
+        g["qkv"] = dqkv.t() @ s["y0"]
+        dx, g["gain0"] = nsmi.ns_rms_norm_grad(dqkv @ m["qkv"], s["h0"], w["gain0"], s["r0"], dh=dx,
+                                               dweight_dtype=F32)
+        g["table"] = nsmi.ns_embedding_grad(dx, s["ids"].reshape(-1), w["table"].shape[0], scale=self.scale)
+        return g
+
+
 def batch(pairs=8, length=64, vocab=1000, seed=1):
     """Ids (2 pairs, length) and the labels of the continuations: both of a
     pair share a prompt; its positions do not count."""
@@ -89,13 +159,12 @@ def batch(pairs=8, length=64, vocab=1000, seed=1):
     return ids.cuda(), labels.cuda()
 
 
-def train(steps=20, beta=0.1):
-    model = Model()
+def train(steps=20, beta=0.1, model=None):
+    model = model or Model()
     ids, labels = batch()
     pairs = ids.shape[0] // 2
-    zero = torch.zeros(2 * pairs, device="cuda")
-    # the reference is the model as it starts
-    reference = nsmi.ns_preference_loss(model.forward(ids)[0], labels, zero)[2].clone()
+    # the reference is the model as it starts: log probabilities of the labels that count
+    reference = nsmi.ns_token_logps(model.forward(ids)[0], labels)[0].sum(-1)
     weights = torch.full((pairs,), 1.0 / pairs, device="cuda")
     history = []
     for _ in range(steps):
@@ -109,5 +178,5 @@ def train(steps=20, beta=0.1):
 
 
 if __name__ == "__main__":
-    for i, loss in enumerate(train()):
-        print(f"step {i:2d}  loss {loss:.4f}")
+    for i, (loss, other) in enumerate(zip(train(), train(model=AttentionModel()))):
+        print(f"step {i:2d}  loss {loss:.4f}  with attention {other:.4f}")
