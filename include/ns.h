@@ -452,8 +452,10 @@ ns_status ns_preference_loss_grad(const ns_preference_args* args, const float* m
  * +inf among a row's logits makes its lse, entropy and log probabilities NaN (a
  * NaN is never among the likeliest; where fewer than top entries are left, the
  * ids behind them are -1), and a row of nothing but -inf has lse -inf and NaN
- * for the others.
- *   logits  (rows, vocab), ld >= vocab;   tokens  (rows);
+ * for the others; the gradient of either is NaN.
+ *   logits  (rows, vocab), ld >= vocab; or, with length != 0, sequences of
+ *           length rows (which divides rows), ld_sequence apart (0: length * ld), at
+ *           least (length - 1) * ld + vocab;   tokens  (rows);
  *   logps, lse, entropy  (rows) fp32;
  *   top_logps  (rows, top) fp32, top_ids  (rows, top) of the tokens' type;
  *              both NULL if top == 0.
@@ -462,7 +464,8 @@ ns_status ns_preference_loss_grad(const ns_preference_args* args, const float* m
  * element of
  *   dlogits[r][v] = dlogps[r] ([v == token] - p) - dentropy[r] p (log p + entropy[r])
  * (0 in rows that do not count) of logits' type, ld_dlogits >= vocab; dlogits
- * may be the logits' own buffer with ld_dlogits == ld. entropy may be NULL
+ * may be the logits' own buffer with ld_dlogits == ld, and then has the logits'
+ * sequences. entropy may be NULL
  * without dentropy. (In fp32, lse's own rounding puts up to |lse| 2^-24, relative,
  * on a row.)
  * 0 <= rows <= NS_MAX_ROWS (0 is a no-op), 1 <= vocab <= NS_MAX_ROWS,
@@ -475,6 +478,7 @@ typedef struct {
   int64_t rows, vocab, ld, top;
   ns_dtype dtype;
   ns_id_type token_type;
+  int64_t length, ld_sequence;
 } ns_token_logps_args;
 ns_status ns_token_logps_workspace_size(int64_t rows, int64_t vocab, int64_t top, size_t* bytes);
 ns_status ns_token_logps(const ns_token_logps_args* args, float* logps, float* lse, float* entropy,

@@ -377,9 +377,23 @@ LogpsPlan logps_plan(int64_t rows, int64_t vocab, int64_t top) {
   p.total = std::max(ALIGN, align_up(p.entries + sizeof(uint64_t) * parts * top));
   return p;
 }
+int64_t logps_length(const ns_token_logps_args& p) { return p.length != 0 ? p.length : std::max<int64_t>(p.rows, 1); }
+int64_t logps_sequence(const ns_token_logps_args& p) {
+  return p.ld_sequence != 0 ? p.ld_sequence : logps_length(p) * p.ld;
+}
+// The logits' buffer.
+Span logps_span(const ns_token_logps_args& p) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p.logits);
+  const int64_t length = logps_length(p);
+  const int64_t last = (p.rows / length - 1) * logps_sequence(p) + (length - 1) * p.ld + p.vocab;
+  return {a, a + static_cast<uintptr_t>(last) * type_bytes(p.dtype)};
+}
 ns_status check_logps(const ns_token_logps_args* p) {
   if (!p || !type_ok(p->dtype) || !ids_ok(p->token_type)) return NS_ERR_INVALID_ARG;
   if (!logps_sizes_ok(p->rows, p->vocab, p->top) || !ld_ok(p->ld, p->vocab)) return NS_ERR_INVALID_ARG;
+  if (p->length < 0 || p->length > NS_MAX_ROWS || p->rows % logps_length(*p) != 0) return NS_ERR_INVALID_ARG;
+  const int64_t length = logps_length(*p), seqs = p->rows / length, seq = logps_sequence(*p);
+  if (seqs > 1 && (seq < (length - 1) * p->ld + p->vocab || seq > MAX_SEQUENCE / seqs)) return NS_ERR_INVALID_ARG;
   if (p->rows > 0 && (!p->logits || !p->tokens || !aligned(p->logits, type_bytes(p->dtype)) ||
                       !aligned(p->tokens, id_bytes(p->token_type))))
     return NS_ERR_INVALID_ARG;
@@ -390,7 +404,9 @@ LogpsArgs logps_args(const ns_token_logps_args& p) {
   a.logits = p.logits;
   a.tokens = p.tokens;
   a.ld = p.ld;
+  a.ld_seq = logps_sequence(p);
   a.rows = static_cast<int>(p.rows);
+  a.length = static_cast<int>(logps_length(p));
   a.vocab = static_cast<int>(p.vocab);
   a.top = static_cast<int>(p.top);
   a.tokens64 = p.token_type == NS_IDS_I64;
@@ -424,8 +440,7 @@ NS_API ns_status ns_token_logps(const ns_token_logps_args* p, float* logps, floa
                          span(top_logps, rows, p->top, p->top, 4),
                          span(top_ids, rows, p->top, p->top, ie),
                          span(ws, 1, plan.total, plan.total, 1)};
-  const Span reads[] = {span(p->logits, rows, p->vocab, p->ld, type_bytes(p->dtype)),
-                        span(p->tokens, 1, rows, rows, ie)};
+  const Span reads[] = {logps_span(*p), span(p->tokens, 1, rows, rows, ie)};
   if (clash(writes, reads)) return NS_ERR_INVALID_ARG;
   if (!workspace_ok(ws, ws_bytes, plan.total)) return NS_ERR_WORKSPACE;
   s = device_status();
@@ -452,15 +467,17 @@ NS_API ns_status ns_token_logps_grad(const ns_token_logps_args* p, const float* 
   const int64_t rows = p->rows;
   const bool in_place = dlogits == p->logits && ld_dlogits == p->ld;
   const Span none = {0, 0};
-  const Span writes[] = {span(dlogits, rows, p->vocab, ld_dlogits, es)};
-  const Span reads[] = {in_place ? none : span(p->logits, rows, p->vocab, p->ld, es),
+  const Span writes[] = {in_place ? logps_span(*p) : span(dlogits, rows, p->vocab, ld_dlogits, es)};
+  const Span reads[] = {in_place ? none : logps_span(*p),
                         span(p->tokens, 1, rows, rows, id_bytes(p->token_type)), floats(lse, rows),
                         floats(entropy, rows), floats(dlogps, rows), floats(dentropy, rows)};
   if (clash(writes, reads)) return NS_ERR_INVALID_ARG;
   s = device_status();
   if (s != NS_OK) return s;
   return from_hip(launch_token_logps_grad(logps_args(*p), p->dtype, lse, entropy, dlogps, dentropy,
-                                          dlogits, ld_dlogits, static_cast<hipStream_t>(stream)));
+                                          dlogits, ld_dlogits,
+                                          in_place ? logps_sequence(*p) : logps_length(*p) * ld_dlogits,
+                                          static_cast<hipStream_t>(stream)));
 }
 
 // -------------------------------------------------------------------- AdamW

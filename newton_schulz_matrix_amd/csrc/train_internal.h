@@ -136,8 +136,8 @@ constexpr int LOGPS_JOIN = 1024;      // entries of a row's pieces, all together
 struct LogpsArgs {
   const void* logits;
   const void* tokens;
-  int64_t ld;
-  int rows, vocab, top;
+  int64_t ld, ld_seq;  // from one row of a sequence, one sequence to the next
+  int rows, length, vocab, top;
   bool tokens64;
 };
 struct LogpsOut {
@@ -157,7 +157,7 @@ hipError_t launch_token_logps(const LogpsArgs& a, int type, const PrefSplit& sp,
                               uint64_t* entries, const LogpsOut& o, hipStream_t stream);
 hipError_t launch_token_logps_grad(const LogpsArgs& a, int type, const float* lse, const float* entropy,
                                    const float* dlogps, const float* dentropy, void* dlogits,
-                                   int64_t ld_dlogits, hipStream_t stream);
+                                   int64_t ld_dlogits, int64_t ld_dseq, hipStream_t stream);
 
 // -------------------------------------------------------------- AdamW
 

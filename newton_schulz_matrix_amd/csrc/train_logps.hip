@@ -28,6 +28,11 @@ __device__ __forceinline__ int64_t token_at(const LogpsArgs& a, int64_t row) {
   return a.tokens64 ? static_cast<const int64_t*>(a.tokens)[row]
                     : static_cast<const int32_t*>(a.tokens)[row];
 }
+// Offset of a row in sequences `apart`, rows `ld` apart.
+__device__ __forceinline__ int64_t offset_of(const LogpsArgs& a, int row, int64_t apart, int64_t ld) {
+  const int seq = row / a.length;
+  return seq * apart + (row - seq * a.length) * ld;
+}
 __device__ __forceinline__ bool counted(const LogpsArgs& a, int64_t token) {
   return token >= 0 && token < a.vocab;
 }
@@ -277,7 +282,7 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
     return;
   }
   const int begin = blockIdx.y * sp.piece, end = min(a.vocab, begin + sp.piece);
-  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+  const T* z = static_cast<const T*>(a.logits) + offset_of(a, row, a.ld_seq, a.ld);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int col0 = threadIdx.x * VEC;
   const float token_logit = static_cast<float>(z[token]);
@@ -400,7 +405,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void join_kernel(LogpsArgs a, int pie
     t += f == 0.0 ? 0.0 * p[k].s : f * (p[k].t + d * p[k].s);
   }
   if (threadIdx.x == 0)
-    write_row(o, row, static_cast<float>(static_cast<const T*>(a.logits)[row * a.ld + token]), m, s, t);
+    write_row(o, row, static_cast<float>(static_cast<const T*>(a.logits)[offset_of(a, row, a.ld_seq, a.ld) + token]), m, s, t);
   __syncthreads();
   const double log_s = log(s);
   for (int i = threadIdx.x; i < all; i += JOIN_THREADS) {
@@ -419,13 +424,13 @@ template <class T, int THREADS, bool ENTROPY>
 __global__ __launch_bounds__(THREADS) void logps_grad_kernel(LogpsArgs a, const float* lse,
                                                              const float* entropy, const float* dlogps,
                                                              const float* dentropy, T* dlogits,
-                                                             int64_t ld_dlogits, int steps) {
+                                                             int64_t ld_dlogits, int64_t ld_dseq, int steps) {
   const int64_t all = static_cast<int64_t>(a.rows) * steps;
   for (int64_t block = blockIdx.x; block < all; block += gridDim.x) {
     const int row = static_cast<int>(block / steps);
     const int base = static_cast<int>(block - static_cast<int64_t>(row) * steps) * step_of(THREADS);
     const int64_t token = token_at(a, row);
-    T* d = dlogits + row * ld_dlogits;
+    T* d = dlogits + offset_of(a, row, ld_dseq, ld_dlogits);
     const int col0 = static_cast<int>(threadIdx.x) * VEC;
     if (!counted(a, token)) {
       const float zero[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -437,7 +442,7 @@ __global__ __launch_bounds__(THREADS) void logps_grad_kernel(LogpsArgs a, const 
       }
       continue;
     }
-    const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+    const T* z = static_cast<const T*>(a.logits) + offset_of(a, row, a.ld_seq, a.ld);
     Raw<T> raw[UNROLL];
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j) {
@@ -503,7 +508,7 @@ hipError_t launch_token_logps(const LogpsArgs& a, int type, const PrefSplit& sp,
 
 hipError_t launch_token_logps_grad(const LogpsArgs& a, int type, const float* lse, const float* entropy,
                                    const float* dlogps, const float* dentropy, void* dlogits,
-                                   int64_t ld_dlogits, hipStream_t stream) {
+                                   int64_t ld_dlogits, int64_t ld_dseq, hipStream_t stream) {
   const int threads = a.vocab <= SHORT_VOCAB ? 64 : 256, step = step_of(threads);
   const int steps = (a.vocab + step - 1) / step;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(a.rows) * steps, 1 << 23)));
@@ -513,7 +518,7 @@ hipError_t launch_token_logps_grad(const LogpsArgs& a, int type, const float* ls
       constexpr int N = n();
       constexpr bool E = with();
       hipLaunchKernelGGL((logps_grad_kernel<T, N, E>), grid, dim3(N), 0, stream, a, lse, entropy, dlogps,
-                         dentropy, static_cast<T*>(dlogits), ld_dlogits, steps);
+                         dentropy, static_cast<T*>(dlogits), ld_dlogits, ld_dseq, steps);
       return hipGetLastError();
     };
     auto shaped = [&](auto n) { return dentropy ? go(n, std::true_type{}) : go(n, std::false_type{}); };

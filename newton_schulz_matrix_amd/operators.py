@@ -68,7 +68,8 @@ class _PreferenceArgs(ctypes.Structure):
 
 class _TokenLogpsArgs(ctypes.Structure):
     _fields_ = [("logits", _vp), ("tokens", _vp), ("rows", _i64), ("vocab", _i64), ("ld", _i64),
-                ("top", _i64), ("dtype", _int), ("token_type", _int)]
+                ("top", _i64), ("dtype", _int), ("token_type", _int), ("length", _i64),
+                ("ld_sequence", _i64)]
 
 
 class _AdamwTensor(ctypes.Structure):
@@ -447,11 +448,21 @@ def ns_preference_loss_grad(logits, labels, margins, lse, dlosses, beta: float =
 # --------------------------------------------------- token log probabilities
 
 def _token_logps_args(logits, tokens, top, dev):
-    if logits.dim() < 1:
+    shape = logits.shape
+    if len(shape) < 1:
         raise ValueError("logits must have at least one dimension")
-    rows, vocab, ld = _rows_of(logits, "logits", dev)
-    return _TokenLogpsArgs(logits.data_ptr(), _dense(tokens, logits.shape[:-1], "tokens", dev), rows,
-                           vocab, ld, top, _code(logits), _ids_type(tokens, "tokens"))
+    length = sequence = 0
+    if len(shape) < 3 or logits.is_contiguous() or 0 in shape:
+        rows, vocab, ld = _rows_of(logits, "logits", dev)
+    else:   # positions and what comes before them may each lie further apart
+        length, vocab, ld = _rows_of(logits[(0,) * (len(shape) - 2)], "logits", dev)
+        seqs, span, sequence = _rows_of(logits[..., 0, :1], "logits", dev)
+        rows = seqs * length
+        if seqs > 1 and sequence < (length - 1) * ld + vocab:
+            raise ValueError(f"logits: overlapping sequences (shape {tuple(shape)}, strides "
+                             f"{tuple(logits.stride())})")
+    return _TokenLogpsArgs(logits.data_ptr(), _dense(tokens, shape[:-1], "tokens", dev), rows, vocab, ld, top,
+                           _code(logits), _ids_type(tokens, "tokens"), length, sequence)
 
 
 def ns_token_logps_workspace_size(rows: int, vocab: int, top: int = 0) -> int:
@@ -460,7 +471,8 @@ def ns_token_logps_workspace_size(rows: int, vocab: int, top: int = 0) -> int:
 
 def ns_token_logps(logits, tokens, top: int = 0, workspace=None):
     """Log probabilities of the tokens (int32 or int64, of any shape) from
-    logits of shape tokens.shape + (vocab,). Returns (logps, lse, entropy,
+    logits of shape tokens.shape + (vocab,) (a slice such as logits[:, :-1] is
+    fine). Returns (logps, lse, entropy,
     top_logps, top_ids): the first three are fp32 and of the tokens' shape, the
     log sum of exponentials and entropy of each row are also what the gradient
     needs; top_logps (fp32) and top_ids (of the tokens' type) are each row's
@@ -498,6 +510,10 @@ def ns_token_logps_grad(logits, tokens, lse, entropy, dlogps, dentropy=None, out
     if out is None:
         out = torch.empty(shape, dtype=logits.dtype, device=logits.device)
         ld_out = args.vocab
+    elif out.data_ptr() == logits.data_ptr() and args.rows > 0:
+        if out.dtype != logits.dtype or out.shape != shape or out.stride() != logits.stride():
+            raise ValueError("out begins where the logits do, but is another view of that memory")
+        ld_out = args.ld
     else:
         ld_out = _like_rows(out, shape, "out", dev, logits.dtype)
 

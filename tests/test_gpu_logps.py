@@ -144,6 +144,30 @@ def test_layouts():
     assert one[0].shape == ()
 
 
+def test_slices_of_sequences():
+    """All positions but the last of each sequence, as a shifted loss takes them; the gradient in place and not."""
+    require_gpu()
+    for vocab in (203, 5000, 40000):
+        whole, _ = make(12, 3 * 5, vocab, BF)
+        whole = whole.view(3, 5, vocab).clone()
+        tokens = torch.randint(-30, vocab, (3, 4)).cuda()
+        part = whole[:, :-1]
+        want = nsmi.ns_token_logps(part.contiguous(), tokens, top=3)
+        got = nsmi.ns_token_logps(part, tokens, top=3)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        dl, dh = normal(1, (3, 4)), normal(2, (3, 4))
+        args = (tokens, got[1], got[2], dl)
+        d = nsmi.ns_token_logps_grad(part.contiguous(), *args, dentropy=dh)
+        assert torch.equal(nsmi.ns_token_logps_grad(part, *args, dentropy=dh), d)
+        last = whole[:, -1].clone()
+        back = nsmi.ns_token_logps_grad(part, *args, dentropy=dh, out=part)
+        assert back.data_ptr() == whole.data_ptr() and torch.equal(part, d) and torch.equal(whole[:, -1], last)
+        with pytest.raises(ValueError):
+            nsmi.ns_token_logps_grad(part, *args, out=whole[:, :-1].as_strided((3, 4, vocab), (4 * vocab, vocab, 1)))
+        with pytest.raises(ValueError):
+            nsmi.ns_token_logps(whole.transpose(0, 1)[:4], tokens.t())
+
+
 def test_a_row_does_not_depend_on_the_others():
     """Few rows are cut into pieces, many are not: the same likeliest entries, sums within their errors."""
     require_gpu()

@@ -30,7 +30,8 @@ def no_gpu():
 
 def logps(call="forward", ws=P[8], n=64 * MB, lse=P[3], entropy=P[4], logps=P[5], top_logps=P[6], top_ids=P[7],
           dlogps=P[5], dentropy=P[6], out=P[9], ld_out=100, **kw):
-    a = dict(logits=P[0], tokens=P[1], rows=8, vocab=100, ld=100, top=3, dtype=BF16, token_type=1)
+    a = dict(logits=P[0], tokens=P[1], rows=8, vocab=100, ld=100, top=3, dtype=BF16, token_type=1, length=0,
+             ld_sequence=0)
     a.update(kw)
     args = ctypes.byref(ops._TokenLogpsArgs(*a.values()))
     if call == "forward":
@@ -47,6 +48,11 @@ def test_token_logps_refusals():
         assert logps(call, rows=0, logits=None, tokens=None) == nsmi.NS_OK
         assert logps(call, token_type=0, tokens=P[1] + 4) == UNSUPPORTED
         assert logps(call, logits=P[0] + 2, ld=101) == UNSUPPORTED     # element alignment is enough
+        assert logps(call, length=4, ld_sequence=500) == UNSUPPORTED and logps(call, length=4) == UNSUPPORTED
+        assert logps(call, length=8, ld_sequence=1) == UNSUPPORTED     # one sequence: its distance does not count
+        for kw in (dict(length=3), dict(length=-4), dict(length=16), dict(length=4, ld_sequence=399),
+                   dict(length=4, ld_sequence=-400), dict(length=4, ld_sequence=1 << 60), dict(length=1 << 40)):
+            assert logps(call, **kw) == BAD, (call, kw)
         for kw in (dict(logits=None), dict(tokens=None), dict(lse=None), dict(rows=-1), dict(vocab=0),
                    dict(rows=nsmi.NS_MAX_ROWS + 1), dict(vocab=nsmi.NS_MAX_ROWS + 1, ld=1 << 30), dict(ld=99),
                    dict(ld=1 << 40), dict(dtype=E4M3), dict(dtype=-1), dict(token_type=2), dict(top=-1),
@@ -61,6 +67,9 @@ def test_token_logps_refusals():
     for kw in (dict(ws=None), dict(n=8), dict(ws=P[8] + 64)):
         assert logps(**kw) == WS, kw
     assert logps("grad", out=P[0]) == UNSUPPORTED                      # in place
+    assert logps("grad", out=P[0], length=2, ld_sequence=8 * MB) == UNSUPPORTED
+    assert logps("grad", out=P[0] + 32 * MB, length=2, ld_sequence=8 * MB) == BAD   # in the last sequence
+    assert logps("grad", out=P[0] + 56 * MB, length=2, ld_sequence=8 * MB) == UNSUPPORTED
     assert logps("grad", dentropy=None, entropy=None) == UNSUPPORTED
     assert logps("grad", dlogps=None) == UNSUPPORTED
     for kw in (dict(out=None), dict(entropy=None), dict(ld_out=99), dict(out=P[0], ld_out=104), dict(out=P[0] + 2),
