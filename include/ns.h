@@ -470,7 +470,8 @@ ns_status ns_preference_loss_grad(const ns_preference_args* args, const float* m
  * on a row.)
  * 0 <= rows <= NS_MAX_ROWS (0 is a no-op), 1 <= vocab <= NS_MAX_ROWS,
  * 0 <= top <= min(vocab, NS_MAX_TOP); the gradient ignores top. Workspace of the
- * forward call: ns_token_logps_workspace_size bytes, 256-byte aligned. */
+ * forward call: ns_token_logps_workspace_size bytes, 256-byte aligned (NULL where
+ * that is 0: rows that are not cut into pieces). */
 #define NS_MAX_TOP 64
 typedef struct {
   const void* logits;

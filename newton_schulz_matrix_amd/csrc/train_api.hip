@@ -374,7 +374,7 @@ LogpsPlan logps_plan(int64_t rows, int64_t vocab, int64_t top) {
   p.split = logps_split(rows, vocab, static_cast<int>(top));
   const size_t parts = p.split.pieces > 1 ? static_cast<size_t>(rows) * p.split.pieces : 0;
   p.entries = align_up(sizeof(LogpsPart) * parts);
-  p.total = std::max(ALIGN, align_up(p.entries + sizeof(uint64_t) * parts * top));
+  p.total = align_up(p.entries + sizeof(uint64_t) * parts * top);
   return p;
 }
 int64_t logps_length(const ns_token_logps_args& p) { return p.length != 0 ? p.length : std::max<int64_t>(p.rows, 1); }
@@ -442,7 +442,7 @@ NS_API ns_status ns_token_logps(const ns_token_logps_args* p, float* logps, floa
                          span(ws, 1, plan.total, plan.total, 1)};
   const Span reads[] = {logps_span(*p), span(p->tokens, 1, rows, rows, ie)};
   if (clash(writes, reads)) return NS_ERR_INVALID_ARG;
-  if (!workspace_ok(ws, ws_bytes, plan.total)) return NS_ERR_WORKSPACE;
+  if (plan.total > 0 && !workspace_ok(ws, ws_bytes, plan.total)) return NS_ERR_WORKSPACE;
   s = device_status();
   if (s != NS_OK) return s;
   unsigned char* w = static_cast<unsigned char*>(ws);

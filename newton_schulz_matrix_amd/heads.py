@@ -217,9 +217,8 @@ def ns_attention(q, k, v, offsets, scale: Optional[float] = None, out=None, work
     ws_ptr = None
     if nbytes:
         workspace = _given_or_new(workspace, nbytes, q.device)
-        ws_ptr = workspace.data_ptr()
-    _check(library().ns_attention(args, to, lse.data_ptr(), ws_ptr, workspace.numel() * workspace.element_size()
-                                  if nbytes else 0, _stream_of(dev)), "ns_attention")
+        ws_ptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(library().ns_attention(args, to, lse.data_ptr(), ws_ptr, nbytes, _stream_of(dev)), "ns_attention")
     return out, lse
 
 

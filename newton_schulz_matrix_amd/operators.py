@@ -483,18 +483,20 @@ def ns_token_logps(logits, tokens, top: int = 0, workspace=None):
     tokens = tokens if tokens.is_contiguous() else tokens.contiguous()
     args = _token_logps_args(logits, tokens, top, dev)
     rows, shape, device = args.rows, logits.shape[:-1], logits.device
-    out = torch.empty(rows * 3, dtype=torch.float32, device=device)
-    top_logps = top_ids = logps_ptr = ids_ptr = None
+    out = torch.empty((3,) + shape, dtype=torch.float32, device=device)
+    top_logps = top_ids = logps_ptr = ids_ptr = ws_ptr = None
     if top > 0:
         top_logps = torch.empty(shape + (top,), dtype=torch.float32, device=device)
         top_ids = torch.empty(shape + (top,), dtype=tokens.dtype, device=device)
         logps_ptr, ids_ptr = top_logps.data_ptr(), top_ids.data_ptr()
-    workspace = _given_or_new(workspace, ns_token_logps_workspace_size(rows, args.vocab, top), device)
+    nbytes = ns_token_logps_workspace_size(rows, args.vocab, top)
+    if nbytes:
+        workspace = _given_or_new(workspace, nbytes, device)
+        ws_ptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     at = out.data_ptr()
-    _check(library().ns_token_logps(args, at, at + 4 * rows, at + 8 * rows, logps_ptr, ids_ptr,
-                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+    _check(library().ns_token_logps(args, at, at + 4 * rows, at + 8 * rows, logps_ptr, ids_ptr, ws_ptr, nbytes,
                                     _stream_of(dev)), "ns_token_logps")
-    logps, lse, entropy = out.view((3,) + shape).unbind(0)
+    logps, lse, entropy = out.unbind(0)
     return logps, lse, entropy, top_logps, top_ids
 
 
@@ -508,7 +510,7 @@ def ns_token_logps_grad(logits, tokens, lse, entropy, dlogps, dentropy=None, out
     args = _token_logps_args(logits, tokens, 0, dev)
     shape = logits.shape
     if out is None:
-        out = torch.empty(shape, dtype=logits.dtype, device=logits.device)
+        out = torch.empty_like(logits, memory_format=torch.contiguous_format)
         ld_out = args.vocab
     elif out.data_ptr() == logits.data_ptr() and args.rows > 0:
         if out.dtype != logits.dtype or out.shape != shape or out.stride() != logits.stride():

@@ -62,10 +62,13 @@ def test_token_logps_refusals():
     assert logps(top=0, top_logps=None, top_ids=None) == UNSUPPORTED
     for kw in (dict(logps=None), dict(entropy=None), dict(top_logps=None), dict(top_ids=None), dict(top=0),
                dict(top_ids=P[7] + 4), dict(top_logps=P[6] + 2), dict(logps=P[3]), dict(lse=P[0]),
-               dict(top_ids=P[1]), dict(top_logps=P[7] + 8), dict(ws=P[0]), dict(ws=P[6])):
+               dict(top_ids=P[1]), dict(top_logps=P[7] + 8)):
         assert logps(**kw) == BAD, kw
+    cut = dict(rows=2, vocab=40000, ld=40000)      # few long rows are cut into pieces; others need no workspace
     for kw in (dict(ws=None), dict(n=8), dict(ws=P[8] + 64)):
-        assert logps(**kw) == WS, kw
+        assert logps(**cut, **kw) == WS and logps(**kw) == UNSUPPORTED, kw
+    for kw in (dict(ws=P[0]), dict(ws=P[6]), dict(ws=P[7])):
+        assert logps(**cut, **kw) == BAD, kw
     assert logps("grad", out=P[0]) == UNSUPPORTED                      # in place
     assert logps("grad", out=P[0], length=2, ld_sequence=8 * MB) == UNSUPPORTED
     assert logps("grad", out=P[0] + 32 * MB, length=2, ld_sequence=8 * MB) == BAD   # in the last sequence
@@ -205,7 +208,7 @@ def test_attention_refusals():
 
 def test_workspace_sizes():
     size = nsmi.ns_token_logps_workspace_size
-    assert size(0, 1) > 0 and size(1 << 23, 1 << 23, 64) > 0
+    assert size(0, 1) == 0 and size(4, 1 << 17, 64) > 0 and size(1 << 23, 1 << 23, 64) == 0
     for bad in ((-1, 8, 0), (8, 0, 0), (8, 8, 9), (8, 100, 65), (8, 8, -1), ((1 << 23) + 1, 8, 0)):
         with pytest.raises(nsmi.NsError):
             size(*bad)
