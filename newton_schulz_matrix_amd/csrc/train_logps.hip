@@ -20,6 +20,14 @@ namespace {
 
 constexpr int UNROLL = 8;                           // vectors of a thread in flight
 constexpr int SHORT_VOCAB = 64 * VEC * UNROLL / 2;  // rows up to this long are one wave's
+// Many rows are one wave's up to longer ones: nothing is brought together between waves
+// then (bf16, us with one wave and with four: 16000 rows of 4096, top 5, 42 and 134; 8192 of
+// 50021 187 and 217; 16384 of 70000 422 and 485, 4100 of 100000 183 and 170; without top 8000 of
+// 12000 42 and 51, 12000 of 21273 114 and 109). Few rows are done sooner by four.
+constexpr int MANY_ROWS = 4096, MANY_VOCAB = 1 << 14, MANY_VOCAB_TOP = 1 << 16;
+constexpr int one_wave_vocab(int rows, int top) {
+  return rows < MANY_ROWS ? SHORT_VOCAB : top > 0 ? MANY_VOCAB_TOP : MANY_VOCAB;
+}
 constexpr int step_of(int threads) { return threads * VEC * UNROLL; }
 constexpr float FAR = 150.f;                        // exp(-FAR) is 0 in fp32
 constexpr float LOG2E = 1.442695041f;
@@ -139,7 +147,6 @@ struct Candidates {
   uint64_t list[CANDIDATES];
   uint64_t ordered[LOGPS_MAX_TOP];
   uint32_t best[64];   // greatest order of each lane
-  int count;
 };
 
 // Zeros behind a list's entries, up to where it is read.
@@ -200,7 +207,6 @@ __device__ __forceinline__ void compact(Candidates& c, Choice& w, int top) {
   wave_settled();
   const int left = min(w.count, top);
   if (lane < left) c.list[lane] = c.ordered[lane];
-  if (lane == 0) c.count = left;
   wave_settled();
   // indices rise from one vector of a wave to the next: an entry equal to the last of these is behind it
   if (w.count >= top) w.raise(static_cast<uint32_t>(c.list[top - 1] >> 32) + 1);
@@ -223,18 +229,19 @@ __device__ __forceinline__ void offer(const Raw<T> (&raw)[UNROLL], const float (
     const unsigned long long hits = __ballot(high[j] >= w.from_value);
     if (hits == 0) continue;
     if (w.count + VEC * __popcll(hits) > CANDIDATES) compact(c, w, top);
-    if (high[j] >= w.from_value) {
-      float v[VEC];
-      widen(raw[j], v);
+    float v[VEC];
+    widen(raw[j], v);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int index = at + j * THREADS * VEC + e;
-        if (v[e] >= w.from_value && index < end)
-          c.list[atomicAdd(&c.count, 1)] = entry_of(order_of(v[e]), index);
-      }
+    for (int e = 0; e < VEC; ++e) {
+      const int index = at + j * THREADS * VEC + e;
+      const bool in = v[e] >= w.from_value && index < end;
+      const unsigned long long all = __ballot(in);
+      if (all == 0) continue;
+      const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(all >> 32),
+                                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), 0));
+      if (in) c.list[w.count + before] = entry_of(order_of(v[e]), index);
+      w.count += __popcll(all);
     }
-    wave_settled();
-    w.count = __builtin_amdgcn_readfirstlane(*const_cast<volatile int*>(&c.count));
   }
 }
 
@@ -273,8 +280,8 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
   __shared__ float red_m[WAVES];
   __shared__ double red_s[WAVES], red_t[WAVES];
   __shared__ Candidates found[TOP ? WAVES : 1];
-  __shared__ uint64_t last[TOP ? LAST + AT_ONCE : 1];
-  __shared__ int lasts;
+  __shared__ uint64_t last[TOP && WAVES > 1 ? LAST + AT_ONCE : 1];
+  __shared__ int counts[WAVES], lasts;
   const int64_t row = blockIdx.x;
   const int64_t token = token_at(a, row);
   if (!counted(a, token)) {
@@ -287,11 +294,7 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
   const int col0 = threadIdx.x * VEC;
   const float token_logit = static_cast<float>(z[token]);
   Candidates& mine = found[TOP ? wave : 0];
-  if constexpr (TOP) {
-    if (lane == 0) mine.count = 0;
-    if (threadIdx.x == 0) lasts = 0;
-    wave_settled();
-  }
+  if (TOP && threadIdx.x == 0) lasts = 0;
   Sums r = {-INFINITY, 0.f, 0.f};
   Choice w = {LOWEST, -INFINITY, -INFINITY, 0};
   for (int base = begin; base < end; base += STEP) {
@@ -315,7 +318,11 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
     }
     if constexpr (TOP) offer<THREADS>(raw, high, base + col0, end, a.top, mine, w);
   }
-  if constexpr (TOP) mine.best[lane] = order_of(w.best);
+  if constexpr (TOP) {
+    mine.best[lane] = order_of(w.best);
+    if (lane == 0) counts[wave] = w.count;
+    pad(mine.list, w.count, CANDIDATES);
+  }
   const float wave_top = wave_max(r.m);
   if (lane == 0) red_m[wave] = wave_top;
   __syncthreads();
@@ -328,7 +335,7 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
     red_s[wave] = ws;
     red_t[wave] = wt;
   }
-  if constexpr (TOP) {   // those of all waves that reach what `top` lanes have reached
+  if constexpr (TOP && WAVES > 1) {   // those of all waves that reach what `top` lanes have reached
     uint32_t best[WAVES];
 #pragma unroll
     for (int u = 0; u < WAVES; ++u) best[u] = found[u].best[lane];
@@ -340,7 +347,6 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
         if (at < LAST) last[at] = e;
       }
     }
-    pad(mine.list, w.count, CANDIDATES);
   }
   __syncthreads();
   double s = 0.0, t = 0.0;
@@ -356,21 +362,21 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
     else parts[part] = {m, s, t};
   }
   if constexpr (TOP) {
-    const int left = lasts;
     const double log_s = whole ? log(s) : 0.0;
     auto put = [&](int rank, uint64_t e) {
       if (rank >= a.top) return;
       if (whole) write_entry(a, o, row, rank, e, m, log_s);
       else entries[part * a.top + rank] = e;
     };
-    if (left <= LAST) {
+    const int left = WAVES > 1 ? lasts : w.count;
+    if (WAVES > 1 && left <= LAST) {
       if (wave == 0) pad(last, left, LAST + AT_ONCE);
       __syncthreads();
       for (int i = threadIdx.x; i < left; i += THREADS) put(rank_in(last, left, last[i]), last[i]);
-    } else {   // many equal entries: ranks among all candidates
+    } else {   // one wave, or many equal entries: ranks among all candidates
       for (int i = lane; i < w.count; i += 64) {
         int rank = 0;
-        for (int u = 0; u < WAVES; ++u) rank += rank_in(found[u].list, found[u].count, mine.list[i]);
+        for (int u = 0; u < WAVES; ++u) rank += rank_in(found[u].list, counts[u], mine.list[i]);
         put(rank, mine.list[i]);
       }
     }
@@ -419,52 +425,82 @@ __global__ __launch_bounds__(JOIN_THREADS) void join_kernel(LogpsArgs a, int pie
 
 // --------------------------------------------------------------- gradient
 
-// Workgroups take a step each, in the order of the addresses.
+// How many elements behind a boundary of N of them an address lies.
+template <int N, class T>
+__device__ __forceinline__ int behind_boundary(const T* p) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) / sizeof(T) % N);
+}
+
+// Workgroups take a step each, in the order of the addresses. A lane's vectors are 16
+// bytes each, so that a wave stores whole lines in fp32 too (5913 rows of 21273: 183 us,
+// 293 with 32 bytes a lane). In long 16-bit rows they begin where the row's gradient is
+// 16-byte aligned (2048 rows of 128001: 196 us, 208 with vectors from the row's first element;
+// 5913 of 21273 112 and 127; 16000 of 2001 32.1 and 31.8). The sums above are laid from a row's
+// first element all the same: their order, and with it their last bits, would
+// depend on where the logits lie.
+constexpr int GRAD_UNROLL = 8, LONG = 4096;
+template <class T>
+constexpr int GRAD_VEC = 16 / sizeof(T);
+template <class T>
+constexpr int grad_step(int threads) {
+  return threads * GRAD_VEC<T> * GRAD_UNROLL;
+}
+template <class T>
+union Sixteen {
+  Quad q;
+  T e[GRAD_VEC<T>];
+};
 template <class T, int THREADS, bool ENTROPY>
 __global__ __launch_bounds__(THREADS) void logps_grad_kernel(LogpsArgs a, const float* lse,
                                                              const float* entropy, const float* dlogps,
                                                              const float* dentropy, T* dlogits,
                                                              int64_t ld_dlogits, int64_t ld_dseq, int steps) {
+  constexpr int N = GRAD_VEC<T>, U = GRAD_UNROLL;
   const int64_t all = static_cast<int64_t>(a.rows) * steps;
   for (int64_t block = blockIdx.x; block < all; block += gridDim.x) {
     const int row = static_cast<int>(block / steps);
-    const int base = static_cast<int>(block - static_cast<int64_t>(row) * steps) * step_of(THREADS);
-    const int64_t token = token_at(a, row);
     T* d = dlogits + offset_of(a, row, ld_dseq, ld_dlogits);
-    const int col0 = static_cast<int>(threadIdx.x) * VEC;
-    if (!counted(a, token)) {
-      const float zero[VEC] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < UNROLL; ++j) {
-        const int at = base + j * THREADS * VEC;
-        if (at >= a.vocab) break;
-        store8_upto<Use::ONCE>(d + at + col0, a.vocab - at - col0, zero);
-      }
-      continue;
-    }
     const T* z = static_cast<const T*>(a.logits) + offset_of(a, row, a.ld_seq, a.ld);
-    Raw<T> raw[UNROLL];
+    const int base = static_cast<int>(block - static_cast<int64_t>(row) * steps) * grad_step<T>(THREADS) -
+                     (sizeof(T) == 2 && a.vocab >= LONG ? behind_boundary<N>(d) : 0);
+    const int first = base + static_cast<int>(threadIdx.x) * N;
+    const int64_t token = token_at(a, row);
+    const bool counts = counted(a, token);
+    Sixteen<T> x[U];
+    if (counts) {
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
-      const int at = base + j * THREADS * VEC;
-      if (at < a.vocab && a.vocab >= VEC) raw[j] = fetch_at<Use::ONCE>(z, a.vocab, at + col0);
-    }
-    const float l = lse[row], g = dlogps ? dlogps[row] : 0.f;
-    const float h = ENTROPY ? dentropy[row] : 0.f, H = ENTROPY ? entropy[row] : 0.f;
+      for (int j = 0; j < U; ++j) {
+        if (base + j * THREADS * N >= a.vocab) break;
+        const int at = first + j * THREADS * N;
+        if (at >= 0 && at + N <= a.vocab) {
+          x[j].q = __builtin_nontemporal_load(reinterpret_cast<const Quad*>(z + at));
+        } else {
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
-      const int at = base + j * THREADS * VEC;
-      if (at >= a.vocab) break;
-      float v[VEC];
-      widen_at(raw[j], z, a.vocab, at + col0, v);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float x = v[e] - l, p = exp_of(x);
-        // an entry at -inf has no share, and p log p goes to 0 there
-        const float slope = ENTROPY ? fmaf(h, fmaxf(x, -FAR) + H, g) : g;
-        v[e] = fmaf(-p, slope, at + col0 + e == token ? g : 0.f);
+          for (int e = 0; e < N; ++e) x[j].e[e] = at + e >= 0 && at + e < a.vocab ? z[at + e] : static_cast<T>(0.f);
+        }
       }
-      store8_upto<Use::ONCE>(d + at + col0, a.vocab - at - col0, v);
+    }
+    const float l = counts ? lse[row] : 0.f, g = counts && dlogps ? dlogps[row] : 0.f;
+    const float h = ENTROPY && counts ? dentropy[row] : 0.f, H = ENTROPY && counts ? entropy[row] : 0.f;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (base + j * THREADS * N >= a.vocab) break;
+      const int at = first + j * THREADS * N;
+      Sixteen<T> y;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float v = static_cast<float>(x[j].e[e]) - l, p = exp_of(v);
+        // an entry at -inf has no share, and p log p goes to 0 there
+        const float slope = ENTROPY ? fmaf(h, fmaxf(v, -FAR) + H, g) : g;
+        y.e[e] = static_cast<T>(counts ? fmaf(-p, slope, at + e == token ? g : 0.f) : 0.f);
+      }
+      if (at >= 0 && at + N <= a.vocab) {
+        __builtin_nontemporal_store(y.q, reinterpret_cast<Quad*>(d + at));
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (at + e >= 0 && at + e < a.vocab) d[at + e] = y.e[e];
+      }
     }
   }
 }
@@ -497,7 +533,7 @@ hipError_t launch_token_logps(const LogpsArgs& a, int type, const PrefSplit& sp,
     auto shaped = [&](auto threads) {
       return a.top > 0 ? go(threads, std::true_type{}) : go(threads, std::false_type{});
     };
-    hipError_t e = a.vocab <= SHORT_VOCAB ? shaped(std::integral_constant<int, 64>{})
+    hipError_t e = a.vocab <= one_wave_vocab(a.rows, a.top) ? shaped(std::integral_constant<int, 64>{})
                                           : shaped(std::integral_constant<int, 256>{});
     if (e != hipSuccess || sp.pieces == 1) return e;
     hipLaunchKernelGGL(join_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(JOIN_THREADS), 0, stream,
@@ -509,11 +545,12 @@ hipError_t launch_token_logps(const LogpsArgs& a, int type, const PrefSplit& sp,
 hipError_t launch_token_logps_grad(const LogpsArgs& a, int type, const float* lse, const float* entropy,
                                    const float* dlogps, const float* dentropy, void* dlogits,
                                    int64_t ld_dlogits, int64_t ld_dseq, hipStream_t stream) {
-  const int threads = a.vocab <= SHORT_VOCAB ? 64 : 256, step = step_of(threads);
-  const int steps = (a.vocab + step - 1) / step;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(a.rows) * steps, 1 << 23)));
+  const int threads = a.vocab <= SHORT_VOCAB ? 64 : 256;
   return by_type(type, [&](auto t) {
     using T = decltype(t);
+    // (a row may begin up to a vector behind the first one's)
+    const int step = grad_step<T>(threads), steps = (a.vocab + GRAD_VEC<T> - 1 + step - 1) / step;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(a.rows) * steps, 1 << 23)));
     auto go = [&](auto n, auto with) {
       constexpr int N = n();
       constexpr bool E = with();
