@@ -104,7 +104,13 @@ __device__ __forceinline__ void copy4(I32x4 from, uint32_t lds, uint32_t at) {
                :: "s"(lds), "v"(at), "s"(from) : "memory", "m0");
 }
 #pragma clang diagnostic pop
-__device__ __forceinline__ void copies_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// The builtin tells the compiler that its own loads are there too: at the first use of
+// one within a loop it would otherwise wait in every round, and so for the copies of
+// the next tile.
+__device__ __forceinline__ void copies_done() {
+  __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt 0, the others as they are
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
@@ -131,10 +137,13 @@ struct Copier {
   // `rows`: how many of the tile's rows there are.
   __device__ __forceinline__ void copy(const void* first, int rows, uint32_t step, int dim,
                                        uint32_t tile) const {
-    const int n = min(rows, ROWS);
-    const I32x4 from = descriptor(first, n > 0 ? (n - 1) * step + 2 * dim : 0);
+    // (a descriptor for each instruction: a distance added to `at` would stay in a register)
 #pragma unroll
-    for (int i = 0; i < N; ++i) copy16(from, tile + lds + i * WAVES * 1024, at + i * EACH * step);
+    for (int i = 0; i < N; ++i) {
+      const int n = min(rows - i * EACH, EACH);
+      const char* const from = static_cast<const char*>(first) + static_cast<int64_t>(i * EACH) * step;
+      copy16(descriptor(from, n > 0 ? (n - 1) * step + 2 * dim : 0), tile + lds + i * WAVES * 1024, at);
+    }
   }
 };
 
@@ -157,6 +166,11 @@ struct RowReader {
       return __builtin_bit_cast(typename Eight<T>::type, v);
     }
   };
+  template <class T>
+  __device__ __forceinline__ typename Eight<T>::type read(uint32_t tile, int k, int further) const {
+    const U32x4 v = *(const __attribute__((address_space(3))) U32x4*)(((tile + at) ^ (k << 5)) + further);
+    return __builtin_bit_cast(typename Eight<T>::type, v);
+  }
   __device__ __forceinline__ In in(uint32_t tile) const {
     In r;
 #pragma unroll
@@ -190,6 +204,13 @@ struct ColumnReader {
       return __builtin_bit_cast(typename Eight<T>::type, v);
     }
   };
+  template <class T>
+  __device__ __forceinline__ typename Eight<T>::type read(uint32_t tile, int t, int further) const {
+    In r;
+    r.at[t][0] = (tile + at) ^ (t << 6);
+    r.at[t][1] = r.at[t][0] ^ (Tile<DP>::swizzle(8) << 4);
+    return r.template read<T>(t, further);
+  }
   __device__ __forceinline__ In in(uint32_t tile) const {
     In r;
 #pragma unroll

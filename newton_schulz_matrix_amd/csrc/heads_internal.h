@@ -55,7 +55,7 @@ struct AttnArgs {
   HeadsAt q, k, v, out;
   HeadsAt dout, dq, dk, dv;    // gradient only
   float* lse;                  // (q_heads, tokens)
-  float* lse2;                 // lse log2(e), gradient only
+  float* lse2;                 // -lse log2(e) (fp16: + 14), gradient only
   float* delta;                // -delta, (q_heads, tokens), gradient only
   const int* offsets;          // (sequences + 1)
   int tokens, sequences, q_heads, k_heads, dim;

@@ -161,7 +161,7 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
   float lse2 = there ? a.lse[stat] * LOG2E : 0.f;
   if (there && half == 0 && side == 0 && part == 0) {
     a.delta[stat] = -dot;
-    a.lse2[stat] = lse2;
+    a.lse2[stat] = (NARROW<T> ? LIFT : 0.f) - lse2;
   }
   const float scaled = NARROW<T> ? ds_scale(peaks) : 1.f;
   const float to_ds = NARROW<T> ? scaled * (1.f / 16384.f) : 1.f;
@@ -243,7 +243,25 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
 constexpr int KV_WAVES = 8, KV_THREADS = 64 * KV_WAVES;
 constexpr int KV_STEP = 128;          // queries of a tile
 
-//
+// The products come in the order they are written in, each operand read two products
+// ahead, the weights' exponentials between those of dout v^T: left to itself the
+// compiler puts every read right before its product, and the kernel takes 14% more
+// cycles (5% more time: the clock falls with the work in each of them). The registers
+// for it (two waves of 256 a SIMD) come from the second half of a wave's keys, which
+// lies in LDS for heads above 64, and from addresses that are made anew for each read.
+constexpr int AHEAD = 2;
+constexpr int KEY_CHUNKS = 4;         // of 16 columns in registers
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+__device__ __forceinline__ uint32_t anew(uint32_t x) {
+  asm volatile("" : "+s"(x));
+  return x;
+}
+__device__ __forceinline__ float4 read4(const __attribute__((address_space(3))) float4* p) {
+  typedef float F4 __attribute__((ext_vector_type(4)));
+  const F4 v = *(const __attribute__((address_space(3))) F4*)p;
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+
 // Where the keys alone would not fill the chip, `parts` workgroups share the
 // queries of the same keys, and leave their sums in fp32 for a kernel that adds
 // them up in order.
@@ -253,8 +271,11 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32;
   constexpr int TILE = KV_STEP * Tile<DP>::ROW, STATS = 2 * KV_STEP * 4, STAGE = 2 * TILE + STATS;
+  static_assert(KC == KEY_CHUNKS || 16 * (KC - KEY_CHUNKS) == 64, "the keys' second half is a tile of 64 columns");
   static_assert(2 * STAGE >= 2 * ROWS * DP * 4, "both sums of half the waves fit in the tiles");
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];   // queries, dout, lse, delta, twice
+  constexpr int KR = std::min(KC, KEY_CHUNKS), KL = KC - KR;   // key chunks in registers, in LDS
+  // queries, dout, lse, delta, twice, and the keys' second half
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE + (KL ? ROWS * Tile<64>::ROW : 0)];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int side = wave / 4;           // of a tile's queries
@@ -293,19 +314,29 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
       copy4(descriptor(from, left > 0 ? 4 * left : 0), to + 2 * TILE + wave * 64 * 4, 4 * lane);
     }
   };
-  if (range.first < steps) fetch_tile(range.first);
+  if (range.first < steps) {
+    fetch_tile(range.first);
+    if constexpr (KL > 0) {
+      const uint32_t k_step = static_cast<uint32_t>(a.k.token * 2);
+      const int further = 16 * KR, left = a.dim - further;
+      const Copier<64, ROWS, KV_WAVES> k_copy(wave, lane, k_step, left);
+      k_copy.copy(static_cast<const T*>(a.k.p) + (at.begin + at.row) * a.k.token + w.head * a.k.head + further,
+                  at.length - at.row, k_step, left, lds + 2 * STAGE);
+    }
+  }
 
   const int first_key = at.row + 32 * (wave & 3), key = first_key + (lane & 31);
   const bool there = key < at.length;
   const int64_t token = at.begin + key;
-  V8 k[KC], v[KC];
-  load_operands<T, DP>(there ? static_cast<const T*>(a.k.p) + token * a.k.token + w.head * a.k.head : nullptr,
-                       a.dim, half, k);
+  V8 k[KR], v[KC];
+  load_operands<T, 16 * KR>(there ? static_cast<const T*>(a.k.p) + token * a.k.token + w.head * a.k.head : nullptr,
+                            min(a.dim, 16 * KR), half, k);
   load_operands<T, DP>(there ? static_cast<const T*>(a.v.p) + token * a.v.token + w.head * a.v.head : nullptr,
                        a.dim, half, v);
   const float scaled = NARROW<T> ? ds_scale(peaks) : 1.f;
   const float to_ds = NARROW<T> ? scaled * (1.f / 16384.f) : 1.f;
   const RowReader<DP> rows(lane);
+  const auto k_rows = RowReader<64>(lane).in(lds + 2 * STAGE + 32 * (wave & 3) * Tile<64>::ROW);
   const ColumnReader<DP> columns(lane);
   const float c = a.scale * LOG2E;
   Acc dk[DT], dv[DT];
@@ -322,23 +353,60 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
     for (int i = 0; i < KV_STEP / 64; ++i) {
       const int row0 = 64 * i + 32 * side, query0 = first_query + row0;
       if (query0 + 31 < first_key) continue;
-      const auto qr = rows.in(qt + row0 * Tile<DP>::ROW);   // dout's tile lies TILE behind
-      const auto qc = columns.in(qt + row0 * Tile<DP>::ROW);
-      const __attribute__((address_space(3))) float* const stats =
-          (const __attribute__((address_space(3))) float*)(qt + 2 * TILE) + row0 + 4 * half;
+      const __attribute__((address_space(3))) float4* const stats =
+          (const __attribute__((address_space(3))) float4*)(qt + 2 * TILE) + row0 / 4 + half;
+      // The products in their order, and what each reads: S, dout v^T (whose tile lies TILE behind), then
+      // dv and dk by halves of the queries and 32 columns.
+      constexpr int ROW_READS = 2 * KC, READS = ROW_READS + 4 * DT;
+      V8 read[READS], kl[KL > 0 ? KL : 1];
+      auto fetch = [&](int n) {
+        if (n >= READS) return;
+        if (n < ROW_READS) {
+          read[n] = rows.template read<T>(anew(qt + row0 * Tile<DP>::ROW), n % KC, n / KC * TILE);
+          if (n >= KR && n < KC) kl[n - KR] = k_rows.template read<T>(n - KR, 0);
+        } else {
+          const int m = n - ROW_READS;
+          read[n] = columns.template read<T>(anew(qt + row0 * Tile<DP>::ROW), m % DT,
+                                             (m < 2 * DT ? TILE : 0) + 16 * (m / DT % 2) * Tile<DP>::ROW);
+        }
+      };
+#pragma unroll
+      for (int n = 0; n < AHEAD; ++n) fetch(n);
       Acc s = no_sum(), dp;
+      float4 lse;
+      auto weights = [&](int g) {
+        s[4 * g] = __builtin_amdgcn_exp2f(fmaf(s[4 * g], c, lse.x));
+        s[4 * g + 1] = __builtin_amdgcn_exp2f(fmaf(s[4 * g + 1], c, lse.y));
+        s[4 * g + 2] = __builtin_amdgcn_exp2f(fmaf(s[4 * g + 2], c, lse.z));
+        s[4 * g + 3] = __builtin_amdgcn_exp2f(fmaf(s[4 * g + 3], c, lse.w));
+      };
 #pragma unroll
-      for (int r = 0; r < 16; ++r) dp[r] = stats[KV_STEP + 8 * (r / 4) + r % 4];   // -delta
-#pragma unroll
-      for (int j = 0; j < KC; ++j) s = product(qr.template read<T>(j, 0), k[j], s);
-#pragma unroll
-      for (int j = 0; j < KC; ++j) dp = product(qr.template read<T>(j, TILE), v[j], dp);
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float lse2 = stats[8 * (r / 4) + r % 4];
-        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, (NARROW<T> ? LIFT : 0.f) - lse2));
-        dp[r] = NARROW<T> ? s[r] * (dp[r] * to_ds) : s[r] * dp[r];
+      for (int g = 0; g < 4; ++g) {
+        const float4 x = read4(stats + KV_STEP / 4 + 2 * g);   // -delta
+        dp[4 * g] = x.x, dp[4 * g + 1] = x.y, dp[4 * g + 2] = x.z, dp[4 * g + 3] = x.w;
       }
+#pragma unroll
+      for (int j = 0; j < KC; ++j) {
+        fetch(j + AHEAD);
+        in_order();
+        s = product(read[j], j < KR ? k[j] : kl[j - KR], s);
+        in_order();
+      }
+#pragma unroll
+      for (int j = 0; j < KC; ++j) {
+        fetch(KC + j + AHEAD);
+        in_order();
+        dp = product(read[KC + j], v[j], dp);
+        in_order();
+        if (j * 4 % KC == 0) {   // weights of four rows meanwhile
+          const int g = j * 4 / KC;
+          if (g > 0) weights(g - 1);
+          lse = read4(stats + 2 * g);   // LIFT - lse2
+        }
+      }
+      weights(3);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) dp[r] = NARROW<T> ? s[r] * (dp[r] * to_ds) : s[r] * dp[r];
       if (query0 < first_key + 31) {   // some keys lie behind some queries
         const int hidden = key - query0 - 4 * half;   // rows below it are
 #pragma unroll
@@ -347,14 +415,16 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
           dp[r] = 8 * (r / 4) + r % 4 < hidden ? 0.f : dp[r];
         }
       }
+      // rounded to T, half a step each
+      const V8 p[2] = {operand<T>(s, 0), operand<T>(s, 1)}, ds[2] = {operand<T>(dp, 0), operand<T>(dp, 1)};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const V8 p = operand<T>(s, j), ds = operand<T>(dp, j);   // rounded to T, half a step each
-#pragma unroll
-        for (int t = 0; t < DT; ++t) {
-          dv[t] = product(qc.template read<T>(t, TILE + 16 * j * Tile<DP>::ROW), p, dv[t]);
-          dk[t] = product(qc.template read<T>(t, 16 * j * Tile<DP>::ROW), ds, dk[t]);
-        }
+      for (int m = 0; m < 4 * DT; ++m) {
+        const int j = m / DT % 2, t = m % DT;
+        fetch(ROW_READS + m + AHEAD);
+        in_order();
+        if (m < 2 * DT) dv[t] = product(read[ROW_READS + m], p[j], dv[t]);
+        else dk[t] = product(read[ROW_READS + m], ds[j], dk[t]);
+        in_order();
       }
     }
   }
