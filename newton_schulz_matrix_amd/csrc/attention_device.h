@@ -147,6 +147,22 @@ struct Copier {
   }
 };
 
+// For kernels that have no registers to spare: reads and products in the order written, the
+// operand of a product read AHEAD products before it, and numbers that are made where they
+// are used instead of being kept (a constant that the compiler does not know, the lane).
+constexpr int AHEAD = 2;
+template <bool ON = true>
+__device__ __forceinline__ void in_order() {
+  if (ON) __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ uint32_t anew(uint32_t x) {
+  asm volatile("" : "+s"(x));
+  return x;
+}
+__device__ __forceinline__ int lane_anew() {
+  return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, anew(0)));
+}
+
 // Reading rows: A (or B) operand of 32 rows at columns 16 k .. + 15, a chunk for each
 // lane. Tiles begin at multiples of a row, so that the chunk is told by the
 // address' bits above 4 alone: the lane's addresses in a tile are one number with
@@ -158,6 +174,16 @@ struct RowReader {
     const int row = lane & 31, half = lane >> 5;
     at = row * Tile<DP>::ROW + ((half ^ Tile<DP>::swizzle(row)) << 4);
   }
+  // One address, the others made where they are used.
+  struct Lean {
+    uint32_t at;
+    template <class T>
+    __device__ __forceinline__ typename Eight<T>::type read(int k, int further) const {
+      const U32x4 v = *(const __attribute__((address_space(3))) U32x4*)((at ^ anew(k << 5)) + further);
+      return __builtin_bit_cast(typename Eight<T>::type, v);
+    }
+  };
+  __device__ __forceinline__ Lean lean_in(uint32_t tile) const { return {tile + at}; }
   struct In {
     uint32_t at[DP / 16];
     template <class T>
@@ -166,11 +192,6 @@ struct RowReader {
       return __builtin_bit_cast(typename Eight<T>::type, v);
     }
   };
-  template <class T>
-  __device__ __forceinline__ typename Eight<T>::type read(uint32_t tile, int k, int further) const {
-    const U32x4 v = *(const __attribute__((address_space(3))) U32x4*)(((tile + at) ^ (k << 5)) + further);
-    return __builtin_bit_cast(typename Eight<T>::type, v);
-  }
   __device__ __forceinline__ In in(uint32_t tile) const {
     In r;
 #pragma unroll
@@ -191,26 +212,30 @@ struct ColumnReader {
     const int row = 4 * (group >> 1) + (j >> 2), column = 16 * (group & 1) + 4 * (j & 3);
     at = row * Tile<DP>::ROW + (((column >> 3) ^ Tile<DP>::swizzle(row)) << 4) + (column & 4) * 2;
   }
+  template <class T>
+  __device__ static __forceinline__ typename Eight<T>::type read_at(uint32_t first, uint32_t eighth) {
+    const S16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) S16x4*)first);
+    const S16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) S16x4*)eighth);
+    const U32x2 a = __builtin_bit_cast(U32x2, x), b = __builtin_bit_cast(U32x2, y);
+    const U32x4 v = {a[0], a[1], b[0], b[1]};
+    return __builtin_bit_cast(typename Eight<T>::type, v);
+  }
   struct In {
     uint32_t at[DP / 32][2];   // four rows, and four from the eighth on
     template <class T>
     __device__ __forceinline__ typename Eight<T>::type read(int t, int further) const {
-      const S16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) S16x4*)(at[t][0] + further));
-      const S16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) S16x4*)(at[t][1] + (further + 8 * Tile<DP>::ROW)));
-      const U32x2 a = __builtin_bit_cast(U32x2, x), b = __builtin_bit_cast(U32x2, y);
-      const U32x4 v = {a[0], a[1], b[0], b[1]};
-      return __builtin_bit_cast(typename Eight<T>::type, v);
+      return read_at<T>(at[t][0] + further, at[t][1] + (further + 8 * Tile<DP>::ROW));
     }
   };
-  template <class T>
-  __device__ __forceinline__ typename Eight<T>::type read(uint32_t tile, int t, int further) const {
-    In r;
-    r.at[t][0] = (tile + at) ^ (t << 6);
-    r.at[t][1] = r.at[t][0] ^ (Tile<DP>::swizzle(8) << 4);
-    return r.template read<T>(t, further);
-  }
+  struct Lean {
+    uint32_t at;
+    template <class T>
+    __device__ __forceinline__ typename Eight<T>::type read(int t, int further) const {
+      return read_at<T>((at ^ anew(t << 6)) + further,
+                        (at ^ anew(t << 6 ^ Tile<DP>::swizzle(8) << 4)) + (further + 8 * Tile<DP>::ROW));
+    }
+  };
+  __device__ __forceinline__ Lean lean_in(uint32_t tile) const { return {tile + at}; }
   __device__ __forceinline__ In in(uint32_t tile) const {
     In r;
 #pragma unroll
@@ -221,6 +246,12 @@ struct ColumnReader {
     return r;
   }
 };
+
+template <bool LEAN, class Reader>
+__device__ __forceinline__ auto lean_or_all(const Reader& r, uint32_t tile) {
+  if constexpr (LEAN) return r.lean_in(tile);
+  else return r.in(tile);
+}
 
 // This lane's B operands of 32 rows of a head from memory (row: the lane's own, null
 // where there is none): k chunk k holds its columns 16 k + 8 (l / 32) .. + 7.

@@ -3,13 +3,18 @@
 //   S = scale q k^T (keys up to the query's own position), out = softmax(S) v,
 //   lse = log sum exp S
 //
-// Bound by the matrix units, and close behind them by the exponentials. A
-// workgroup takes 128 queries of one head, 32 a wave, and goes over the keys up
-// to its last query in tiles of 64, with the running maximum and sum of each row. Products are
-// taken transposed (keys x queries, columns x queries): a lane then holds one
-// query, a row's maximum and sum are its own registers and one exchange, and the
-// weights are the next product's operand as they stand. Keys and values come
-// into LDS directly, the next tile while this one is worked on.
+// Bound by the matrix units, at a clock that falls with what is done in each cycle
+// (2.4 GHz at most, 1.9 here): fewer reads of LDS are worth more than a denser order of
+// instructions. A workgroup takes 128 or 256 queries of one head, 32 or 64 a wave, and
+// goes over the keys up to its last query in tiles of 64, with the running maximum and
+// sum of each row. Products are taken transposed (keys x queries, columns x queries): a
+// lane then holds one query (or two), a row's maximum and sum are its own registers and
+// one exchange, and the weights are the next product's operand as they stand. Keys and
+// values come into LDS directly, the next tile while this one is worked on.
+//
+// Measured, bf16, 32 heads of 128 that read 8: 16384 tokens of one sequence 1925 us
+// (1142 TFLOP/s of what a query sees; a library product of 8192 cubed reaches 1180), 16256
+// tokens of eight sequences of 0 to 5113 463 us (972).
 #include <algorithm>
 #include <type_traits>
 
@@ -21,7 +26,6 @@ namespace nsmi {
 namespace {
 
 constexpr int WAVES = 4, THREADS = 64 * WAVES;
-constexpr int QUERIES = 32 * WAVES;   // of a workgroup
 constexpr int KEYS = 64;              // of a tile
 
 // The weights of a row stand against a reference that trails its running maximum
@@ -47,16 +51,26 @@ __device__ __forceinline__ void clear_rows(const AttnArgs& a, int head, int firs
 
 // With two SIDES eight waves share 128 queries, each half of every tile's keys, and
 // bring their sums together at the end: for launches that leave most of a CU empty.
-template <class T, int DP, int SIDES>
+//
+// With two GROUPS a wave has 64 queries, so that an operand from LDS serves two
+// products: half the reads, and half the copies of tiles. It takes 32 keys at once then and
+// reads operands AHEAD, in the order written, to stay within 256 registers.
+template <class T, int DP, int SIDES, int GROUPS>
 __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs a, int tiles, int parts, float* sums,
                                                                        float2* known_to) {
   typedef typename Eight<T>::type V8;
-  constexpr int KC = DP / 16, DT = DP / 32, SUB = KEYS / 32 / SIDES;   // 32 keys a time, SUB of them a tile
+  constexpr int KC = DP / 16, DT = DP / 32;
+  constexpr int SUB = GROUPS == 2 ? 1 : KEYS / 32 / SIDES;   // times 32 keys at once
+  constexpr int QUERIES = 128 * GROUPS;
+  constexpr bool WIDE = GROUPS == 2;
+  constexpr int EARLIER = WIDE ? AHEAD : 0;
   constexpr int TILE = KEYS * Tile<DP>::ROW;
   __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];   // keys, values, twice
   __shared__ float2 known[SIDES == 2 ? WAVES * 64 : 1];            // reference and sum of the second side
-  static_assert(4 * TILE >= QUERIES * DP * 4, "the sums of one side fit in the tiles");
+  static_assert(SIDES == 1 || GROUPS == 1, "the sums of two groups do not fit in the tiles");
+  static_assert(SIDES == 1 || 4 * TILE >= QUERIES * DP * 4, "the sums of one side fit in the tiles");
   const int lane = threadIdx.x & 63, half = lane >> 5;
+  auto own_lane = [&] { return WIDE ? lane_anew() : lane; };
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int side = wave / WAVES;
   const unsigned blocks = gridDim.x / parts;
@@ -73,7 +87,6 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
   const T* k = static_cast<const T*>(a.k.p) + at.begin * a.k.token + kv_head * a.k.head;
   const T* v = static_cast<const T*>(a.v.p) + at.begin * a.v.token + kv_head * a.v.head;
   const uint32_t k_step = static_cast<uint32_t>(a.k.token * 2), v_step = static_cast<uint32_t>(a.v.token * 2);
-  const Copier<DP, KEYS, WAVES * SIDES> k_copy(wave, lane, k_step, a.dim), v_copy(wave, lane, v_step, a.dim);
   const uint32_t lds = lds_address(smem);
   const int keys = min(at.length, at.row + QUERIES);   // that any query here sees
   const Range range = range_of((keys + KEYS - 1) / KEYS, part, parts);
@@ -81,122 +94,165 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
 
   auto fetch_tile = [&](int n) {
     const uint32_t to = lds + (n & 1) * 2 * TILE;
-    const int first = n * KEYS;
+    const int first = n * KEYS, l = own_lane();
+    const Copier<DP, KEYS, WAVES * SIDES> k_copy(wave, l, k_step, a.dim), v_copy(wave, l, v_step, a.dim);
     k_copy.copy(k + first * a.k.token, at.length - first, k_step, a.dim, to);
     v_copy.copy(v + first * a.v.token, at.length - first, v_step, a.dim, to + TILE);
   };
   if (range.first < steps) fetch_tile(range.first);
 
-  const int first_query = at.row + 32 * (wave % WAVES), query = first_query + (lane & 31);
-  const bool there = query < at.length;
-  V8 q[KC];
-  load_operands<T, DP>(there ? static_cast<const T*>(a.q.p) + (at.begin + query) * a.q.token + w.head * a.q.head
-                             : nullptr,
-                       a.dim, half, q);
+  // (the wave's queries, 32 a group; a lane has one of each)
+  const int first_query = at.row + 32 * GROUPS * (wave % WAVES), query = first_query + (lane & 31);
+  V8 q[GROUPS][KC];
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g)
+    load_operands<T, DP>(query + 32 * g < at.length ? static_cast<const T*>(a.q.p) +
+                                                          (at.begin + query + 32 * g) * a.q.token + w.head * a.q.head
+                                                    : nullptr,
+                         a.dim, half, q[g]);
   const RowReader<DP> rows(lane);
   const ColumnReader<DP> columns(lane);
   const float c = a.scale * 1.442695041f;   // weights as powers of two
-  Acc o[DT];
+  Acc o[GROUPS][DT];
+  float ref[GROUPS], sum[GROUPS];
 #pragma unroll
-  for (int t = 0; t < DT; ++t) o[t] = no_sum();
-  float ref = -INFINITY, sum = 0.f;
+  for (int g = 0; g < GROUPS; ++g) {
+#pragma unroll
+    for (int t = 0; t < DT; ++t) o[g][t] = no_sum();
+    ref[g] = -INFINITY, sum[g] = 0.f;
+  }
 
   for (int n = range.first; n < steps; ++n) {
     copies_done();
     __syncthreads();   // tile n is there, and nobody reads the place of tile n + 1
     if (n + 1 < steps) fetch_tile(n + 1);
-    const int first_key = n * KEYS + 32 * side;
-    if (first_key > first_query + 31) continue;
-    const uint32_t tile = lds + (n & 1) * 2 * TILE + 32 * side * Tile<DP>::ROW;
-    const auto kt = rows.in(tile);
-    const auto vt = columns.in(tile + TILE);
-    Acc s[SUB];
+#pragma unroll 1
+    for (int u = 0; u < KEYS / 32 / SIDES / SUB; ++u) {
+      const int row0 = 32 * side + 32 * SUB * u, first_key = n * KEYS + row0;
+      if (first_key > first_query + 32 * GROUPS - 1) break;
+      const uint32_t tile = lds + (n & 1) * 2 * TILE + row0 * Tile<DP>::ROW;
+      const auto kt = lean_or_all<WIDE>(rows, tile);
+      const auto vt = lean_or_all<WIDE>(columns, tile);   // TILE behind
+      constexpr int ROW_READS = SUB * KC, READS = ROW_READS + 2 * SUB * DT;
+      V8 read[READS];
+      auto fetch = [&](int m) {
+        if (m >= READS) return;
+        if (m < ROW_READS)
+          read[m] = kt.template read<T>(m / SUB, m % SUB * 32 * Tile<DP>::ROW);
+        else
+          read[m] = vt.template read<T>((m - ROW_READS) % DT, TILE + (m - ROW_READS) / DT * 16 * Tile<DP>::ROW);
+      };
 #pragma unroll
-    for (int i = 0; i < SUB; ++i) {
-      s[i] = no_sum();
+      for (int m = 0; m < EARLIER; ++m) fetch(m);
+      Acc s[GROUPS][SUB];
 #pragma unroll
-      for (int j = 0; j < KC; ++j) s[i] = product(kt.template read<T>(j, 32 * i * Tile<DP>::ROW), q[j], s[i]);
-    }
-    if (first_key + 32 * SUB - 1 > first_query) {   // some keys lie behind some queries
+      for (int m = 0; m < ROW_READS; ++m) {
+        fetch(m + EARLIER);
+        in_order<WIDE>();
 #pragma unroll
-      for (int i = 0; i < SUB; ++i)
+        for (int g = 0; g < GROUPS; ++g)
+          s[g][m % SUB] = product(read[m], q[g][m / SUB], m < SUB ? no_sum() : s[g][m % SUB]);
+        in_order<WIDE>();
+      }
+      V8 p[GROUPS][2 * SUB];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int key = first_key + 32 * i + 8 * (r / 4) + 4 * half + r % 4;
-          s[i][r] = key > query ? -INFINITY : s[i][r];
+      for (int g = 0; g < GROUPS; ++g) {
+        if (first_key + 32 * SUB - 1 > first_query + 32 * g) {   // some keys lie behind some queries
+          const int l = own_lane(), hidden = first_query + 32 * g + (l & 31) - first_key - 4 * (l >> 5);
+#pragma unroll
+          for (int i = 0; i < SUB; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              s[g][i][r] = 32 * i + 8 * (r / 4) + r % 4 > hidden ? -INFINITY : s[g][i][r];
         }
-    }
-    float top = s[0][0];
+        float top = s[g][0][0];
 #pragma unroll
-    for (int i = 0; i < SUB; ++i)
+        for (int i = 0; i < SUB; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[i][r]);
-    float lower, upper;
-    both_halves(top, lower, upper);
-    top = fmaxf(lower, upper) * c;
-    if (__any(top > ref + LAG + LIFT<T>)) {
-      const float to = fmaxf(ref, top - LIFT<T>);
-      // (a row of another side or part may not have met a key yet: its sums stay 0)
-      const float by = to == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref - to);
-      ref = to;
-      sum *= by;
+          for (int r = 0; r < 16; ++r) top = fmaxf(top, s[g][i][r]);
+        float lower, upper;
+        both_halves(top, lower, upper);
+        top = fmaxf(lower, upper) * c;
+        if (__any(top > ref[g] + LAG + LIFT<T>)) {
+          const float to = fmaxf(ref[g], top - LIFT<T>);
+          // (a row of another side or part may not have met a key yet: its sums stay 0)
+          const float by = to == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref[g] - to);
+          ref[g] = to;
+          sum[g] *= by;
 #pragma unroll
-      for (int t = 0; t < DT; ++t)
+          for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[t][r] *= by;
-    }
-    const float base = ref == -INFINITY ? 0.f : ref;
+            for (int r = 0; r < 16; ++r) o[g][t][r] *= by;
+        }
+        const float base = ref[g] == -INFINITY ? 0.f : ref[g];
 #pragma unroll
-    for (int i = 0; i < SUB; ++i)
+        for (int i = 0; i < SUB; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[i][r] = __builtin_amdgcn_exp2f(fmaf(s[i][r], c, -base));
-        sum += s[i][r];
+          for (int r = 0; r < 16; ++r) {
+            s[g][i][r] = __builtin_amdgcn_exp2f(fmaf(s[g][i][r], c, -base));
+            sum[g] += s[g][i][r];
+          }
+        // weights of at most 2^15, rounded to T: half a step each
+#pragma unroll
+        for (int j = 0; j < 2 * SUB; ++j) p[g][j] = operand<T>(s[g][j / 2], j % 2);
       }
 #pragma unroll
-    for (int j = 0; j < 2 * SUB; ++j) {
-      const V8 p = operand<T>(s[j / 2], j % 2);   // weights of at most 2^15, rounded to T: half a step each
+      for (int m = 0; m < 2 * SUB * DT; ++m) {
+        fetch(ROW_READS + m + EARLIER);
+        in_order<WIDE>();
 #pragma unroll
-      for (int t = 0; t < DT; ++t) o[t] = product(vt.template read<T>(t, 16 * j * Tile<DP>::ROW), p, o[t]);
+        for (int g = 0; g < GROUPS; ++g) o[g][m % DT] = product(read[ROW_READS + m], p[g][m / DT], o[g][m % DT]);
+        in_order<WIDE>();
+      }
     }
   }
 
-  float lower, upper;
-  both_halves(sum, lower, upper);
-  sum = lower + upper;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    float lower, upper;
+    both_halves(sum[g], lower, upper);
+    sum[g] = lower + upper;
+  }
   if constexpr (SIDES == 2) {
     __syncthreads();
     float* const shared = reinterpret_cast<float*>(smem) + wave % WAVES * 64 * DP / 2 + lane;
     if (side == 1) {
-      known[wave % WAVES * 64 + lane] = make_float2(ref, sum);
+      known[wave % WAVES * 64 + lane] = make_float2(ref[0], sum[0]);
 #pragma unroll
       for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) shared[64 * (16 * t + r)] = o[t][r];
+        for (int r = 0; r < 16; ++r) shared[64 * (16 * t + r)] = o[0][t][r];
     }
     __syncthreads();
     if (side == 1) return;
     const float2 other = known[wave * 64 + lane];
-    const float to = fmaxf(ref, other.x), base = to == -INFINITY ? 0.f : to;
-    const float mine = __builtin_amdgcn_exp2f(ref - base), theirs = __builtin_amdgcn_exp2f(other.x - base);
-    ref = to;
-    sum = sum * mine + other.y * theirs;
+    const float to = fmaxf(ref[0], other.x), base = to == -INFINITY ? 0.f : to;
+    const float mine = __builtin_amdgcn_exp2f(ref[0] - base), theirs = __builtin_amdgcn_exp2f(other.x - base);
+    ref[0] = to;
+    sum[0] = sum[0] * mine + other.y * theirs;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) o[t][r] = o[t][r] * mine + shared[64 * (16 * t + r)] * theirs;
+      for (int r = 0; r < 16; ++r) o[0][t][r] = o[0][t][r] * mine + shared[64 * (16 * t + r)] * theirs;
   }
-  if (parts > 1) {
-    const int64_t row = (static_cast<int64_t>(part) * a.q_heads + w.head) * a.tokens + at.begin + query;
-    store_sums<DP>(there ? sums + row * a.dim : nullptr, a.dim, half, o, 1.f);
-    if (there && half == 0) known_to[row] = make_float2(ref, sum);
-    return;
+  const int l = own_lane();
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    const int query = first_query + 32 * g + (l & 31), half = l >> 5;
+    const bool there = query < at.length;
+    const int64_t token = at.begin + query;
+    if (parts > 1) {
+      const int64_t row = (static_cast<int64_t>(part) * a.q_heads + w.head) * a.tokens + token;
+      store_sums<DP>(there ? sums + row * a.dim : nullptr, a.dim, half, o[g], 1.f);
+      if (there && half == 0) known_to[row] = make_float2(ref[g], sum[g]);
+      continue;
+    }
+    T* out = static_cast<T*>(a.out.p) + token * a.out.token + w.head * a.out.head;
+    store_columns<T, DP>(there ? out : nullptr, a.dim, half, o[g], 1.f / sum[g]);
+    if (there && half == 0)
+      a.lse[static_cast<int64_t>(w.head) * a.tokens + token] =
+          0.693147182f * (ref[g] + __builtin_amdgcn_logf(sum[g]));
   }
-  T* out = static_cast<T*>(a.out.p) + (at.begin + query) * a.out.token + w.head * a.out.head;
-  store_columns<T, DP>(there ? out : nullptr, a.dim, half, o, 1.f / sum);
-  if (there && half == 0)
-    a.lse[static_cast<int64_t>(w.head) * a.tokens + at.begin + query] =
-        0.693147182f * (ref + __builtin_amdgcn_logf(sum));
 }
 
 // Brings the parts' sums of a row together, eight columns a lane.
@@ -236,27 +292,41 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int par
 // heads that read 2 24 and 22 (134, 52); 8192 of 8 that read 2 203 and 161; of 12 that read 4,
 // where it is one part, two take 241 instead of 228.
 int attention_parts(int64_t tokens, int64_t sequences, int64_t heads, int64_t rows, bool keys) {
-  const int64_t blocks = tiles_of(tokens, sequences, QUERIES) * heads;
+  const int64_t blocks = tiles_of(tokens, sequences, 32 * WAVES) * heads;
   const int64_t few = std::min<int64_t>({8, 3 * CUS / blocks, rows / 512});
   if (few >= 2) return static_cast<int>(few);
   return keys && blocks < 3 * CUS && tokens / std::max<int64_t>(1, sequences) >= 4096 ? 2 : 1;
 }
 
+// Whether a wave takes 64 queries, for heads above 64: where the rows of all heads are 2304 times
+// 128 or more, and 512 or more a sequence. Us with 32 and 64 a wave (bf16, heads of 128): 4096
+// times 128, 16384 tokens of one sequence, 2076 and 1925; 2560, 1305 and 1238; 2048, 1042 and
+// 1052; 1024, 152 and 173: the chip is full of the wide ones at 512, and the longest of them are not
+// done when the others are. 32 sequences of 512, 135 and 134; 40 of 200, 55 and 60. Heads of
+// 64, whose four waves a SIMD hide more: 4096, 600 and 618.
+bool many_queries(const AttnArgs& a) {
+  return a.tokens * a.q_heads >= 9 * CUS * 128 && a.tokens >= 512 * a.sequences;
+}
+
 hipError_t launch_attention(const AttnArgs& a, int type, int parts, float* sums, float2* known, hipStream_t stream) {
-  const int64_t tiles = tiles_of(a.tokens, a.sequences, QUERIES);
-  auto on = [&](auto t, auto dp, auto sides) {
+  const int64_t tiles = tiles_of(a.tokens, a.sequences, 32 * WAVES);
+  auto on = [&](auto t, auto dp, auto sides, auto groups) {
     using T = decltype(t);
-    constexpr int DP = dp(), SIDES = sides();
-    hipLaunchKernelGGL((attention_kernel<T, DP, SIDES>), dim3(static_cast<unsigned>(tiles * a.q_heads * parts)),
-                       dim3(THREADS * SIDES), 0, stream, a, static_cast<int>(tiles), parts, sums, known);
+    constexpr int DP = dp(), SIDES = sides(), GROUPS = groups();
+    const int64_t n = tiles_of(a.tokens, a.sequences, 32 * WAVES * GROUPS);
+    hipLaunchKernelGGL((attention_kernel<T, DP, SIDES, GROUPS>), dim3(static_cast<unsigned>(n * a.q_heads * parts)),
+                       dim3(THREADS * SIDES), 0, stream, a, static_cast<int>(n), parts, sums, known);
     if (parts > 1)
       hipLaunchKernelGGL(attention_join_kernel<T>, dim3((a.tokens * (a.dim / 8) + 255) / 256, a.q_heads), dim3(256),
                          0, stream, a, parts, sums, known);
     return hipGetLastError();
   };
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
   auto sided = [&](auto t, auto dp) {
-    return two_sides(tiles * a.q_heads * parts) ? on(t, dp, std::integral_constant<int, 2>{})
-                                                : on(t, dp, std::integral_constant<int, 1>{});
+    if constexpr (dp() == 128)
+      if (parts == 1 && many_queries(a)) return on(t, dp, One{}, Two{});
+    return two_sides(tiles * a.q_heads * parts) ? on(t, dp, Two{}, One{}) : on(t, dp, One{}, One{});
   };
   auto shaped = [&](auto t) {
     return a.dim <= 64 ? sided(t, std::integral_constant<int, 64>{}) : sided(t, std::integral_constant<int, 128>{});

@@ -243,19 +243,13 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
 constexpr int KV_WAVES = 8, KV_THREADS = 64 * KV_WAVES;
 constexpr int KV_STEP = 128;          // queries of a tile
 
-// The products come in the order they are written in, each operand read two products
-// ahead, the weights' exponentials between those of dout v^T: left to itself the
-// compiler puts every read right before its product, and the kernel takes 14% more
-// cycles (5% more time: the clock falls with the work in each of them). The registers
-// for it (two waves of 256 a SIMD) come from the second half of a wave's keys, which
-// lies in LDS for heads above 64, and from addresses that are made anew for each read.
-constexpr int AHEAD = 2;
+// The products come in the order they are written in, each operand read AHEAD, the
+// weights' exponentials between those of dout v^T: left to itself the compiler puts every
+// read right before its product, and the kernel takes 14% more cycles (5% more time: the
+// clock falls with the work in each of them). The registers for it (two waves of 256 a
+// SIMD) come from the second half of a wave's keys, which lies in LDS for heads above 64,
+// and from addresses that are made where they are used.
 constexpr int KEY_CHUNKS = 4;         // of 16 columns in registers
-__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
-__device__ __forceinline__ uint32_t anew(uint32_t x) {
-  asm volatile("" : "+s"(x));
-  return x;
-}
 __device__ __forceinline__ float4 read4(const __attribute__((address_space(3))) float4* p) {
   typedef float F4 __attribute__((ext_vector_type(4)));
   const F4 v = *(const __attribute__((address_space(3))) F4*)p;
@@ -353,21 +347,22 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
     for (int i = 0; i < KV_STEP / 64; ++i) {
       const int row0 = 64 * i + 32 * side, query0 = first_query + row0;
       if (query0 + 31 < first_key) continue;
+      const auto qr = rows.lean_in(qt + row0 * Tile<DP>::ROW);   // dout's tile lies TILE behind
+      const auto qc = columns.lean_in(qt + row0 * Tile<DP>::ROW);
       const __attribute__((address_space(3))) float4* const stats =
           (const __attribute__((address_space(3))) float4*)(qt + 2 * TILE) + row0 / 4 + half;
-      // The products in their order, and what each reads: S, dout v^T (whose tile lies TILE behind), then
-      // dv and dk by halves of the queries and 32 columns.
+      // The products in their order, and what each reads: S, dout v^T, then dv and dk
+      // by halves of the queries and 32 columns.
       constexpr int ROW_READS = 2 * KC, READS = ROW_READS + 4 * DT;
       V8 read[READS], kl[KL > 0 ? KL : 1];
       auto fetch = [&](int n) {
         if (n >= READS) return;
         if (n < ROW_READS) {
-          read[n] = rows.template read<T>(anew(qt + row0 * Tile<DP>::ROW), n % KC, n / KC * TILE);
+          read[n] = qr.template read<T>(n % KC, n / KC * TILE);
           if (n >= KR && n < KC) kl[n - KR] = k_rows.template read<T>(n - KR, 0);
         } else {
           const int m = n - ROW_READS;
-          read[n] = columns.template read<T>(anew(qt + row0 * Tile<DP>::ROW), m % DT,
-                                             (m < 2 * DT ? TILE : 0) + 16 * (m / DT % 2) * Tile<DP>::ROW);
+          read[n] = qc.template read<T>(m % DT, (m < 2 * DT ? TILE : 0) + 16 * (m / DT % 2) * Tile<DP>::ROW);
         }
       };
 #pragma unroll

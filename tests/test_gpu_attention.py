@@ -46,9 +46,15 @@ def weight_error(c, ends, scale, lse):
     return (dim + 8) * U32 * most + 4 * U32 * np.abs(lse).max(initial=0.0) + 16 * U32
 
 
-def check(c, scale=None, **outs):
+def check(c, scale=None, times=1, **outs):
+    """(times: the heads that many times one behind the other, which must all come out alike.)"""
     dtype, dim = c["q"].dtype, c["q"].shape[2]
-    out, lse = nsmi.ns_attention(c["q"], c["k"], c["v"], c["offsets"], scale=scale, **outs)
+    out, lse = nsmi.ns_attention(*(c[x].repeat(1, times, 1) if times > 1 else c[x] for x in "qkv"), c["offsets"],
+                                 scale=scale, **outs)
+    if times > 1:
+        outs_of, lses = out.unflatten(1, (times, -1)), lse.unflatten(0, (times, -1))
+        assert (outs_of == outs_of[:, :1]).all() and (lses == lses[:1]).all()
+        out, lse = outs_of[:, 0], lses[0]
     ends = c["offsets"].tolist()
     s = dim ** -0.5 if scale is None else scale
     n = ends[-1]
@@ -96,6 +102,22 @@ def test_peaked_and_flat(dtype):
     check(c)
     c["k"] = c["k"].flip(0).contiguous()
     check(c)
+
+
+# Rows of all heads from 294912 on, 512 or more a sequence: waves take 64 queries for heads above 64.
+@pytest.mark.parametrize("lengths, rest, dim", [([577], 0, 128), ([513, 1100], 0, 72), ([1400, 0, 301], 61, 104),
+                                                ([2049], 0, 64), ([1, 1, 2300], 1, 128)], ids=str)
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_many_queries(lengths, rest, dim, dtype):
+    require_gpu()
+    c = make(9, lengths, 4, 2, dim, dtype, rest=rest)
+    times = -(-294912 // (4 * c["q"].shape[0]))
+    out, lse = check(c, times=times)
+    n = sum(lengths)
+    assert not out[n:].any() and not lse[:, n:].any()
+    c = make(10, lengths, 4, 2, dim, dtype, peak=30.0)
+    c["k"][:, 1] = torch.linspace(0, 4, n, device="cuda").to(dtype)[:, None]
+    check(c, times=times)
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
