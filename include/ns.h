@@ -564,8 +564,8 @@ ns_status ns_qk_norm_rope_grad(const ns_qk_norm_rope_args* args, ns_heads dq_out
  *   lse     (q_heads, tokens) fp32.
  * Rows behind the last sequence are not read; of out and lse (of the gradients)
  * they stay as they are, or, with clear_rest != 0, become 0. A NaN or infinity in a
- * row of a sequence may reach earlier rows of the same sequence within 128 of
- * it, never another sequence.
+ * row of a sequence may reach results of the same sequence's rows within 128 of it
+ * whose formulas do not hold it, never another sequence.
  * S, the softmax and all sums are fp32; P and, in the gradient, P and dS are
  * rounded to the tensors' type for the products with v, dout, k and q (fp16: scaled
  * into its range first).

@@ -3,7 +3,7 @@
 //   P = exp(S - lse), S = scale q k^T;   delta = sum of dout out over a head's columns
 //   dv = P^T dout,  dS = P (dout v^T - delta),  dq = scale dS k,  dk = scale dS^T q
 //
-// Bound by the matrix units. Two launches: dq, where a workgroup keeps 128 queries and
+// Bound by the matrix units, at 1.9 GHz of 2.4. Two launches: dq, where a workgroup keeps 128 queries and
 // goes over the keys before them, and which leaves delta of its rows; dk and dv,
 // where it keeps 128 keys of one key head and goes over the queries of its group's
 // heads behind them. S and dout v^T are worked out in both (seven products instead of five): the
@@ -11,6 +11,10 @@
 // order changes the sums, or a place for every pair of tiles. Everything is laid out
 // as in the forward pass: the weights of a lane are one row or column, and go on as
 // the next product's operand.
+//
+// Measured, bf16, 32 heads of 128 that read 8, 16256 tokens of eight sequences of 0 to 5113:
+// dq 700 us, dk and dv 910 (1.12 TFLOP that the gradient cannot do without, 1.57 with S and
+// dout v^T again: 970 TFLOP/s; a library product of 8192 cubed reaches 1180).
 //
 // fp16: weights and dS of a long row lie among its subnormals. Weights are taken
 // times 2^14, and dS times a power of two that keeps the largest one possible

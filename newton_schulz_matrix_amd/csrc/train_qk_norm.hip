@@ -11,6 +11,11 @@
 // in a row where pairs are neighbours), and two of the rest for the lanes behind.
 // A wave takes one token, several heads at a time, so that its lanes keep the
 // same pairs and the angles are worked out once for all heads of a token.
+//
+// Measured, bf16, heads of 128, 32 of queries and 8 of keys: 16384 tokens 66 us (336 MB:
+// 5.1 TB/s), the gradient 104 + 5 us (503 MB: 4.8), where a library copy of 1 GB runs at 5.0. With
+// few small heads the angles (a reduction in 64 bits and a sine a pair and token) bound
+// it: 65536 tokens of 8 heads of 80, 53 us (3.2 TB/s).
 #include <algorithm>
 #include <type_traits>
 
