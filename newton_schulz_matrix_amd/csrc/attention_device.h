@@ -398,6 +398,20 @@ __device__ __forceinline__ Range range_of(int64_t steps, int part, int parts) {
   return {static_cast<int>(steps * part / parts), static_cast<int>(steps * (part + 1) / parts)};
 }
 
+// Which part of which tile's work a workgroup has (block < 0: none). The parts of eight
+// tiles come one behind the other, so that the longest tiles' parts are all begun
+// first, and a tile's keys stay on the XCD that work_of() has in mind.
+struct Share {
+  int block, part;
+};
+__device__ __forceinline__ Share share_of(int blocks, int parts) {
+  const int n = blockIdx.x / 8, block = n / parts * 8 + blockIdx.x % 8;
+  return {block < blocks ? block : -1, n % parts};
+}
+inline unsigned shared_blocks(int64_t blocks, int parts) {
+  return static_cast<unsigned>((blocks + 7) / 8 * 8 * parts);
+}
+
 // A part's result in memory as fp32: rows of a head by columns of the lane, as for
 // store_columns.
 template <int DP>

@@ -73,9 +73,10 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
   auto own_lane = [&] { return WIDE ? lane_anew() : lane; };
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int side = wave / WAVES;
-  const unsigned blocks = gridDim.x / parts;
-  const int part = blockIdx.x / blocks;
-  const Work w = work_of(blockIdx.x - part * blocks, a.q_heads, a.k_heads);
+  const Share share = share_of(tiles * a.q_heads, parts);
+  if (share.block < 0) return;
+  const int part = share.part;
+  const Work w = work_of(share.block, a.q_heads, a.k_heads);
   const Place at = place_of<QUERIES, false>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
   if (at.rest) {
@@ -314,7 +315,7 @@ hipError_t launch_attention(const AttnArgs& a, int type, int parts, float* sums,
     using T = decltype(t);
     constexpr int DP = dp(), SIDES = sides(), GROUPS = groups();
     const int64_t n = tiles_of(a.tokens, a.sequences, 32 * WAVES * GROUPS);
-    hipLaunchKernelGGL((attention_kernel<T, DP, SIDES, GROUPS>), dim3(static_cast<unsigned>(n * a.q_heads * parts)),
+    hipLaunchKernelGGL((attention_kernel<T, DP, SIDES, GROUPS>), dim3(shared_blocks(n * a.q_heads, parts)),
                        dim3(THREADS * SIDES), 0, stream, a, static_cast<int>(n), parts, sums, known);
     if (parts > 1)
       hipLaunchKernelGGL(attention_join_kernel<T>, dim3((a.tokens * (a.dim / 8) + 255) / 256, a.q_heads), dim3(256),

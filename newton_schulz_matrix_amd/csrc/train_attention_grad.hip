@@ -113,9 +113,10 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int side = wave / WAVES;
-  const unsigned blocks = gridDim.x / parts;
-  const int part = blockIdx.x / blocks;
-  const Work w = work_of(blockIdx.x - part * blocks, a.q_heads, a.k_heads);
+  const Share share = share_of(tiles * a.q_heads, parts);
+  if (share.block < 0) return;
+  const int part = share.part;
+  const Work w = work_of(share.block, a.q_heads, a.k_heads);
   const Place at = place_of<ROWS, false>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
   if (at.rest) {
@@ -277,9 +278,10 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const ui
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int side = wave / 4;           // of a tile's queries
-  const unsigned blocks = gridDim.x / parts;
-  const int part = blockIdx.x / blocks;
-  const Work w = work_of(blockIdx.x - part * blocks, a.k_heads, a.k_heads);
+  const Share share = share_of(tiles * a.k_heads, parts);
+  if (share.block < 0) return;
+  const int part = share.part;
+  const Work w = work_of(share.block, a.k_heads, a.k_heads);
   const Place at = place_of<ROWS, true>(a.offsets, a.sequences, a.tokens, tiles, w.tile);
   if (at.length == 0) return;
   if (at.rest) {
@@ -494,13 +496,13 @@ hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k
     };
     auto queries = [&](auto sides) {
       constexpr int SIDES = sides();
-      hipLaunchKernelGGL((dq_kernel<T, DP, SIDES>), dim3(static_cast<unsigned>(tiles * a.q_heads * q_parts)),
+      hipLaunchKernelGGL((dq_kernel<T, DP, SIDES>), dim3(shared_blocks(tiles * a.q_heads, q_parts)),
                          dim3(THREADS * SIDES), 0, stream, a, peaks, static_cast<int>(tiles), q_parts, sums);
     };
     if (two_sides(tiles * a.q_heads * q_parts)) queries(std::integral_constant<int, 2>{});
     else queries(std::integral_constant<int, 1>{});
     join(1, a.dq, a.dq, a.q_heads, q_parts);
-    hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(static_cast<unsigned>(tiles * a.k_heads * k_parts)),
+    hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(shared_blocks(tiles * a.k_heads, k_parts)),
                        dim3(KV_THREADS), 0, stream, a, peaks, static_cast<int>(tiles), k_parts, sums);
     join(2, a.dk, a.dv, a.k_heads, k_parts);
     return hipGetLastError();
