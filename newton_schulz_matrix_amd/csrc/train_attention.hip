@@ -286,15 +286,17 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int par
 }  // namespace
 
 // Up to eight parts, of 512 rows or more, where there are few workgroups: as many as
-// make three of them for a CU. Two of the keys where there are less than three for a CU
-// and the sequences are long: all are on the chip at once then, and those of the ends take twice the
-// average. Forward (and whole gradient) of bf16 heads of 128, us in one part and so: 16384
-// tokens of 1 head 313 and 130 (733, 367); 4096 of 4 heads 71 and 48 (194, 144); 1500 of 8
-// heads that read 2 24 and 22 (134, 52); 8192 of 8 that read 2 203 and 161; of 12 that read 4,
-// where it is one part, two take 241 instead of 228.
+// make three of them for a CU, or two and a half where they are those of keys, of which a CU
+// holds one. Two of the keys where there are less than three for a CU and the sequences are
+// long: all are on the chip at once then, and those of the ends take twice the average.
+// Forward and whole gradient of bf16 heads of 128, us in one part and so: 16384 tokens of 1
+// head 313 and 94 (733, 286); 4096 of 4 heads 71 and 41 (194, 116); 1500 of 8 heads that read 2 24
+// and 22 (134, 68); 8192 of 8 that read 2 203 and 161; of 12 that read 4, where it is one part,
+// two take 241 instead of 228. Three parts of the keys for a CU: 302, 129 and 68 for the first
+// three gradients; two: 295, 113 and, 2048 tokens of 16 that read 4, 120 instead of 118.
 int attention_parts(int64_t tokens, int64_t sequences, int64_t heads, int64_t rows, bool keys) {
   const int64_t blocks = tiles_of(tokens, sequences, 32 * WAVES) * heads;
-  const int64_t few = std::min<int64_t>({8, 3 * CUS / blocks, rows / 512});
+  const int64_t few = std::min<int64_t>({8, (keys ? 6 : 5) * CUS / (2 * blocks), rows / 512});
   if (few >= 2) return static_cast<int>(few);
   return keys && blocks < 3 * CUS && tokens / std::max<int64_t>(1, sequences) >= 4096 ? 2 : 1;
 }
