@@ -298,7 +298,7 @@ AttnGradPlan attention_grad_plan(int64_t tokens, int64_t sequences, int64_t q_he
   p.k_parts = attention_parts(tokens, sequences, k_heads, tokens * (q_heads / k_heads), false);
   p.delta = rows;
   p.peaks = 2 * rows;
-  p.sums = p.peaks + align_up(sizeof(uint32_t) * 2 * PEAKS);
+  p.sums = p.peaks + align_up(sizeof(float) * 2 * PEAKS);
   const int64_t most = std::max(p.q_parts > 1 ? p.q_parts * q_heads : 0, p.k_parts > 1 ? 2 * p.k_parts * k_heads : 0);
   p.total = p.sums + align_up(sizeof(float) * static_cast<size_t>(most) * tokens * dim);
   return p;
@@ -388,7 +388,7 @@ NS_API ns_status ns_attention_grad(const ns_attention_args* p, ns_heads dout, ns
   a.lse2 = reinterpret_cast<float*>(w);
   a.delta = reinterpret_cast<float*>(w + plan.delta);
   return from_hip(launch_attention_grad(a, p->dtype, plan.q_parts, plan.k_parts,
-                                        reinterpret_cast<uint32_t*>(w + plan.peaks),
+                                        reinterpret_cast<float*>(w + plan.peaks),
                                         reinterpret_cast<float*>(w + plan.sums),
                                         static_cast<hipStream_t>(stream)));
 }

@@ -73,10 +73,9 @@ struct AttnArgs {
 int attention_parts(int64_t tokens, int64_t sequences, int64_t heads, int64_t rows, bool keys);
 hipError_t launch_attention(const AttnArgs& a, int type, int parts, float* sums, float2* known, hipStream_t stream);
 
-// Greatest norms of a head's rows in dout and v, in so many places each, so that
-// waves do not queue for one (fp16 only).
-constexpr int PEAKS = 64;
-hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k_parts, uint32_t* peaks, float* sums,
+// Greatest norms of a head's rows in dout and v, in so many workgroups' shares each (fp16 only).
+constexpr int PEAKS = 256;
+hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k_parts, float* peaks, float* sums,
                                  hipStream_t stream);
 
 }  // namespace nsmi

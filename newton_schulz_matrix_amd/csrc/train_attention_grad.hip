@@ -42,48 +42,61 @@ constexpr bool NARROW<_Float16> = true;
 constexpr float LIFT = 14.f;
 
 // What dS is multiplied by, for fp16.
-__device__ __forceinline__ float ds_scale(const uint32_t* peaks) {
+__device__ __forceinline__ float ds_scale(const float* peaks) {
   const int lane = threadIdx.x & 63;
-  static_assert(PEAKS == 64, "one for each lane");
-  const float most = 2.f * wave_max(__builtin_bit_cast(float, peaks[lane])) *
-                     wave_max(__builtin_bit_cast(float, peaks[PEAKS + lane]));
+  static_assert(PEAKS == 256, "four for each lane");
+  float of[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 x = reinterpret_cast<const float4*>(peaks + i * PEAKS)[lane];
+    of[i] = wave_max(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
+  }
+  const float most = 2.f * of[0] * of[1];
   if (!(most > 0.f && most < INFINITY)) return 1.f;
   int e;
   frexpf(most, &e);
   return ldexpf(1.f, min(max(14 - e, -60), 60));
 }
 
-__global__ void clear_peaks_kernel(uint32_t* peaks) {
-  peaks[threadIdx.x] = 0;
-}
-
-// fp16: the greatest norms of dout's rows of a head and v's, 16 lanes a row, 16 rows
-// one behind the other a workgroup. A maximum does not depend on the order in which
-// it is taken.
+// fp16: the greatest norms of dout's rows of a head and of v's, one of each for a
+// workgroup, 16 lanes a row. (2064 tokens of 8 heads of 80: 5 us; a maximum in one place for
+// all needs a launch that clears it first.)
+constexpr int NORM_THREADS = 1024, NORM_ROWS = NORM_THREADS / 16;
 template <class T>
-__global__ __launch_bounds__(256) void norms_kernel(AttnArgs a, uint32_t* peaks) {
-  __shared__ float tops[4];
+__global__ __launch_bounds__(NORM_THREADS) void norms_kernel(AttnArgs a, float* peaks) {
+  __shared__ float tops[2][NORM_THREADS / 64];
   const int lane = threadIdx.x & 15;
-  const int token = blockIdx.x * 16 + threadIdx.x / 16, head = blockIdx.y;
   const int first = offset_at(a.offsets, 0, a.tokens), last = offset_at(a.offsets, a.sequences, a.tokens);
-  const bool of_v = head >= a.q_heads;
-  float norm = 0.f;
-  if (token >= first && token < last && 8 * lane < a.dim) {
-    const HeadsAt& from = of_v ? a.v : a.dout;
-    float x[VEC];
-    load8(static_cast<const T*>(from.p) + token * from.token + (head - (of_v ? a.q_heads : 0)) * from.head + 8 * lane,
-          x);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) norm = fmaf(x[e], x[e], norm);
+  for (int i = 0; i < 2; ++i) {
+    const HeadsAt& from = i ? a.v : a.dout;
+    const int heads = i ? a.k_heads : a.q_heads;
+    const int64_t rows = static_cast<int64_t>(last - first) * heads;
+    float top = 0.f;
+    for (int64_t row = blockIdx.x * NORM_ROWS + threadIdx.x / 16; row - threadIdx.x / 16 < rows;
+         row += PEAKS * NORM_ROWS) {
+      float norm = 0.f;
+      if (row < rows && 8 * lane < a.dim) {
+        const int64_t token = row / heads;
+        float x[VEC];
+        load8(static_cast<const T*>(from.p) + (first + token) * from.token + (row - token * heads) * from.head +
+                  8 * lane,
+              x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) norm = fmaf(x[e], x[e], norm);
+      }
+#pragma unroll
+      for (int off = 8; off >= 1; off >>= 1) norm += __shfl_xor(norm, off, 64);
+      top = fmaxf(top, norm);   // (a NaN is passed over: its rows are NaN anyway)
+    }
+    top = wave_max(top);
+    if ((threadIdx.x & 63) == 0) tops[i][threadIdx.x >> 6] = top;
   }
-#pragma unroll
-  for (int off = 8; off >= 1; off >>= 1) norm += __shfl_xor(norm, off, 64);
-  norm = wave_max(norm);   // (a NaN is passed over: its rows are NaN anyway)
-  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = norm;
   __syncthreads();
-  if (threadIdx.x != 0) return;
-  norm = sqrtf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
-  atomicMax(peaks + (of_v ? PEAKS : 0) + (blockIdx.x + 7 * head) % PEAKS, __builtin_bit_cast(uint32_t, norm));
+  if (threadIdx.x >= 2) return;
+  float top = 0.f;
+  for (int w = 0; w < NORM_THREADS / 64; ++w) top = fmaxf(top, tops[threadIdx.x][w]);
+  peaks[threadIdx.x * PEAKS + blockIdx.x] = sqrtf(top);
 }
 
 // Rows behind the last sequence: zeros.
@@ -103,7 +116,7 @@ __device__ __forceinline__ void clear_rows(const HeadsAt& to, int head, int dim,
 // tile's keys, and add up at the end: for launches that leave most of a CU empty. The
 // rows' delta and lse log2(e) are left for the kernel below.
 template <class T, int DP, int SIDES>
-__global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, const uint32_t* peaks, int tiles,
+__global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, const float* peaks, int tiles,
                                                                int parts, float* sums) {
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32;
@@ -265,7 +278,7 @@ __device__ __forceinline__ float4 read4(const __attribute__((address_space(3))) 
 // queries of the same keys, and leave their sums in fp32 for a kernel that adds
 // them up in order.
 template <class T, int DP>
-__global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const uint32_t* peaks, int tiles,
+__global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const float* peaks, int tiles,
                                                             int parts, float* sums) {
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32;
@@ -478,16 +491,14 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, HeadsAt first, He
 
 }  // namespace
 
-hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k_parts, uint32_t* peaks, float* sums,
+hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k_parts, float* peaks, float* sums,
                                  hipStream_t stream) {
   const int64_t tiles = tiles_of(a.tokens, a.sequences, ROWS);
   auto on = [&](auto t, auto dp) {
     using T = decltype(t);
     constexpr int DP = dp();
     if constexpr (NARROW<T>) {
-      hipLaunchKernelGGL(clear_peaks_kernel, dim3(1), dim3(2 * PEAKS), 0, stream, peaks);
-      hipLaunchKernelGGL(norms_kernel<T>, dim3((a.tokens + 15) / 16, a.q_heads + a.k_heads), dim3(256), 0, stream,
-                         a, peaks);
+      hipLaunchKernelGGL(norms_kernel<T>, dim3(PEAKS), dim3(NORM_THREADS), 0, stream, a, peaks);
     }
     auto join = [&](int tensors, const HeadsAt& first, const HeadsAt& second, int heads, int parts) {
       if (parts > 1)
