@@ -104,6 +104,8 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
 
   // (the wave's queries, 32 a group; a lane has one of each)
   const int first_query = at.row + 32 * GROUPS * (wave % WAVES), query = first_query + (lane & 31);
+  // (a wave without rows only brings tiles in: one row behind the last full tile would cost a tile's time)
+  const int last_query = first_query < at.length ? first_query + 32 * GROUPS - 1 : -1;
   V8 q[GROUPS][KC];
 #pragma unroll
   for (int g = 0; g < GROUPS; ++g)
@@ -130,7 +132,7 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs 
 #pragma unroll 1
     for (int u = 0; u < KEYS / 32 / SIDES / SUB; ++u) {
       const int row0 = 32 * side + 32 * SUB * u, first_key = n * KEYS + row0;
-      if (first_key > first_query + 32 * GROUPS - 1) break;
+      if (first_key > last_query) break;
       const uint32_t tile = lds + (n & 1) * 2 * TILE + row0 * Tile<DP>::ROW;
       const auto kt = lean_or_all<WIDE>(rows, tile);
       const auto vt = lean_or_all<WIDE>(columns, tile);   // TILE behind

@@ -156,6 +156,7 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
 
   const int first_query = at.row + 32 * (wave % WAVES), query = first_query + (lane & 31);
   const bool there = query < at.length;
+  const int last_query = first_query < at.length ? first_query + 31 : -1;   // none: it only brings tiles in
   const int64_t token = at.begin + query;
   V8 q[KC], g[KC];
   load_operands<T, DP>(there ? static_cast<const T*>(a.q.p) + token * a.q.token + w.head * a.q.head : nullptr,
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
 #pragma unroll
     for (int i = 0; i < STEP / 32 / SIDES; ++i) {
       const int key0 = key1 + 32 * i, at_row = 32 * i * Tile<DP>::ROW;
-      if (key0 > first_query + 31) break;
+      if (key0 > last_query) break;
       Acc s = no_sum(), dp = no_sum();
 #pragma unroll
       for (int j = 0; j < KC; ++j) s = product(kt.template read<T>(j, at_row), q[j], s);
@@ -365,7 +366,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const fl
 #pragma unroll 1
     for (int i = 0; i < KV_STEP / 64; ++i) {
       const int row0 = 64 * i + 32 * side, query0 = first_query + row0;
-      if (query0 + 31 < first_key) continue;
+      if (query0 + 31 < first_key || max(query0, first_key) >= at.length) continue;
       const auto qr = rows.lean_in(qt + row0 * Tile<DP>::ROW);   // dout's tile lies TILE behind
       const auto qc = columns.lean_in(qt + row0 * Tile<DP>::ROW);
       const __attribute__((address_space(3))) float4* const stats =
