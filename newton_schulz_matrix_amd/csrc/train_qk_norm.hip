@@ -455,10 +455,11 @@ __global__ __launch_bounds__(DW_COLS * DW_GROUPS) void qk_dweight_kernel(const f
   if (to) to[col < dim ? col : col - dim] = static_cast<TO>(static_cast<float>(s));
 }
 
-// Calls f with the widest vectors that the sizes allow, as a type.
-template <class F>
+// Calls f with the widest vectors that the sizes allow, up to MOST, as a type.
+template <int MOST, class F>
 hipError_t by_vector(const QkArgs& a, F f) {
-  if (a.dim % 16 == 0 && a.rotary % 16 == 0) return f(std::integral_constant<int, 8>{});
+  if constexpr (MOST == 8)
+    if (a.dim % 16 == 0 && a.rotary % 16 == 0) return f(std::integral_constant<int, 8>{});
   if (a.dim % 8 == 0 && a.rotary % 8 == 0) return f(std::integral_constant<int, 4>{});
   return f(std::integral_constant<int, 2>{});
 }
@@ -470,6 +471,9 @@ int team_of(int dim, int w) {
 
 }  // namespace
 
+// fp32 has vectors of 4 (16 bytes; 30000 tokens of 8 heads of 80: 25.6 us, 29 with vectors
+// of 8; 8192 of 40 heads of 128 65 and 67; the gradient is no faster with them, 108 and 105).
+//
 // Workgroups that take many tokens bring the weights to LDS once for all of them (65536
 // tokens of 8 heads of 80: 52.8 us, 61 with a workgroup for each four).
 constexpr int NORM_BLOCKS = 4096;
@@ -477,7 +481,7 @@ constexpr int NORM_BLOCKS = 4096;
 hipError_t launch_qk_norm_rope(const QkArgs& a, int type, hipStream_t stream) {
   return by_type(type, [&](auto t) {
     using T = decltype(t);
-    return by_vector(a, [&](auto w) {
+    return by_vector<sizeof(T) == 4 ? 4 : 8>(a, [&](auto w) {
       constexpr int W = w();
       const int team = team_of(a.dim, W), each = 64 / team;
       const int all = (a.part[0].heads + a.part[1].heads + each - 1) / each;
@@ -485,8 +489,8 @@ hipError_t launch_qk_norm_rope(const QkArgs& a, int type, hipStream_t stream) {
       const int rounds = a.tokens < 2048 ? 1 : all;
       const int chunks = (all + rounds - 1) / rounds;
       const int64_t units = static_cast<int64_t>(a.tokens) * chunks;
-      hipLaunchKernelGGL((qk_norm_kernel<T, W>), dim3(std::min<int64_t>((units + WAVES - 1) / WAVES, NORM_BLOCKS)), dim3(THREADS), 0,
-                         stream, a, team, rounds, chunks);
+      hipLaunchKernelGGL((qk_norm_kernel<T, W>), dim3(std::min<int64_t>((units + WAVES - 1) / WAVES, NORM_BLOCKS)),
+                         dim3(THREADS), 0, stream, a, team, rounds, chunks);
       return hipGetLastError();
     });
   });
@@ -505,7 +509,7 @@ hipError_t launch_qk_norm_rope_grad(const QkArgs& a, int type, float* partial, v
   if (blocks > 0) {
     const hipError_t e = by_type(type, [&](auto t) {
       using T = decltype(t);
-      return by_vector(a, [&](auto w) {
+      return by_vector<8>(a, [&](auto w) {
         constexpr int W = w();
         const int team = team_of(a.dim, W), each = 64 / team;
         const int rounds = (a.part[0].heads + a.part[1].heads + each - 1) / each;
