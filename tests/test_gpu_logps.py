@@ -125,6 +125,27 @@ def test_nan_and_infinite_logits(vocab):
     assert got[4][3, 0] == 9 and got[4][4].tolist() == [50, -1, -1, -1, -1]
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+@pytest.mark.parametrize("top", [5, 32, 33, 64])
+def test_likeliest_beside_many_nan(dtype, top):
+    """Whole vectors of NaN, and single ones, between entries that rise, fall or lie anywhere."""
+    require_gpu()
+    for vocab in (130, 3000, 50021):
+        z, tokens = make(13, 6, vocab, dtype, ignored=0)
+        z[1] = torch.linspace(-8, 8, vocab, device="cuda").to(dtype)
+        z[2] = z[1].flip(0)
+        at = torch.arange(vocab, device="cuda")
+        z[:3, at // 8 % 2 == 1] = float("nan")
+        z[3, at // 64 % 3 != 1] = float("nan")
+        z[4, at % 2 == 0] = float("nan")
+        z[5, 60:] = float("nan")
+        ids = nsmi.ns_token_logps(z, tokens, top=top)[4]
+        order = torch.sort(torch.nan_to_num(z.float(), nan=-1e30), dim=-1, descending=True, stable=True).indices
+        left = (~z.isnan()).sum(-1, keepdim=True)
+        want = torch.where(torch.arange(top, device="cuda") < left, order[:, :top], -1)
+        assert torch.equal(ids, want)
+
+
 def test_layouts():
     """Rows further apart, odd addresses, more dimensions, int32 tokens, strided tokens."""
     require_gpu()
