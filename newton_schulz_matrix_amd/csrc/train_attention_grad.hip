@@ -13,8 +13,8 @@
 // the next product's operand.
 //
 // Measured, bf16, 32 heads of 128 that read 8, 16256 tokens of eight sequences of 0 to 5113:
-// dq 700 us, dk and dv 910 (1.12 TFLOP that the gradient cannot do without, 1.57 with S and
-// dout v^T again: 970 TFLOP/s; a library product of 8192 cubed reaches 1180).
+// dq 690 us, dk and dv 890 (1.12 TFLOP that the gradient cannot do without, 1.57 with S and
+// dout v^T again: 990 TFLOP/s; a library product of 8192 cubed reaches 1180).
 //
 // fp16: weights and dS of a long row lie among its subnormals. Weights are taken
 // times 2^14, and dS times a power of two that keeps the largest one possible
