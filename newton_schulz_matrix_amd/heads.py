@@ -86,44 +86,52 @@ def _new_or_heads(t, name: str, dev: int, like):
 
 # ------------------------------------- norm and rotation of queries and keys
 
+_NO_SECTIONS = (_i64 * 4)()
+
+
 def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, sections, interleaved, dev):
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q and k must be (tokens, heads, dim), not {tuple(q.shape)} and {tuple(k.shape)}")
+    tokens, q_heads, dim = q.shape
+    k_tokens, k_heads, k_dim = k.shape
+    if k_tokens != tokens or k_dim != dim:
         raise ValueError(f"q and k must be (tokens, heads, dim) of the same tokens and dim, not "
                          f"{tuple(q.shape)} and {tuple(k.shape)}")
-    tokens, _, dim = q.shape
-    if k.dtype is not q.dtype:
-        _mismatch(k, k.shape, "k", q.dtype)
+    dtype = q.dtype
+    if k.dtype is not dtype:
+        _mismatch(k, k.shape, "k", dtype)
     heads_q, heads_k = _heads_of(q, "q", dev), _heads_of(k, "k", dev)
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight: give both or neither")
-    weight_ptrs, weight_code = (None, None), 0
+    q_ptr = k_ptr = None
+    weight_code = 0
     if q_weight is not None:
-        weight_ptrs = (_dense(q_weight, (dim,), "q_weight", dev),
-                       _dense(k_weight, (dim,), "k_weight", dev, q_weight.dtype))
+        q_ptr = _dense(q_weight, (dim,), "q_weight", dev)
+        k_ptr = _dense(k_weight, (dim,), "k_weight", dev, q_weight.dtype)
         weight_code = _code(q_weight)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be 1-D: one for each pair that turns")
     pairs = inv_freq.shape[0]
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    parts = (_i64 * 4)()
-    if positions.dim() not in (1, 2) or positions.shape[-1] != tokens or axes > 4:
+    place = positions.shape
+    axes = 1 if len(place) == 1 else place[0] if len(place) == 2 else 5
+    if axes > 4 or place[-1] != tokens:
         raise ValueError(f"positions must be (tokens,) or (axes, tokens) with up to 4 axes, not "
-                         f"{tuple(positions.shape)} for {tokens} tokens")
+                         f"{tuple(place)} for {tokens} tokens")
+    parts, ld_positions = _NO_SECTIONS, 0
     if axes > 1:
         if sections is None or len(sections) != axes or sum(sections) != pairs or min(sections) < 0:
             raise ValueError(f"sections must give the pairs of each of the {axes} axes, {pairs} in all")
-        parts[:axes] = list(sections)
+        parts, ld_positions = (_i64 * 4)(*sections), positions.stride(0)
     elif sections is not None and list(sections) != [pairs]:
         raise ValueError(f"sections: one axis has all {pairs} pairs")
     if positions.get_device() != dev:
         _device_tensor(positions, "positions")
-    if positions.stride(-1) != 1 and tokens > 1:
+    if not positions.is_contiguous() and positions.stride(-1) != 1 and tokens > 1:
         raise ValueError("positions: an axis' positions must be contiguous")
-    return _QkNormRopeArgs(heads_q, heads_k, *weight_ptrs, positions.data_ptr(),
-                           _dense(inv_freq, (pairs,), "inv_freq", dev, torch.float32), tokens, q.shape[1],
-                           k.shape[1], dim, 2 * pairs, positions.stride(0) if axes > 1 else 0, axes,
-                           parts, 1 if interleaved else 0, _code(q), weight_code,
-                           _ids_type(positions, "positions"), eps)
+    return _QkNormRopeArgs(heads_q, heads_k, q_ptr, k_ptr, positions.data_ptr(),
+                           _dense(inv_freq, (pairs,), "inv_freq", dev, torch.float32), tokens, q_heads,
+                           k_heads, dim, 2 * pairs, ld_positions, axes, parts, 1 if interleaved else 0,
+                           _code(q), weight_code, _ids_type(positions, "positions"), eps)
 
 
 def ns_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-6,
