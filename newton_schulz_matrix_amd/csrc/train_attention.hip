@@ -310,7 +310,8 @@ int attention_parts(int64_t tokens, int64_t sequences, int64_t heads, int64_t ro
 // done when the others are. 32 sequences of 512, 135 and 134; 40 of 200, 55 and 60. Heads of
 // 64, whose four waves a SIMD hide more: 4096, 600 and 618.
 bool many_queries(const AttnArgs& a) {
-  return a.tokens * a.q_heads >= 9 * CUS * 128 && a.tokens >= 512 * a.sequences;
+  const int64_t tokens = a.tokens;
+  return tokens * a.q_heads >= 9 * CUS * 128 && tokens / 512 >= a.sequences;
 }
 
 hipError_t launch_attention(const AttnArgs& a, int type, int parts, float* sums, float2* known, hipStream_t stream) {
