@@ -6,7 +6,7 @@
 // Bound by the matrix units, at a clock that falls with what is done in each cycle
 // (2.4 GHz at most, 1.9 here): fewer reads of LDS are worth more than a denser order of
 // instructions. A workgroup takes 128 or 256 queries of one head, 32 or 64 a wave, and
-// goes over the keys up to its last query in tiles of 64, with the running maximum and
+// goes over the keys up to its last query in tiles of 64 (or 32), with the running maximum and
 // sum of each row. Products are taken transposed (keys x queries, columns x queries): a
 // lane then holds one query (or two), a row's maximum and sum are its own registers and
 // one exchange, and the weights are the next product's operand as they stand. Keys and
@@ -26,7 +26,6 @@ namespace nsmi {
 namespace {
 
 constexpr int WAVES = 4, THREADS = 64 * WAVES;
-constexpr int KEYS = 64;              // of a tile
 
 // The weights of a row stand against a reference that trails its running maximum
 // by up to 2^LAG: the sums are rescaled only where it falls further behind. For fp16
@@ -55,9 +54,11 @@ __device__ __forceinline__ void clear_rows(const AttnArgs& a, int head, int firs
 // With two GROUPS a wave has 64 queries, so that an operand from LDS serves two
 // products: half the reads, and half the copies of tiles. It takes 32 keys at once then and
 // reads operands AHEAD, in the order written, to stay within 256 registers.
-template <class T, int DP, int SIDES, int GROUPS>
-__global__ __launch_bounds__(THREADS * SIDES, 2) void attention_kernel(AttnArgs a, int tiles, int parts, float* sums,
-                                                                       float2* known_to) {
+//
+// Tiles of 32 KEYS instead of 64 leave registers and LDS for three workgroups a CU instead of two.
+template <class T, int DP, int SIDES, int GROUPS, int KEYS>
+__global__ __launch_bounds__(THREADS * SIDES, KEYS == 32 ? 3 : 2) void attention_kernel(
+    AttnArgs a, int tiles, int parts, float* sums, float2* known_to) {
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32;
   constexpr int SUB = GROUPS == 2 ? 1 : KEYS / 32 / SIDES;   // times 32 keys at once
@@ -314,13 +315,22 @@ bool many_queries(const AttnArgs& a) {
   return tokens * a.q_heads >= 9 * CUS * 128 && tokens / 512 >= a.sequences;
 }
 
+// Whether tiles of 32 keys pay, for heads above 64: at 512 workgroups or more of sequences of less
+// than 512 on average, else at 1024. Us with 64 and 32 (bf16, 32 heads of 128 unless said): 128
+// sequences of 64, 51 and 42; 64 of 128, 49 and 41; 40 of 200, 56 and 49; 16 of 512, 66 and 64;
+// 4096 tokens of one, 156 and 148; 16384 of 8 heads 581 and 563, of 16 heads 1062 and 1075;
+// 4096 of 24 heads, 792 workgroups, 118 and 130.
+bool short_tiles(const AttnArgs& a, int64_t tiles) {
+  return tiles * a.q_heads >= (a.tokens / 512 < a.sequences ? 2 * CUS : 4 * CUS);
+}
+
 hipError_t launch_attention(const AttnArgs& a, int type, int parts, float* sums, float2* known, hipStream_t stream) {
   const int64_t tiles = tiles_of(a.tokens, a.sequences, 32 * WAVES);
-  auto on = [&](auto t, auto dp, auto sides, auto groups) {
+  auto on = [&](auto t, auto dp, auto sides, auto groups, auto keys) {
     using T = decltype(t);
-    constexpr int DP = dp(), SIDES = sides(), GROUPS = groups();
+    constexpr int DP = dp(), SIDES = sides(), GROUPS = groups(), KEYS = keys();
     const int64_t n = tiles_of(a.tokens, a.sequences, 32 * WAVES * GROUPS);
-    hipLaunchKernelGGL((attention_kernel<T, DP, SIDES, GROUPS>), dim3(shared_blocks(n * a.q_heads, parts)),
+    hipLaunchKernelGGL((attention_kernel<T, DP, SIDES, GROUPS, KEYS>), dim3(shared_blocks(n * a.q_heads, parts)),
                        dim3(THREADS * SIDES), 0, stream, a, static_cast<int>(n), parts, sums, known);
     if (parts > 1)
       hipLaunchKernelGGL(attention_join_kernel<T>, dim3((a.tokens * (a.dim / 8) + 255) / 256, a.q_heads), dim3(256),
@@ -329,10 +339,14 @@ hipError_t launch_attention(const AttnArgs& a, int type, int parts, float* sums,
   };
   using One = std::integral_constant<int, 1>;
   using Two = std::integral_constant<int, 2>;
+  using Short = std::integral_constant<int, 32>;
+  using Long = std::integral_constant<int, 64>;
   auto sided = [&](auto t, auto dp) {
-    if constexpr (dp() == 128)
-      if (parts == 1 && many_queries(a)) return on(t, dp, One{}, Two{});
-    return two_sides(tiles * a.q_heads * parts) ? on(t, dp, Two{}, One{}) : on(t, dp, One{}, One{});
+    if constexpr (dp() == 128) {
+      if (parts == 1 && many_queries(a)) return on(t, dp, One{}, Two{}, Long{});
+      if (parts == 1 && short_tiles(a, tiles)) return on(t, dp, One{}, One{}, Short{});
+    }
+    return two_sides(tiles * a.q_heads * parts) ? on(t, dp, Two{}, One{}, Long{}) : on(t, dp, One{}, One{}, Long{});
   };
   auto shaped = [&](auto t) {
     return a.dim <= 64 ? sided(t, std::integral_constant<int, 64>{}) : sided(t, std::integral_constant<int, 128>{});

@@ -120,6 +120,21 @@ def test_many_queries(lengths, rest, dim, dtype):
     check(c, times=times)
 
 
+# From 512 workgroups of short sequences on, or 1024: tiles of 32 keys for heads above 64.
+@pytest.mark.parametrize("lengths, rest, dim, heads", [([130, 1, 0, 64, 200, 33], 0, 128, 52), ([700], 0, 72, 148),
+                                                       ([31, 32, 33, 63, 65, 257], 70, 96, 64),
+                                                       ([1] * 70 + [129, 40], 1, 128, 8), ([640, 389], 5, 120, 96)], ids=str)
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_many_workgroups(lengths, rest, dim, heads, dtype):
+    require_gpu()
+    c = make(11, lengths, 4, 2, dim, dtype, rest=rest)
+    out, lse = check(c, times=heads // 4)
+    n = sum(lengths)
+    assert not out[n:].any() and not lse[:, n:].any()
+    c = make(12, lengths, 4, 2, dim, dtype, peak=30.0)
+    check(c, times=heads // 4)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_rows_behind_the_last_sequence(dtype):
     require_gpu()
