@@ -92,15 +92,17 @@ __device__ __forceinline__ I32x4 descriptor(const void* p, uint32_t bytes) {
 
 // Copies 16 (4) bytes a lane from memory to LDS: lane i's land at `lds` + 16 i (4 i).
 // In inline assembly, so that the only waits for them are copies_done()'s: the
-// compiler would wait for every copy in flight before any LDS read.
+// compiler would wait for every copy in flight before any LDS read. Between writing
+// m0 and the copy that reads it stands one wait state: the hardware does not wait by
+// itself, and the compiler looks for such pairs outside of inline assembly only.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy16(I32x4 from, uint32_t lds, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(lds), "v"(at), "s"(from) : "memory", "m0");
 }
 __device__ __forceinline__ void copy4(I32x4 from, uint32_t lds, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :: "s"(lds), "v"(at), "s"(from) : "memory", "m0");
 }
 #pragma clang diagnostic pop

@@ -104,12 +104,14 @@ __device__ __forceinline__ i32x4 make_rsrc(const void* p, uint32_t bytes) {
 // at LDS byte address lds_addr + 16 i. Written as inline assembly so that
 // the only waits on it are the explicit vmcnt waits of the main loop (the
 // compiler would otherwise wait for every in-flight copy before any LDS
-// read). M0 is not used for anything else in this kernel.
+// read). M0 is not used for anything else in this kernel. Between writing it and
+// the copy that reads it stands one wait state: the hardware does not wait by
+// itself, and the compiler looks for such pairs outside of inline assembly only.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_copy16(i32x4 rsrc, uint32_t lds_addr, uint32_t voff,
                                            uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :: "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff) : "memory", "m0");
 }
 #pragma clang diagnostic pop
