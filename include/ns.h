@@ -568,7 +568,8 @@ ns_status ns_qk_norm_rope_grad(const ns_qk_norm_rope_args* args, ns_heads dq_out
  * whose formulas do not hold it, never another sequence.
  * S, the softmax and all sums are fp32; P and, in the gradient, P and dS are
  * rounded to the tensors' type for the products with v, dout, k and q (fp16: scaled
- * into its range first).
+ * into its range first, dS by a power of two from what lies in its own sequence and
+ * group of heads).
  * The gradient call takes out and lse of the forward call and the gradient of out,
  * and writes
  *   delta[i] = dout[i] . out[i],   dS = P (dout v^T - delta)

@@ -289,7 +289,7 @@ AttnPlan attention_plan(int64_t tokens, int64_t sequences, int64_t q_heads, int6
 }
 struct AttnGradPlan {
   int q_parts, k_parts;
-  size_t delta, peaks, sums, total;   // byte offsets, bytes
+  size_t delta, reach, norms, sums, total;   // byte offsets, bytes
 };
 AttnGradPlan attention_grad_plan(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t k_heads, int64_t dim) {
   AttnGradPlan p;
@@ -297,8 +297,9 @@ AttnGradPlan attention_grad_plan(int64_t tokens, int64_t sequences, int64_t q_he
   p.q_parts = attention_parts(tokens, sequences, q_heads, tokens, true);
   p.k_parts = attention_parts(tokens, sequences, k_heads, tokens * (q_heads / k_heads), false);
   p.delta = rows;
-  p.peaks = 2 * rows;
-  p.sums = p.peaks + align_up(sizeof(float) * 2 * PEAKS);
+  p.reach = 2 * rows;
+  p.norms = 3 * rows;
+  p.sums = p.norms + align_up(sizeof(float) * static_cast<size_t>(tokens) * k_heads);
   const int64_t most = std::max(p.q_parts > 1 ? p.q_parts * q_heads : 0, p.k_parts > 1 ? 2 * p.k_parts * k_heads : 0);
   p.total = p.sums + align_up(sizeof(float) * static_cast<size_t>(most) * tokens * dim);
   return p;
@@ -387,8 +388,9 @@ NS_API ns_status ns_attention_grad(const ns_attention_args* p, ns_heads dout, ns
   a.lse = const_cast<float*>(lse);
   a.lse2 = reinterpret_cast<float*>(w);
   a.delta = reinterpret_cast<float*>(w + plan.delta);
+  a.reach = reinterpret_cast<float*>(w + plan.reach);
+  a.v_norms = reinterpret_cast<float*>(w + plan.norms);
   return from_hip(launch_attention_grad(a, p->dtype, plan.q_parts, plan.k_parts,
-                                        reinterpret_cast<float*>(w + plan.peaks),
                                         reinterpret_cast<float*>(w + plan.sums),
                                         static_cast<hipStream_t>(stream)));
 }

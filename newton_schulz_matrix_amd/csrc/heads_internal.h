@@ -57,6 +57,8 @@ struct AttnArgs {
   float* lse;                  // (q_heads, tokens)
   float* lse2;                 // -lse log2(e) (fp16: + 14), gradient only
   float* delta;                // -delta, (q_heads, tokens), gradient only
+  float* reach;                // what a row's dS may reach, (q_heads, tokens), gradient of fp16 only
+  float* v_norms;              // (k_heads, tokens), gradient of fp16 only
   const int* offsets;          // (sequences + 1)
   int tokens, sequences, q_heads, k_heads, dim;
   bool clear_rest;
@@ -73,9 +75,7 @@ struct AttnArgs {
 int attention_parts(int64_t tokens, int64_t sequences, int64_t heads, int64_t rows, bool keys);
 hipError_t launch_attention(const AttnArgs& a, int type, int parts, float* sums, float2* known, hipStream_t stream);
 
-// Greatest norms of a head's rows in dout and v, in so many workgroups' shares each (fp16 only).
-constexpr int PEAKS = 256;
-hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k_parts, float* peaks, float* sums,
+hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k_parts, float* sums,
                                  hipStream_t stream);
 
 }  // namespace nsmi

@@ -18,8 +18,11 @@
 //
 // fp16: weights and dS of a long row lie among its subnormals. Weights are taken
 // times 2^14, and dS times a power of two that keeps the largest one possible
-// (2 max |dout| max |v|, norms of a head's rows) below 2^15; both are taken back from
-// the sums in fp32.
+// below 2^14; both are taken back from the sums in fp32. What a row's dS may reach is
+// |dout| max |v| + |delta|, over the keys before its tile's end: dq's power of two is
+// the row's own, that of dk the greatest of the rows behind the keys in their sequence
+// and group of heads. No other sequence and no other group of heads has a part in it,
+// and rows that are not finite have none (theirs are NaN whatever they are scaled by).
 #include <algorithm>
 #include <type_traits>
 
@@ -41,62 +44,52 @@ template <>
 constexpr bool NARROW<_Float16> = true;
 constexpr float LIFT = 14.f;
 
-// What dS is multiplied by, for fp16.
-__device__ __forceinline__ float ds_scale(const float* peaks) {
-  const int lane = threadIdx.x & 63;
-  static_assert(PEAKS == 256, "four for each lane");
-  float of[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 x = reinterpret_cast<const float4*>(peaks + i * PEAKS)[lane];
-    of[i] = wave_max(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
-  }
-  const float most = 2.f * of[0] * of[1];
+// What dS is multiplied by, for fp16, if it may reach `most`.
+__device__ __forceinline__ float ds_scale(float most) {
   if (!(most > 0.f && most < INFINITY)) return 1.f;
   int e;
   frexpf(most, &e);
   return ldexpf(1.f, min(max(14 - e, -60), 60));
 }
 
-// fp16: the greatest norms of dout's rows of a head and of v's, one of each for a
-// workgroup, 16 lanes a row. (2064 tokens of 8 heads of 80: 5 us; a maximum in one place for
-// all needs a launch that clears it first.)
-constexpr int NORM_THREADS = 1024, NORM_ROWS = NORM_THREADS / 16;
+// Greatest finite of `lines` times n numbers, `apart` from one line to the next, for all of
+// a workgroup (at least 0).
+template <int WAVES_OF>
+__device__ __forceinline__ float greatest(const float* p, int lines, int64_t apart, int n, float (&tops)[WAVES_OF]) {
+  float top = 0.f;
+  for (int line = 0; line < lines; ++line, p += apart)
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += 64 * WAVES_OF) top = p[i] < INFINITY ? fmaxf(top, p[i]) : top;
+  top = wave_max(top);
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WAVES_OF; ++w) top = fmaxf(top, tops[w]);
+  return top;
+}
+
+// fp16: the norms of v's rows, 16 lanes a row.
+constexpr int NORM_THREADS = 256, NORM_ROWS = NORM_THREADS / 16, NORM_BLOCKS = 2048;
 template <class T>
-__global__ __launch_bounds__(NORM_THREADS) void norms_kernel(AttnArgs a, float* peaks) {
-  __shared__ float tops[2][NORM_THREADS / 64];
+__global__ __launch_bounds__(NORM_THREADS) void norms_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 15;
   const int first = offset_at(a.offsets, 0, a.tokens), last = offset_at(a.offsets, a.sequences, a.tokens);
+  const int64_t rows = static_cast<int64_t>(last - first) * a.k_heads;
+  for (int64_t row = blockIdx.x * NORM_ROWS + threadIdx.x / 16; row - threadIdx.x / 16 < rows;
+       row += static_cast<int64_t>(gridDim.x) * NORM_ROWS) {
+    const int64_t token = first + row / a.k_heads;
+    const int head = static_cast<int>(row % a.k_heads);
+    float norm = 0.f;
+    if (row < rows && 8 * lane < a.dim) {
+      float x[VEC];
+      load8(static_cast<const T*>(a.v.p) + token * a.v.token + head * a.v.head + 8 * lane, x);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const HeadsAt& from = i ? a.v : a.dout;
-    const int heads = i ? a.k_heads : a.q_heads;
-    const int64_t rows = static_cast<int64_t>(last - first) * heads;
-    float top = 0.f;
-    for (int64_t row = blockIdx.x * NORM_ROWS + threadIdx.x / 16; row - threadIdx.x / 16 < rows;
-         row += PEAKS * NORM_ROWS) {
-      float norm = 0.f;
-      if (row < rows && 8 * lane < a.dim) {
-        const int64_t token = row / heads;
-        float x[VEC];
-        load8(static_cast<const T*>(from.p) + (first + token) * from.token + (row - token * heads) * from.head +
-                  8 * lane,
-              x);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) norm = fmaf(x[e], x[e], norm);
-      }
-#pragma unroll
-      for (int off = 8; off >= 1; off >>= 1) norm += __shfl_xor(norm, off, 64);
-      top = fmaxf(top, norm);   // (a NaN is passed over: its rows are NaN anyway)
+      for (int e = 0; e < VEC; ++e) norm = fmaf(x[e], x[e], norm);
     }
-    top = wave_max(top);
-    if ((threadIdx.x & 63) == 0) tops[i][threadIdx.x >> 6] = top;
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) norm += __shfl_xor(norm, off, 64);
+    if (row < rows && lane == 0) a.v_norms[head * static_cast<int64_t>(a.tokens) + token] = sqrtf(norm);
   }
-  __syncthreads();
-  if (threadIdx.x >= 2) return;
-  float top = 0.f;
-  for (int w = 0; w < NORM_THREADS / 64; ++w) top = fmaxf(top, tops[threadIdx.x][w]);
-  peaks[threadIdx.x * PEAKS + blockIdx.x] = sqrtf(top);
 }
 
 // Rows behind the last sequence: zeros.
@@ -114,15 +107,15 @@ __device__ __forceinline__ void clear_rows(const HeadsAt& to, int head, int dim,
 
 // 32 queries a wave. With two SIDES eight waves share 128 queries, each half of every
 // tile's keys, and add up at the end: for launches that leave most of a CU empty. The
-// rows' delta and lse log2(e) are left for the kernel below.
+// rows' delta, lse log2(e) and what their dS may reach are left for the kernel below.
 template <class T, int DP, int SIDES>
-__global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, const float* peaks, int tiles,
-                                                               int parts, float* sums) {
+__global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, int tiles, int parts, float* sums) {
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32;
   constexpr int TILE = STEP * Tile<DP>::ROW;
   __shared__ __attribute__((aligned(1024))) char smem[4 * TILE];   // keys, values, twice
   static_assert(4 * TILE >= ROWS * DP * 4, "the sums of one side fit in the tiles");
+  __shared__ float tops[WAVES * SIDES];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int side = wave / WAVES;
@@ -163,7 +156,7 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
                        a.dim, half, q);
   load_operands<T, DP>(there ? static_cast<const T*>(a.dout.p) + token * a.dout.token + w.head * a.dout.head : nullptr,
                        a.dim, half, g);
-  float dot = 0.f;
+  float dot = 0.f, norm = 0.f;
   {
     V8 o[KC];
     load_operands<T, DP>(there ? static_cast<const T*>(a.out.p) + token * a.out.token + w.head * a.out.head : nullptr,
@@ -171,18 +164,28 @@ __global__ __launch_bounds__(THREADS * SIDES, 2) void dq_kernel(AttnArgs a, cons
 #pragma unroll
     for (int j = 0; j < KC; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dot = fmaf(static_cast<float>(g[j][e]), static_cast<float>(o[j][e]), dot);
+      for (int e = 0; e < 8; ++e) {
+        dot = fmaf(static_cast<float>(g[j][e]), static_cast<float>(o[j][e]), dot);
+        if (NARROW<T>) norm = fmaf(static_cast<float>(g[j][e]), static_cast<float>(g[j][e]), norm);
+      }
   }
   float lower, upper;
   both_halves(dot, lower, upper);
   dot = lower + upper;
+  float scaled = 1.f;   // each lane its query's
+  if constexpr (NARROW<T>) {
+    const float* norms = a.v_norms + kv_head * static_cast<int64_t>(a.tokens) + at.begin;
+    both_halves(norm, lower, upper);
+    norm = fmaf(sqrtf(lower + upper), greatest(norms, 1, 0, keys, tops), fabsf(dot));
+    scaled = ds_scale(norm);
+  }
   const int64_t stat = static_cast<int64_t>(w.head) * a.tokens + token;
   float lse2 = there ? a.lse[stat] * LOG2E : 0.f;
   if (there && half == 0 && side == 0 && part == 0) {
     a.delta[stat] = -dot;
     a.lse2[stat] = (NARROW<T> ? LIFT : 0.f) - lse2;
+    if (NARROW<T>) a.reach[stat] = norm;
   }
-  const float scaled = NARROW<T> ? ds_scale(peaks) : 1.f;
   const float to_ds = NARROW<T> ? scaled * (1.f / 16384.f) : 1.f;
   const float delta = dot * to_ds;
   if (NARROW<T>) lse2 -= LIFT;
@@ -279,8 +282,7 @@ __device__ __forceinline__ float4 read4(const __attribute__((address_space(3))) 
 // queries of the same keys, and leave their sums in fp32 for a kernel that adds
 // them up in order.
 template <class T, int DP>
-__global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const float* peaks, int tiles,
-                                                            int parts, float* sums) {
+__global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, int tiles, int parts, float* sums) {
   typedef typename Eight<T>::type V8;
   constexpr int KC = DP / 16, DT = DP / 32;
   constexpr int TILE = KV_STEP * Tile<DP>::ROW, STATS = 2 * KV_STEP * 4, STAGE = 2 * TILE + STATS;
@@ -289,6 +291,7 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const fl
   constexpr int KR = std::min(KC, KEY_CHUNKS), KL = KC - KR;   // key chunks in registers, in LDS
   // queries, dout, lse, delta, twice, and the keys' second half
   __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE + (KL ? ROWS * Tile<64>::ROW : 0)];
+  __shared__ float tops[KV_WAVES];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int side = wave / 4;           // of a tile's queries
@@ -347,7 +350,9 @@ __global__ __launch_bounds__(KV_THREADS, 2) void dkv_kernel(AttnArgs a, const fl
                             min(a.dim, 16 * KR), half, k);
   load_operands<T, DP>(there ? static_cast<const T*>(a.v.p) + token * a.v.token + w.head * a.v.head : nullptr,
                        a.dim, half, v);
-  const float scaled = NARROW<T> ? ds_scale(peaks) : 1.f;
+  float scaled = 1.f;
+  if constexpr (NARROW<T>)
+    scaled = ds_scale(greatest(a.reach + stat0 + at.row, group, a.tokens, at.length - at.row, tops));
   const float to_ds = NARROW<T> ? scaled * (1.f / 16384.f) : 1.f;
   const RowReader<DP> rows(lane);
   const auto k_rows = RowReader<64>(lane).in(lds + 2 * STAGE + 32 * (wave & 3) * Tile<64>::ROW);
@@ -492,14 +497,16 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, HeadsAt first, He
 
 }  // namespace
 
-hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k_parts, float* peaks, float* sums,
+hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k_parts, float* sums,
                                  hipStream_t stream) {
   const int64_t tiles = tiles_of(a.tokens, a.sequences, ROWS);
   auto on = [&](auto t, auto dp) {
     using T = decltype(t);
     constexpr int DP = dp();
     if constexpr (NARROW<T>) {
-      hipLaunchKernelGGL(norms_kernel<T>, dim3(PEAKS), dim3(NORM_THREADS), 0, stream, a, peaks);
+      const int64_t rows = static_cast<int64_t>(a.tokens) * a.k_heads;
+      hipLaunchKernelGGL(norms_kernel<T>, dim3(std::min<int64_t>((rows + NORM_ROWS - 1) / NORM_ROWS, NORM_BLOCKS)),
+                         dim3(NORM_THREADS), 0, stream, a);
     }
     auto join = [&](int tensors, const HeadsAt& first, const HeadsAt& second, int heads, int parts) {
       if (parts > 1)
@@ -509,13 +516,13 @@ hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k
     auto queries = [&](auto sides) {
       constexpr int SIDES = sides();
       hipLaunchKernelGGL((dq_kernel<T, DP, SIDES>), dim3(shared_blocks(tiles * a.q_heads, q_parts)),
-                         dim3(THREADS * SIDES), 0, stream, a, peaks, static_cast<int>(tiles), q_parts, sums);
+                         dim3(THREADS * SIDES), 0, stream, a, static_cast<int>(tiles), q_parts, sums);
     };
     if (two_sides(tiles * a.q_heads * q_parts)) queries(std::integral_constant<int, 2>{});
     else queries(std::integral_constant<int, 1>{});
     join(1, a.dq, a.dq, a.q_heads, q_parts);
     hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(shared_blocks(tiles * a.k_heads, k_parts)),
-                       dim3(KV_THREADS), 0, stream, a, peaks, static_cast<int>(tiles), k_parts, sums);
+                       dim3(KV_THREADS), 0, stream, a, static_cast<int>(tiles), k_parts, sums);
     join(2, a.dk, a.dv, a.k_heads, k_parts);
     return hipGetLastError();
   };
