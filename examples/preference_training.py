@@ -163,8 +163,9 @@ def train(steps=20, beta=0.1, model=None):
     model = model or Model()
     ids, labels = batch()
     pairs = ids.shape[0] // 2
-    # the reference is the model as it starts: log probabilities of the labels that count
-    reference = nsmi.ns_token_logps(model.forward(ids)[0], labels)[0].sum(-1)
+    # the reference is the model as it starts: log probabilities of the labels that count, added up
+    # in 64 bits like the policy's, from which they are subtracted
+    reference = nsmi.ns_token_logps(model.forward(ids)[0], labels)[0].double().sum(-1).float()
     weights = torch.full((pairs,), 1.0 / pairs, device="cuda")
     history = []
     for _ in range(steps):

@@ -145,6 +145,30 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
+constexpr float FAR = 150.f;   // exp(-FAR) is 0 in fp32
+
+// exp(x) by the hardware's 2^x, without the rounding of the product
+// p = x log2(e): exp(x) = 2^p exp(x - p ln 2), where the second factor is 1 + c. That
+// rounding is up to |x| half steps of the result. bf16 logits take few
+// values, so the roundings of p do not average out over a row: left alone they
+// put 2e-8 on its sum, much the same for every row, which the difference of
+// two sequences' sums keeps. x is not below -FAR.
+__device__ __forceinline__ float exp_exact(float x) {
+  const float p = x * 1.442695041f;
+  const float c = fmaf(p, 1.904654299e-9f, fmaf(-p, 0.693147182f, x));
+  const float t = __builtin_amdgcn_exp2f(p);
+  return fmaf(t, c, t);
+}
+// The same with ln 2 in one fp32 number, which is 1.9e-9 above it: a power of
+// e^(1 - OF_E), so that sums of such powers are brought from one reference to another by
+// them, and sum exp x is sum e^((1 - OF_E) x) plus OF_E times the sum of those terms times x.
+constexpr double OF_E = 1.904654299e-9 * 1.442695041;
+__device__ __forceinline__ float exp_near(float x) {
+  const float p = x * 1.442695041f;
+  const float t = __builtin_amdgcn_exp2f(p);
+  return fmaf(t, fmaf(-p, 0.693147182f, x), t);
+}
+
 // One of three element types chosen at run time: the switch goes once around
 // a whole kernel launch, on the host.
 template <class F>

@@ -32,20 +32,6 @@ namespace {
 constexpr int UNROLL = 8;                           // vectors of a thread in flight
 constexpr int SHORT_VOCAB = 64 * VEC * UNROLL / 2;
 constexpr int step_of(int threads) { return threads * VEC * UNROLL; }   // elements of a step
-constexpr float FAR = 150.f;                        // exp(-FAR) is 0 in fp32
-
-// exp(x) by the hardware's 2^x, without the rounding of the product
-// p = x log2(e): exp(x) = 2^p exp(x - p ln 2), where the second factor is 1 + c. That
-// rounding is up to |x| half steps of the result. bf16 logits take few
-// values, so the roundings of p do not average out over a row: left alone they
-// put 2e-8 on its sum, much the same for every row, which the difference of
-// two sequences' sums keeps. x is not below -FAR.
-__device__ __forceinline__ float exp_exact(float x) {
-  const float p = x * 1.442695041f;
-  const float c = fmaf(p, 1.904654299e-9f, fmaf(-p, 0.693147182f, x));
-  const float t = __builtin_amdgcn_exp2f(p);
-  return fmaf(t, c, t);
-}
 
 // The exponent's base for a maximum m: exp(z - m) for m = -inf (no terms yet,
 // or none but masked ones) is taken against 0 instead, which gives 0.
