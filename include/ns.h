@@ -577,13 +577,16 @@ ns_status ns_qk_norm_rope_grad(const ns_qk_norm_rope_args* args, ns_heads dq_out
  * (dk and dv summed over the heads of a group). Nothing depends on the order in
  * which the device runs: results are reproducible.
  * 0 <= tokens <= NS_MAX_ROWS (0 is a no-op), 0 <= sequences <= NS_MAX_ROWS, 1 <= k_heads,
- * q_heads a multiple of it up to NS_MAX_HEADS, dim a multiple of 8 up to 128; scale finite
- * and > 0. All tensors 16-byte aligned with strides that are multiples of 8; a
- * tensor's ld_token >= dim (also of one that is only read) and at most 2^23. Workspaces:
+ * q_heads a multiple of it up to NS_MAX_HEADS, and with tokens
+ * (tokens / 128 + sequences + 1) * q_heads <= NS_MAX_HEAD_TILES (rounded down: 32 heads,
+ * 130055 sequences of a token each); dim a multiple of 8 up to 128; scale finite and > 0.
+ * All tensors 16-byte aligned with strides that are multiples of 8; a tensor's ld_token >= dim
+ * (also of one that is only read) and at most 2^23. Workspaces:
  * ns_attention_workspace_size and ns_attention_grad_workspace_size bytes, 256-byte
  * aligned (NULL where the size is 0). They hold the sums of up to 8 parts where few
  * tiles of 128 rows are cut into them: how a row's sum is ordered depends on the
  * sizes of the call. */
+#define NS_MAX_HEAD_TILES (1 << 22)
 typedef struct {
   ns_heads q, k, v;
   const int32_t* offsets;

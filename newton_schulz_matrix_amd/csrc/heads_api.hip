@@ -244,8 +244,11 @@ HeadsAt place(const ns_heads& h, const View& v) {
   return {h.data, v.tokens <= 1 ? v.dim : v.ld_token, v.heads <= 1 ? 0 : v.ld_head};
 }
 bool attention_sizes_ok(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t k_heads, int64_t dim) {
-  return rows_ok(tokens) && rows_ok(sequences) && q_heads >= 1 && q_heads <= NS_MAX_HEADS && k_heads >= 1 &&
-         k_heads <= q_heads && q_heads % k_heads == 0 && dim >= 8 && dim <= ATTN_MAX_DIM && dim % 8 == 0;
+  if (!rows_ok(tokens) || !rows_ok(sequences) || q_heads < 1 || q_heads > NS_MAX_HEADS || k_heads < 1 ||
+      k_heads > q_heads || q_heads % k_heads != 0 || dim < 8 || dim > ATTN_MAX_DIM || dim % 8 != 0)
+    return false;
+  // a launch's workgroups, of which each has 128 rows of a head at most
+  return tokens == 0 || (tokens / 128 + sequences + 1) * q_heads <= NS_MAX_HEAD_TILES;
 }
 struct AttnViews {
   View q, k, v;
@@ -271,8 +274,6 @@ ns_status check_attention(const ns_attention_args* p, AttnArgs* a, AttnViews* in
   a->dim = static_cast<int>(p->dim);
   a->clear_rest = p->clear_rest != 0;
   a->scale = p->scale;
-  // a launch's workgroups, of which each has 128 rows of a head at most
-  if ((p->tokens / 128 + p->sequences + 1) * p->q_heads > (int64_t{1} << 31) / 512) return NS_ERR_INVALID_ARG;
   return NS_OK;
 }
 struct AttnPlan {

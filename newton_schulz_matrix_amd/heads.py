@@ -19,6 +19,7 @@ from .operators import (_code, _dense, _device_of, _f32, _given_or_new, _i64, _i
                         _size, _sized, _stream_of, _vp, torch)
 
 NS_MAX_HEADS = 1024
+NS_MAX_HEAD_TILES = 1 << 22
 
 
 class _Heads(ctypes.Structure):
@@ -212,7 +213,8 @@ def ns_attention(q, k, v, offsets, scale: Optional[float] = None, out=None, work
     """Causal attention of packed sequences: q (tokens, q_heads, dim), k and v
     (tokens, k_heads, dim) in bf16 or fp16, q_heads a multiple of k_heads, dim a
     multiple of 8 up to 128; offsets (sequences + 1) int32 on the device, where
-    each sequence begins and the last one ends (offsets[0] is 0). scale is
+    each sequence begins and the last one ends (offsets[0] is 0);
+    (tokens // 128 + sequences + 1) * q_heads up to NS_MAX_HEAD_TILES. scale is
     dim ** -0.5 by default. Returns (out, lse): out like q, and the log sum of
     exponentials of each row, (q_heads, tokens) fp32, for the gradient. Rows
     behind the last sequence are zeros in a new out, and left as they are in one
@@ -257,6 +259,6 @@ def ns_attention_grad(dout, q, k, v, out, lse, offsets, scale: Optional[float] =
     return dq, dk, dv
 
 
-__all__ = ["NS_MAX_HEADS", "ns_qk_norm_rope", "ns_qk_norm_rope_grad",
+__all__ = ["NS_MAX_HEADS", "NS_MAX_HEAD_TILES", "ns_qk_norm_rope", "ns_qk_norm_rope_grad",
            "ns_qk_norm_rope_grad_workspace_size", "ns_attention", "ns_attention_workspace_size",
            "ns_attention_grad", "ns_attention_grad_workspace_size"]
