@@ -430,9 +430,15 @@ __device__ __forceinline__ void store_sums(float* row, int dim, int half, const 
 }
 
 // Whether workgroups of eight waves share the keys of 128 queries: where there is no
-// more than one for a CU (2064 fp16 tokens of 6 heads: dq 33 us with four waves, 26 with
-// eight; one tile of keys, 23 tokens of 32 heads, has nothing to share: 5.5 and 6.4).
-inline bool two_sides(int64_t workgroups) { return workgroups <= CUS; }
+// more than one for a CU, and sequences are longer than 384 on average. Us with four waves and
+// with eight, forward and whole gradient, one sequence: bf16, 32 heads of 128, 23 tokens 5.1
+// and 6.1 (18.1, 19.1), 128 7.0 and 8.6 (30.6, 33.2), 256 9.6 and 10.8 (40.0, 41.6), 384 12.1 and
+// 12.9 (46.5, 46.8), 512 14.7 and 15.3 (54.3, 53.2); 8 heads, 384 11.5 and 12.2 (42.3, 42.3), 900
+// 21.1 and 20.3 (63.2, 58.2); fp16, 6 heads of 80, 256 8.7 and 9.0 (40.3, 39.6), 512 13.3 and 12.8
+// (45.7, 42.7), 900 20.9 and 18.8 (61.5, 54.8).
+inline bool two_sides(int64_t workgroups, int64_t tokens, int64_t sequences) {
+  return workgroups <= CUS && tokens > 384 * sequences;
+}
 
 // Which head and tile a workgroup takes. Workgroups go to the eight XCDs in turn,
 // each with an L2 of its own: heads that read the same keys and values go to one

@@ -346,7 +346,8 @@ hipError_t launch_attention(const AttnArgs& a, int type, int parts, float* sums,
       if (parts == 1 && many_queries(a)) return on(t, dp, One{}, Two{}, Long{});
       if (parts == 1 && short_tiles(a, tiles)) return on(t, dp, One{}, One{}, Short{});
     }
-    return two_sides(tiles * a.q_heads * parts) ? on(t, dp, Two{}, One{}, Long{}) : on(t, dp, One{}, One{}, Long{});
+    return two_sides(tiles * a.q_heads * parts, a.tokens, a.sequences) ? on(t, dp, Two{}, One{}, Long{})
+                                                                       : on(t, dp, One{}, One{}, Long{});
   };
   auto shaped = [&](auto t) {
     return a.dim <= 64 ? sided(t, std::integral_constant<int, 64>{}) : sided(t, std::integral_constant<int, 128>{});

@@ -518,7 +518,7 @@ hipError_t launch_attention_grad(const AttnArgs& a, int type, int q_parts, int k
       hipLaunchKernelGGL((dq_kernel<T, DP, SIDES>), dim3(shared_blocks(tiles * a.q_heads, q_parts)),
                          dim3(THREADS * SIDES), 0, stream, a, static_cast<int>(tiles), q_parts, sums);
     };
-    if (two_sides(tiles * a.q_heads * q_parts)) queries(std::integral_constant<int, 2>{});
+    if (two_sides(tiles * a.q_heads * q_parts, a.tokens, a.sequences)) queries(std::integral_constant<int, 2>{});
     else queries(std::integral_constant<int, 1>{});
     join(1, a.dq, a.dq, a.q_heads, q_parts);
     hipLaunchKernelGGL((dkv_kernel<T, DP>), dim3(shared_blocks(tiles * a.k_heads, k_parts)),
