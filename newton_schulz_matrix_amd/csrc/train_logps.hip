@@ -30,9 +30,12 @@ namespace {
 constexpr int UNROLL = 8;                           // vectors of a thread in flight
 constexpr int SHORT_VOCAB = 64 * VEC * UNROLL / 2;  // rows up to this long are one wave's
 // Many rows are one wave's up to longer ones: nothing is brought together between waves
-// then (bf16, us with one wave and with four: 16000 rows of 4096, top 5, 42 and 134; 8192 of
-// 50021 187 and 217; 16384 of 70000 422 and 485, 4100 of 100000 183 and 170; without top 8000 of
-// 12000 42 and 51, 12000 of 21273 114 and 109). Few rows are done sooner by four.
+// then (bf16, us with one wave and with four: 16000 rows of 4096, top 5, 45 and 121; 4096 of
+// 40000 76 and 88; 8192 of 50021 194 and 223; without top 4096 of 12000 26 and 28, 12000 of 21273
+// 119 and 120, 4096 of 128000 201 and 194). Few rows are done sooner by four. With alternatives
+// one wave is 4 to 15% faster on longer rows too (4096 of 128000, top 5, 209 and 219; 16384 of
+// 70000 442 and 517), but 60% slower where they rise throughout (4096 of 128000 765 and 473):
+// four from there on.
 constexpr int MANY_ROWS = 4096, MANY_VOCAB = 1 << 14, MANY_VOCAB_TOP = 1 << 16;
 constexpr int one_wave_vocab(int rows, int top) {
   return rows < MANY_ROWS ? SHORT_VOCAB : top > 0 ? MANY_VOCAB_TOP : MANY_VOCAB;
@@ -73,16 +76,26 @@ __device__ __forceinline__ void widen(const Raw<__bf16>& raw, float (&v)[VEC]) {
 
 // Sums of a thread against a reference m, which is at most LAG below its
 // greatest entry: x is at most LAG, and the entropy's two terms do not cancel.
+// s and t are those of a step's terms, which go to all_s and all_t at its end: beside the sum of
+// a thousand terms the small ones would be lost, in every row alike (rows of 65536, standard
+// deviation 4, lse too low by 21 half steps of 1, by 1 so; it costs 1%).
 constexpr float LAG = 1.f;
 struct Sums {
-  float m, s, t;
+  float m = -INFINITY, s = 0.f, t = 0.f, all_s = 0.f, all_t = 0.f;
 };
+__device__ __forceinline__ void end_step(Sums& r) {
+  r.all_s += r.s;
+  r.all_t += r.t;
+  r.s = r.t = 0.f;
+}
 // Brings the sums to another reference.
 __device__ __forceinline__ void rebase(Sums& r, float m) {
-  const float d = base_of(r.m) - base_of(m);   // (r.m = -inf: both sums are 0)
+  const float d = base_of(r.m) - base_of(m);   // (r.m = -inf: all sums are 0)
   const float f = r.m == -INFINITY || d < -FAR ? 0.f : exp_near(d);
   r.t = f == 0.f ? 0.f : f * fmaf(r.s, d, r.t);
+  r.all_t = f == 0.f ? 0.f : f * fmaf(r.all_s, d, r.all_t);
   r.s *= f;
+  r.all_s *= f;
   r.m = m;
 }
 // Takes in one vector, whose greatest entry is `high`.
@@ -330,7 +343,7 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
   const float token_logit = static_cast<float>(z[token]);
   Candidates& mine = found[TOP ? wave : 0];
   if (TOP && threadIdx.x == 0) lasts = 0;
-  Sums r = {-INFINITY, 0.f, 0.f};
+  Sums r;
   Choice w = {LOWEST, -INFINITY, -INFINITY, -INFINITY, 0};
   for (int base = begin; base < end; base += STEP) {
     float high[UNROLL];
@@ -351,6 +364,7 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
       high[j] = highest(v);
       if (j < there) take(v, high[j], r);
     }
+    end_step(r);
     if constexpr (TOP) offer<THREADS>(raw, high, base + col0, end, a.top, mine, w);
   }
   if constexpr (TOP) {
@@ -365,7 +379,7 @@ __global__ __launch_bounds__(THREADS) void logps_kernel(LogpsArgs a, PrefSplit s
 #pragma unroll
   for (int u = 1; u < WAVES; ++u) m = fmaxf(m, red_m[u]);
   rebase(r, m);
-  const double ws = wave_sum64(static_cast<double>(r.s)), wt = wave_sum64(static_cast<double>(r.t));
+  const double ws = wave_sum64(static_cast<double>(r.all_s)), wt = wave_sum64(static_cast<double>(r.all_t));
   if (lane == 0) {
     red_s[wave] = ws;
     red_t[wave] = wt;

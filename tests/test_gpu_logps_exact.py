@@ -110,3 +110,20 @@ def test_reference_of_the_example_adds_up_like_the_policy():
     assert ref.dtype == torch.float32
     tokens = nsmi.ns_token_logps(logits, labels)[0].double().cpu().numpy()
     assert np.array_equal(ref.cpu().numpy(), tokens.sum(-1).astype(np.float32))
+
+
+@pytest.mark.parametrize("rows, vocab", [(4096, 65536), (4096, 16384), (600, 65536)])
+@pytest.mark.parametrize("dtype", [BF, SF])
+def test_small_entries_are_not_lost_beside_long_sums(rows, vocab, dtype):
+    """Rows whose small entries are many and far below the largest: a thread's sum of a
+    thousand of them in fp32 drops what lies below half a step of it, always to one side. Sums of
+    64 terms in fp32 lose 1 half step so at this spread, of 256 5, of 1024 20 (a model of the
+    additions on the CPU, 65536 entries); those of 64 are allowed for, three times."""
+    require_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    logits = torch.randn((rows, vocab), generator=gen, device="cuda").mul_(4.0).to(dtype)
+    lse = nsmi.ns_token_logps(logits, torch.zeros(rows, dtype=torch.int64, device="cuda"), top=5)[1].double()
+    off = torch.cat([lse[a:a + 256] - torch.logsumexp(logits[a:a + 256].double(), -1) for a in range(0, rows, 256)])
+    off = off.cpu().numpy()
+    row = 2.0 ** -20 / math.sqrt(3)   # lse of 16 to 32
+    assert abs(off.mean()) < 6 * row / math.sqrt(rows) + 3 * U32, (off.mean() / U32, off.std() / U32)
