@@ -16,9 +16,9 @@
 // it knows a threshold that `top` entries reach. Few rows are cut into pieces
 // of which a second kernel makes one. Rows begin at any element.
 //
-// Measured, bf16: 4096 rows of 128000, a fifth of them not counted, 5 alternatives, 168 us (0.84
-// GB read: 5.0 TB/s, the rate of a library copy); its gradient with entropy 331 (1.89 GB: 5.7); 8 rows
-// of 50021 with 20 alternatives 11 + 5, the latency of the two kernels.
+// Measured, bf16: 4096 rows of 128000, a fifth of them not counted, 5 alternatives, 185 us (0.84
+// GB read: 4.5 TB/s); its gradient with entropy 338 (1.89 GB: 5.6); 8 rows
+// of 50021 with 20 alternatives 12 + 5, the latency of the two kernels.
 #include <algorithm>
 
 #include "train_device.h"
